@@ -79,6 +79,9 @@ enum exl3_status {
 #define EXL3_MAX_TOPK 32
 #define EXL3_MAX_STAGES 8
 #define EXL3_MAX_FEATURES 65536
+#define EXL3_MAX_ADAPTERS 1024
+#define EXL3_MAX_RANK 128
+#define EXL3_LORA_MAX_ROWS (1 << 26)
 
 int32_t exl3_abi_version(void);
 /* Static string for a status code (host; never NULL). */
@@ -161,8 +164,10 @@ typedef struct exl3_route_meta {
 enum exl3_kernel_id {
   EXL3_K_PACK = 1, EXL3_K_ROTATE = 2, EXL3_K_GATEUP = 3, EXL3_K_DOWN = 4,
   EXL3_K_COMBINE = 5, EXL3_K_LINEAR = 6, EXL3_K_DECODE = 7,
-  EXL3_K_EXPERTS = 8 /* 128-row tiles: gate/up and down of a single pass in one launch, or one
-                        launch of the passes pipelined across launches */
+  EXL3_K_EXPERTS = 8, /* 128-row tiles: gate/up and down of a single pass in one launch, or one
+                         launch of the passes pipelined across launches */
+  EXL3_K_ROUTE = 9, EXL3_K_BALANCE = 10, EXL3_K_BALANCE_SUM = 11, EXL3_K_ROUTE_BACKWARD = 12,
+  EXL3_K_LORA_A = 13, EXL3_K_LORA_B = 14
 };
 typedef struct exl3_profile {
   void **events;        /* host: 2 * cap event handles (hipEvent_t) */
@@ -311,6 +316,128 @@ typedef struct exl3_moe_layout_t {
 int32_t exl3_moe_layout(int32_t rows, int32_t topk, int32_t num_experts,
                         int32_t hidden, int32_t intermediate, int32_t capacity,
                         exl3_moe_layout_t *layout /* host */);
+
+/*
+ * Router: logits -> route IDs and weights for exl3_route_pack /
+ * exl3_moe_forward, the balance loss of that routing, and the gradient of
+ * both with respect to the logits.
+ *
+ * logits: [rows][num_experts] fp16, bf16 or fp32, consecutive rows ld_logits
+ * elements apart (>= num_experts); natural alignment of the element type.
+ * A logit of -inf or NaN takes its expert out of that row (never chosen,
+ * probability and gradient 0); +inf counts as the largest finite fp32. With
+ *   t_e = exp(l_e) (EXL3_SOFTMAX) or 1 / (1 + exp(-l_e)) (EXL3_SIGMOID),
+ * a row's scores are the logits, or with a bias (sigmoid only) t_e + bias_e,
+ * computed in fp64. The topk best scores are taken in descending order, ties
+ * to the lower expert; a score of -inf or NaN is never taken. Weights (the
+ * bias takes no part in them), computed in fp32 and rounded once:
+ *   renorm != 0   w_j = scale * t_j / (sum of t over the row's chosen experts)
+ *   renorm == 0   w_j = scale * t_j / (sum of t over all experts)  softmax
+ *                 w_j = scale * t_j                                sigmoid
+ */
+enum exl3_scoring { EXL3_SOFTMAX = 0, EXL3_SIGMOID = 1 };
+typedef struct exl3_router {
+  int32_t num_experts; /* 1 .. EXL3_MAX_EXPERTS */
+  int32_t topk;        /* 1 .. min(EXL3_MAX_TOPK, num_experts) */
+  int32_t scoring;     /* exl3_scoring */
+  int32_t renorm;
+  float scale;         /* finite */
+  const float *bias;   /* device [num_experts], or NULL; EXL3_SIGMOID only,
+                          read by exl3_route_topk alone */
+} exl3_router;
+
+/*
+ * ids: [rows][topk] EXL3_I32 or EXL3_I64; w: [rows][topk] fp16, bf16 or fp32.
+ * row_mask: NULL, or device uint8 [rows]; a row whose entry is 0 (padding)
+ * gets ID -1 and weight 0 throughout, as do the entries of a row that has
+ * fewer than topk experts left: the pack drops and counts those pairs.
+ */
+int32_t exl3_route_topk(const exl3_router *router, const void *logits, int32_t logits_dtype,
+                        int64_t ld_logits, int32_t rows, const uint8_t *row_mask, void *ids,
+                        int32_t ids_dtype, void *w, int32_t w_dtype, void *stream,
+                        exl3_profile *prof);
+
+/*
+ * Balance loss and per-expert counts. ids: [rows][topk] as routed; IDs outside
+ * [0, num_experts) are left out. A row takes part iff one of its IDs is left;
+ * T rows do. With p_te = t_te / (sum of t over the row):
+ *   count_e = number of IDs equal to e       prob_e = (sum over rows of p_te) / T
+ *   loss = coef * num_experts * sum_e (count_e / (T topk)) * prob_e
+ * (T == 0: loss and prob are 0). The router's renorm, scale and bias take no
+ * part. Sums run in fp32 in a fixed order: the same call gives the same bytes.
+ * ws: exl3_balance_workspace_size(rows, num_experts) bytes, 16-byte aligned;
+ * calls that share it must be ordered on one stream.
+ * rows == 0 enqueues the zero results.
+ */
+typedef struct exl3_balance {
+  int32_t *count;  /* device [num_experts] */
+  int32_t *tokens; /* device [1]: T */
+  float *prob;     /* device [num_experts] */
+  float *loss;     /* device [1] */
+} exl3_balance;
+size_t exl3_balance_workspace_size(int32_t rows, int32_t num_experts);
+int32_t exl3_balance_loss(const exl3_router *router, const void *logits, int32_t logits_dtype,
+                          int64_t ld_logits, int32_t rows, const void *ids, int32_t ids_dtype,
+                          float coef, const exl3_balance *balance, void *ws, size_t ws_bytes,
+                          void *stream, exl3_profile *prof);
+
+/*
+ * Gradient with respect to the logits, of the weights (dw: [rows][topk] fp16,
+ * bf16 or fp32, the gradient of w; NULL: none), of the balance loss (balance
+ * with its count and tokens as exl3_balance_loss wrote them, prob and loss not
+ * read; dloss: device fp32 [1], the gradient of loss, NULL = 1; balance NULL:
+ * none), or of both in one pass. ids name the chosen experts (those outside
+ * [0, num_experts) are left out; an expert named twice in a row gets the sum).
+ * Counts and the choice of experts are held constant. dlogits:
+ * [rows][num_experts] fp16, bf16 or fp32, ld_dlogits elements apart, every
+ * element written, computed in fp32 and rounded once; it must not overlap
+ * logits unless it is the same array with the same dtype and row distance.
+ */
+int32_t exl3_route_backward(const exl3_router *router, const void *logits, int32_t logits_dtype,
+                            int64_t ld_logits, int32_t rows, const void *ids, int32_t ids_dtype,
+                            const void *dw, int32_t dw_dtype, const exl3_balance *balance,
+                            float coef, const float *dloss, void *dlogits,
+                            int32_t dlogits_dtype, int64_t ld_dlogits, void *stream,
+                            exl3_profile *prof);
+
+/*
+ * Low-rank adapters of many requests at once, beside a projection they share
+ * (exl3_linear, or any other whose output is at hand). Row t names its
+ * adapter by ids[t]:
+ *   out_t = base_t + scale_a * (x_t A_a^T) B_a^T      a = ids[t]
+ * and a row whose ID lies outside [0, num_adapters) keeps base_t. x, A and B
+ * share one dtype (fp16 or bf16); the inner product x A^T and all sums are
+ * kept to fp32 accuracy and the output is rounded once. A row's output bytes
+ * do not depend on the other rows, their number or their order.
+ */
+typedef struct exl3_lora_adapters {
+  int32_t in_features;  /* K: multiple of 8, at most EXL3_MAX_FEATURES */
+  int32_t out_features; /* N: multiple of 8, at most EXL3_MAX_FEATURES */
+  int32_t rank;         /* R: 1 .. EXL3_MAX_RANK */
+  int32_t num_adapters; /* 1 .. EXL3_MAX_ADAPTERS */
+  const uint16_t *a;    /* device [num_adapters][R][K], 16-byte aligned */
+  const uint16_t *b;    /* device [num_adapters][N][R], 16-byte aligned */
+  const float *scale;   /* device [num_adapters], or NULL (all 1) */
+  const int32_t *ranks; /* device [num_adapters], or NULL (all R): adapter i
+                           uses the first ranks[i] of its R rows and columns
+                           (clamped to [0, R]); the rest is not used */
+} exl3_lora_adapters;
+/*
+ * rows: at most EXL3_LORA_MAX_ROWS. x: [rows][K], rows ld_x elements apart. ids: [rows] EXL3_I32 or EXL3_I64.
+ * base: [rows][N] fp16, bf16 or fp32, ld_base apart, or NULL (zeros); out:
+ * [rows][N] fp16, bf16 or fp32, ld_out apart. x, base, out: 16-byte aligned,
+ * their row distances at least a row and a multiple of 16 bytes. out may be
+ * base itself (same dtype and row distance), otherwise it overlaps no input.
+ * ws: exl3_lora_workspace_size(rows, in_features, rank) bytes, 16-byte
+ * aligned (the inner products); calls that share it must be ordered on one
+ * stream.
+ */
+size_t exl3_lora_workspace_size(int32_t rows, int32_t in_features, int32_t rank);
+int32_t exl3_lora(const exl3_lora_adapters *adapters, const uint16_t *x, int32_t x_dtype,
+                  int64_t ld_x, int32_t rows, const void *ids, int32_t ids_dtype,
+                  const void *base, int32_t base_dtype, int64_t ld_base, void *out,
+                  int32_t out_dtype, int64_t ld_out, void *ws, size_t ws_bytes, void *stream,
+                  exl3_profile *prof);
 
 /*
  * Diagnostic: decode `ntiles` consecutive trellis tiles of width K with the

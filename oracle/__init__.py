@@ -25,6 +25,8 @@ Modules:
   linear    one EXL3 projection with additive stages (pure / R modes)
   route     route histogram, exclusive scan, stable pack
   moe       routed-experts layer (gate/up, SwiGLU, down, top-k combine)
+  router    top-k router, balance loss and their gradient (own definitions)
+  lora      low-rank adapters beside a shared projection (own definition)
   brute     dense dequantise-then-matmul brute force for tiny shapes
 
 Every function here is pinned by ``tests/test_oracle_*.py`` (``-m "not gpu"``)
@@ -32,4 +34,4 @@ against closed forms, library routines, brute force or the format's printed
 test vectors; none is "parity unpinned".
 """
 
-from . import trellis, hadamard, linear, route, moe, brute  # noqa: F401
+from . import trellis, hadamard, linear, route, moe, router, lora, brute  # noqa: F401

@@ -7,6 +7,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 #include <mutex>
@@ -47,6 +48,12 @@ bool aligned_to(const void *p, unsigned a) { return ((uintptr_t)p & (a - 1)) == 
 // natural alignment is enough.
 unsigned ids_align(int32_t t) { return t == EXL3_I64 ? 8u : 4u; }
 unsigned w_align(int32_t t) { return t == EXL3_F32 ? 4u : 2u; }
+
+bool ids_dtype_ok(int32_t t) { return t == EXL3_I32 || t == EXL3_I64; }
+bool float_dtype_ok(int32_t t) { return t == EXL3_F16 || t == EXL3_BF16 || t == EXL3_F32; }
+size_t float_size(int32_t t) { return t == EXL3_F32 ? 4 : 2; }
+// Row distances are bounded so that no element index overflows 64 bits.
+constexpr int64_t kMaxLd = (int64_t)1 << 32;
 
 // Device residency: the pointer must be device (or managed) memory of the
 // current device. Called only after every host-side check passed.
@@ -479,8 +486,10 @@ const char *exl3_status_string(int32_t s) {
     case EXL3_OK: return "ok";
     case EXL3_E_NULL: return "null pointer";
     case EXL3_E_DTYPE: return "unsupported dtype";
-    case EXL3_E_SHAPE: return "bad or inconsistent shape (features must be positive multiples of 128)";
-    case EXL3_E_ALIGN: return "pointer not 16-byte aligned";
+    case EXL3_E_SHAPE:
+      return "bad or inconsistent shape (features must be positive multiples of 128, of 8 for "
+             "exl3_lora; row distances at least a row)";
+    case EXL3_E_ALIGN: return "pointer or row distance not aligned (16 bytes, or the element type's size)";
     case EXL3_E_DEVICE: return "pointer not on the current HIP device (or no device)";
     case EXL3_E_WORKSPACE: return "workspace missing or too small";
     case EXL3_E_ARG: return "argument out of range";
@@ -880,6 +889,255 @@ int32_t exl3_profile_read(const exl3_profile *prof, float *ms) {
     ms[i] = t;
   }
   return status;
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------- router operators
+namespace {
+
+// What every router entry point is given. ids is written by exl3_route_topk
+// and read by the others.
+int32_t check_router(const exl3_router *r, const void *logits, int32_t logits_dtype,
+                     int64_t ld_logits, int32_t rows, const void *ids, int32_t ids_dtype) {
+  if (rows < 0) return EXL3_E_ARG;
+  if (!r) return EXL3_E_NULL;
+  if (r->num_experts < 1 || r->num_experts > EXL3_MAX_EXPERTS) return EXL3_E_ARG;
+  if (r->topk < 1 || r->topk > EXL3_MAX_TOPK || r->topk > r->num_experts) return EXL3_E_ARG;
+  if (r->scoring != EXL3_SOFTMAX && r->scoring != EXL3_SIGMOID) return EXL3_E_ARG;
+  if (!std::isfinite(r->scale)) return EXL3_E_ARG;
+  if ((int64_t)rows * r->topk > (int64_t)1 << 30) return EXL3_E_ARG;
+  if (!float_dtype_ok(logits_dtype) || !ids_dtype_ok(ids_dtype)) return EXL3_E_DTYPE;
+  if (rows == 0) return EXL3_OK;
+  if (!logits || !ids) return EXL3_E_NULL;
+  if (ld_logits < r->num_experts || ld_logits > kMaxLd) return EXL3_E_SHAPE;
+  if (!aligned_to(logits, float_size(logits_dtype)) || !aligned_to(ids, ids_align(ids_dtype)))
+    return EXL3_E_ALIGN;
+  return EXL3_OK;
+}
+
+RouterParams router_params(const exl3_router *r, const void *logits, int32_t logits_dtype,
+                           int64_t ld_logits, int32_t rows, const void *ids, int32_t ids_dtype) {
+  RouterParams p{};
+  p.logits = logits;
+  p.logits_dtype = logits_dtype;  // EXL3_F16, BF16, F32 are the kernels' 1, 2, 3
+  p.vec4 = ld_logits % 4 == 0 && aligned_to(logits, 4 * float_size(logits_dtype));
+  p.ld_logits = ld_logits;
+  p.rows = rows;
+  p.E = r->num_experts;
+  p.topk = r->topk;
+  p.sigmoid = r->scoring == EXL3_SIGMOID;
+  p.renorm = r->renorm != 0;
+  p.scale = r->scale;
+  p.ids = const_cast<void *>(ids);
+  p.ids_i64 = ids_dtype == EXL3_I64;
+  return p;
+}
+
+struct BalanceLayout {
+  size_t count, tokens, total;  // the probabilities come first
+  int nblk;
+};
+BalanceLayout balance_layout(int32_t rows, int32_t E) {
+  BalanceLayout L{};
+  L.nblk = balance_blocks(rows);
+  L.count = align_up(4 * (size_t)L.nblk * E);
+  L.tokens = L.count + align_up(4 * (size_t)L.nblk * E);
+  L.total = L.tokens + align_up(4 * (size_t)L.nblk);
+  return L;
+}
+
+}  // namespace
+
+extern "C" {
+
+int32_t exl3_route_topk(const exl3_router *router, const void *logits, int32_t logits_dtype,
+                        int64_t ld_logits, int32_t rows, const uint8_t *row_mask, void *ids,
+                        int32_t ids_dtype, void *w, int32_t w_dtype, void *stream,
+                        exl3_profile *prof) {
+  if (int32_t s = check_router(router, logits, logits_dtype, ld_logits, rows, ids, ids_dtype))
+    return s;
+  if (router->bias && router->scoring != EXL3_SIGMOID) return EXL3_E_ARG;
+  if (!float_dtype_ok(w_dtype)) return EXL3_E_DTYPE;
+  if (rows == 0) return EXL3_OK;
+  if (!w) return EXL3_E_NULL;
+  if (!aligned_to(w, w_align(w_dtype)) || !aligned_to(router->bias, 4)) return EXL3_E_ALIGN;
+  for (const void *q : {logits, (const void *)ids, (const void *)w, (const void *)router->bias,
+                        (const void *)row_mask})
+    if (q && check_device(q)) return EXL3_E_DEVICE;
+
+  RouterParams p = router_params(router, logits, logits_dtype, ld_logits, rows, ids, ids_dtype);
+  p.bias = router->bias;
+  p.row_mask = row_mask;
+  p.w = w;
+  p.w_dtype = w_dtype;
+  ProfScope ps(prof, (hipStream_t)stream, EXL3_K_ROUTE);
+  return launch_route_topk(p, (hipStream_t)stream) == hipSuccess ? EXL3_OK : EXL3_E_LAUNCH;
+}
+
+size_t exl3_balance_workspace_size(int32_t rows, int32_t num_experts) {
+  if (rows < 0 || num_experts < 1 || num_experts > EXL3_MAX_EXPERTS) return 0;
+  return std::max(kAlign, balance_layout(rows, num_experts).total);
+}
+
+int32_t exl3_balance_loss(const exl3_router *router, const void *logits, int32_t logits_dtype,
+                          int64_t ld_logits, int32_t rows, const void *ids, int32_t ids_dtype,
+                          float coef, const exl3_balance *balance, void *ws, size_t ws_bytes,
+                          void *stream, exl3_profile *prof) {
+  if (int32_t s = check_router(router, logits, logits_dtype, ld_logits, rows, ids, ids_dtype))
+    return s;
+  if (!std::isfinite(coef)) return EXL3_E_ARG;
+  if (!balance || !balance->count || !balance->tokens || !balance->prob || !balance->loss || !ws)
+    return EXL3_E_NULL;
+  const void *res[] = {balance->count, balance->tokens, balance->prob, balance->loss};
+  for (const void *q : res)
+    if (!aligned_to(q, 4)) return EXL3_E_ALIGN;
+  if (!aligned16(ws)) return EXL3_E_ALIGN;
+  if (ws_bytes < exl3_balance_workspace_size(rows, router->num_experts)) return EXL3_E_WORKSPACE;
+  if (rows > 0)
+    for (const void *q : {logits, ids})
+      if (check_device(q)) return EXL3_E_DEVICE;
+  for (const void *q : res)
+    if (check_device(q)) return EXL3_E_DEVICE;
+  if (check_device(ws)) return EXL3_E_DEVICE;
+
+  hipStream_t st = (hipStream_t)stream;
+  RouterParams p = router_params(router, logits, logits_dtype, ld_logits, rows, ids, ids_dtype);
+  const BalanceLayout L = balance_layout(rows, router->num_experts);
+  p.nblk = L.nblk;
+  p.part_prob = at<float>(ws, 0);
+  p.part_count = at<int32_t>(ws, L.count);
+  p.part_tokens = at<int32_t>(ws, L.tokens);
+  p.coef = coef;
+  p.count = balance->count;
+  p.tokens = balance->tokens;
+  p.prob = balance->prob;
+  p.loss = balance->loss;
+  if (rows > 0) {
+    ProfScope ps(prof, st, EXL3_K_BALANCE);
+    if (launch_balance(p, st) != hipSuccess) return EXL3_E_LAUNCH;
+  }
+  ProfScope ps(prof, st, EXL3_K_BALANCE_SUM);
+  return launch_balance_sum(p, st) == hipSuccess ? EXL3_OK : EXL3_E_LAUNCH;
+}
+
+int32_t exl3_route_backward(const exl3_router *router, const void *logits, int32_t logits_dtype,
+                            int64_t ld_logits, int32_t rows, const void *ids, int32_t ids_dtype,
+                            const void *dw, int32_t dw_dtype, const exl3_balance *balance,
+                            float coef, const float *dloss, void *dlogits,
+                            int32_t dlogits_dtype, int64_t ld_dlogits, void *stream,
+                            exl3_profile *prof) {
+  if (int32_t s = check_router(router, logits, logits_dtype, ld_logits, rows, ids, ids_dtype))
+    return s;
+  if (!float_dtype_ok(dlogits_dtype) || (dw && !float_dtype_ok(dw_dtype))) return EXL3_E_DTYPE;
+  if (!std::isfinite(coef)) return EXL3_E_ARG;
+  if (rows == 0) return EXL3_OK;
+  if (!dlogits || (!dw && !balance)) return EXL3_E_NULL;
+  if (balance && (!balance->count || !balance->tokens)) return EXL3_E_NULL;
+  if (ld_dlogits < router->num_experts || ld_dlogits > kMaxLd) return EXL3_E_SHAPE;
+  // in place only with every element over itself
+  if (dlogits == logits && (dlogits_dtype != logits_dtype || ld_dlogits != ld_logits))
+    return EXL3_E_ARG;
+  if (!aligned_to(dlogits, float_size(dlogits_dtype))) return EXL3_E_ALIGN;
+  if (dw && !aligned_to(dw, w_align(dw_dtype))) return EXL3_E_ALIGN;
+  if (balance && (!aligned_to(balance->count, 4) || !aligned_to(balance->tokens, 4) ||
+                  !aligned_to(dloss, 4)))
+    return EXL3_E_ALIGN;
+  for (const void *q : {logits, ids, (const void *)dlogits, dw})
+    if (q && check_device(q)) return EXL3_E_DEVICE;
+  if (balance)
+    for (const void *q : {(const void *)balance->count, (const void *)balance->tokens,
+                          (const void *)dloss})
+      if (q && check_device(q)) return EXL3_E_DEVICE;
+
+  RouterParams p = router_params(router, logits, logits_dtype, ld_logits, rows, ids, ids_dtype);
+  p.dw = dw;
+  p.dw_dtype = dw_dtype;
+  if (balance) {
+    p.count = balance->count;
+    p.tokens = balance->tokens;
+    p.dloss = dloss;
+    p.coef = coef;
+  }
+  p.dlogits = dlogits;
+  p.dlogits_dtype = dlogits_dtype;
+  p.ld_dlogits = ld_dlogits;
+  ProfScope ps(prof, (hipStream_t)stream, EXL3_K_ROUTE_BACKWARD);
+  return launch_route_backward(p, (hipStream_t)stream) == hipSuccess ? EXL3_OK : EXL3_E_LAUNCH;
+}
+
+// ---------------------------------------------------------------- adapters
+size_t exl3_lora_workspace_size(int32_t rows, int32_t in_features, int32_t rank) {
+  if (rows < 0 || in_features < 1 || in_features > EXL3_MAX_FEATURES || rank < 1 ||
+      rank > EXL3_MAX_RANK)
+    return 0;
+  return std::max(kAlign, 4 * (size_t)lora_groups(in_features) * (size_t)rows *
+                              (size_t)lora_padded_rank(rank));
+}
+
+int32_t exl3_lora(const exl3_lora_adapters *ad, const uint16_t *x, int32_t x_dtype, int64_t ld_x,
+                  int32_t rows, const void *ids, int32_t ids_dtype, const void *base,
+                  int32_t base_dtype, int64_t ld_base, void *out, int32_t out_dtype,
+                  int64_t ld_out, void *ws, size_t ws_bytes, void *stream, exl3_profile *prof) {
+  if (rows < 0 || rows > EXL3_LORA_MAX_ROWS) return EXL3_E_ARG;
+  if (rows == 0) return EXL3_OK;
+  if (!ad || !ad->a || !ad->b || !x || !ids || !out || !ws) return EXL3_E_NULL;
+  if (ad->rank < 1 || ad->rank > EXL3_MAX_RANK) return EXL3_E_ARG;
+  if (ad->num_adapters < 1 || ad->num_adapters > EXL3_MAX_ADAPTERS) return EXL3_E_ARG;
+  if (!x_dtype_ok(x_dtype) || !ids_dtype_ok(ids_dtype) || !out_dtype_ok(out_dtype) ||
+      (base && !out_dtype_ok(base_dtype)))
+    return EXL3_E_DTYPE;
+  const int64_t K = ad->in_features, N = ad->out_features;
+  for (int64_t f : {K, N})
+    if (f < 8 || f > EXL3_MAX_FEATURES || f % 8) return EXL3_E_SHAPE;
+  if (ld_x < K || ld_out < N || (base && ld_base < N)) return EXL3_E_SHAPE;
+  if (ld_x > kMaxLd || ld_out > kMaxLd || (base && ld_base > kMaxLd)) return EXL3_E_SHAPE;
+  if (base == out && (base_dtype != out_dtype || ld_base != ld_out)) return EXL3_E_ARG;
+  for (const void *q : {(const void *)ad->a, (const void *)ad->b, (const void *)x, base,
+                        (const void *)out, (const void *)ws})
+    if (!aligned16(q)) return EXL3_E_ALIGN;
+  if (ld_x % 8 || ld_out * (int64_t)float_size(out_dtype) % 16 ||
+      (base && ld_base * (int64_t)float_size(base_dtype) % 16))
+    return EXL3_E_ALIGN;
+  if (!aligned_to(ids, ids_align(ids_dtype)) || !aligned_to(ad->scale, 4) ||
+      !aligned_to(ad->ranks, 4))
+    return EXL3_E_ALIGN;
+  if (ws_bytes < exl3_lora_workspace_size(rows, ad->in_features, ad->rank))
+    return EXL3_E_WORKSPACE;
+  for (const void *q : {(const void *)ad->a, (const void *)ad->b, (const void *)ad->scale,
+                        (const void *)ad->ranks, (const void *)x, ids, base, (const void *)out,
+                        (const void *)ws})
+    if (q && check_device(q)) return EXL3_E_DEVICE;
+
+  hipStream_t st = (hipStream_t)stream;
+  LoraParams p{};
+  p.K = ad->in_features;
+  p.N = ad->out_features;
+  p.R = ad->rank;
+  p.adapters = ad->num_adapters;
+  p.a = ad->a;
+  p.b = ad->b;
+  p.scale = ad->scale;
+  p.ranks = ad->ranks;
+  p.x = x;
+  p.bf16 = x_dtype == EXL3_BF16;
+  p.ldx = ld_x;
+  p.rows = rows;
+  p.ids = ids;
+  p.ids_i64 = ids_dtype == EXL3_I64;
+  p.base = base;
+  p.base_dtype = base_dtype;
+  p.ldbase = ld_base;
+  p.out = out;
+  p.out_dtype = out_dtype;
+  p.ldout = ld_out;
+  p.part = (float *)ws;
+  {
+    ProfScope ps(prof, st, EXL3_K_LORA_A);
+    if (launch_lora_a(p, st) != hipSuccess) return EXL3_E_LAUNCH;
+  }
+  ProfScope ps(prof, st, EXL3_K_LORA_B);
+  return launch_lora_b(p, st) == hipSuccess ? EXL3_OK : EXL3_E_LAUNCH;
 }
 
 }  // extern "C"

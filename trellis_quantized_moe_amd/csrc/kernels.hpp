@@ -118,6 +118,59 @@ struct PackParams {
   int nblk;
 };
 
+// Router kernels (router.hip). dtype codes: 1 fp16, 2 bf16, 3 fp32.
+struct RouterParams {
+  const void *logits;  // [rows][E], rows ld_logits elements apart
+  int logits_dtype;
+  int vec4;  // each group of four logits of a row can be one load
+  int64_t ld_logits;
+  int rows, E, topk;
+  int sigmoid, renorm;
+  float scale;
+  const float *bias;        // route_topk: [E] or null
+  const uint8_t *row_mask;  // route_topk: [rows] or null
+  void *ids;                // [rows][topk]; route_topk writes, the others read
+  int ids_i64;
+  void *w;  // route_topk: [rows][topk]
+  int w_dtype;
+  // balance: partial sums of nblk workgroups, and the results
+  float *part_prob;      // [nblk][E]
+  int32_t *part_count;   // [nblk][E]
+  int32_t *part_tokens;  // [nblk]
+  int nblk;
+  float coef;
+  int32_t *count, *tokens;  // backward reads them (count null: no balance loss)
+  float *prob, *loss;
+  // backward
+  const void *dw;  // [rows][topk] or null
+  int dw_dtype;
+  const float *dloss;  // [1] or null (1)
+  void *dlogits;
+  int dlogits_dtype;
+  int64_t ld_dlogits;
+};
+
+// Low-rank adapters (lora.hip).
+struct LoraParams {
+  int K, N, R, adapters;
+  const uint16_t *a, *b;  // [adapters][R][K], [adapters][N][R]
+  const float *scale;     // [adapters] or null
+  const int32_t *ranks;   // [adapters] or null
+  const uint16_t *x;      // [rows][K], rows ldx apart
+  int bf16;
+  int64_t ldx;
+  int rows;
+  const void *ids;
+  int ids_i64;
+  const void *base;  // [rows][N] or null, dtype codes as RouterParams
+  int base_dtype;
+  int64_t ldbase;
+  void *out;
+  int out_dtype;
+  int64_t ldout;
+  float *part;  // x A^T: [lora_groups(K)][rows][lora_padded_rank(R)]
+};
+
 hipError_t launch_gemm(int epi, const GemmParams &p, int tiles, int nblocks,
                        hipStream_t s, bool wide);
 // 128-row tiles (gemm_wide.hip); called by launch_gemm.
@@ -152,6 +205,16 @@ bool pack_rotate_fits(int64_t pairs, int passes);
 hipError_t launch_pack_rotate(const PackParams &p, const RotParams &rp, hipStream_t s);
 hipError_t launch_decode_tiles(const uint16_t *words, int ntiles, int K,
                                uint16_t *out, hipStream_t s);
+
+hipError_t launch_route_topk(const RouterParams &p, hipStream_t s);
+int balance_blocks(int rows);  // RouterParams::nblk of a call
+hipError_t launch_balance(const RouterParams &p, hipStream_t s);
+hipError_t launch_balance_sum(const RouterParams &p, hipStream_t s);
+hipError_t launch_route_backward(const RouterParams &p, hipStream_t s);
+int lora_groups(int K);
+int lora_padded_rank(int R);
+hipError_t launch_lora_a(const LoraParams &p, hipStream_t s);
+hipError_t launch_lora_b(const LoraParams &p, hipStream_t s);
 
 constexpr int kBM = 16;       // rows per narrow GEMM work tile
 constexpr int kMaxTopk = 32;  // EXL3_MAX_TOPK

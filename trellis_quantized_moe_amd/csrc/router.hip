@@ -1,0 +1,528 @@
+// Router kernels: logits -> route IDs and weights, the balance loss of a
+// routing with its per-expert counts, and the gradient of both with respect to
+// the logits. Every one reads each logit once.
+//
+// Layout: 16 lanes hold one row, four rows to a wave. Lane i of a row holds
+// experts 64 j + 4 i + v (v = 0..3) of block j in l[4 j + v]: 16 bytes of fp32
+// or 8 of a 16-bit type in one load, and a block of a row is one run of 256 or
+// 128 bytes. Reductions over a row are four rotations inside the 16 lanes of a
+// DPP row, with no LDS traffic.
+#include <type_traits>
+
+#include "common.hpp"
+#include "kernels.hpp"
+
+namespace exl3 {
+
+namespace {
+
+constexpr int kRowsPerWg = 16;  // 256 threads
+constexpr float kFltMax = 3.40282346638528859812e+38f;
+constexpr float kNegInf = -__builtin_inff();
+
+// ------------------------------------------------- 16-lane row reductions
+// ror16<N>(v): the value of the lane N places on inside the 16-lane DPP row.
+template <int N>
+__device__ __forceinline__ int ror16(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, 0x120 + N, 0xf, 0xf, true);
+}
+template <int N>
+__device__ __forceinline__ float ror16(float v) {
+  return __builtin_bit_cast(float, ror16<N>(__builtin_bit_cast(int, v)));
+}
+template <int N>
+__device__ __forceinline__ double ror16(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)ror16<N>((int)(uint32_t)u);
+  const uint32_t hi = (uint32_t)ror16<N>((int)(uint32_t)(u >> 32));
+  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+__device__ __forceinline__ float kmax(float a, float b) { return fmaxf(a, b); }
+__device__ __forceinline__ double kmax(double a, double b) { return fmax(a, b); }
+// Every lane gets the result; sums add the same pairs in every lane.
+template <typename T>
+__device__ __forceinline__ T row_max(T v) {
+  v = kmax(v, ror16<8>(v));
+  v = kmax(v, ror16<4>(v));
+  v = kmax(v, ror16<2>(v));
+  return kmax(v, ror16<1>(v));
+}
+__device__ __forceinline__ int row_min(int v) {
+  v = min(v, ror16<8>(v));
+  v = min(v, ror16<4>(v));
+  v = min(v, ror16<2>(v));
+  return min(v, ror16<1>(v));
+}
+__device__ __forceinline__ float row_sum(float v) {
+  v += ror16<8>(v);
+  v += ror16<4>(v);
+  v += ror16<2>(v);
+  return v + ror16<1>(v);
+}
+__device__ __forceinline__ bool row_any(bool b) {
+  const int shift = (threadIdx.x & 48);
+  return ((__ballot(b) >> shift) & 0xffffull) != 0;
+}
+
+// ------------------------------------------------------------------ loads
+// dtype codes of the launch parameters: 1 fp16, 2 bf16, 3 fp32
+__device__ __forceinline__ float load_as_f32(const void *p, int dtype, int64_t i) {
+  if (dtype == 3) return ((const float *)p)[i];
+  const uint16_t b = ((const uint16_t *)p)[i];
+  return dtype == 2 ? bf16_bits_to_f32(b) : f16_bits_to_f32(b);
+}
+// NaN and -inf -> -inf (the expert takes no part), +inf -> the largest finite
+// fp32 (exp(l - max) stays defined).
+__device__ __forceinline__ float clean(float l) {
+  return l == l ? fminf(l, kFltMax) : kNegInf;
+}
+__device__ __forceinline__ int64_t load_id(const void *p, int i64, int64_t i) {
+  return i64 ? ((const int64_t *)p)[i] : (int64_t)((const int32_t *)p)[i];
+}
+
+// The lane's logits of the row whose first element has index `at`. vec4:
+// every group of four starts on a multiple of four elements and is one load; a
+// group that runs past E is read element by element. The type is tested once
+// around each loop, so all loads of a row are in flight together.
+template <int I>
+__device__ __forceinline__ void load_row(const RouterParams &p, int64_t at, int lane,
+                                         float (&l)[4 * I]) {
+  auto scalar = [&](int j) {
+    const int e0 = 64 * j + 4 * lane;
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+      l[4 * j + v] =
+          e0 + v < p.E ? load_as_f32(p.logits, p.logits_dtype, at + e0 + v) : kNegInf;
+  };
+  if (p.vec4 && p.logits_dtype == 3) {
+    const float *q = (const float *)p.logits + at + 4 * lane;
+#pragma unroll
+    for (int j = 0; j < I; ++j) {
+      if (64 * j + 4 * lane + 4 <= p.E) {
+        const f32x4 x = *(const f32x4 *)(q + 64 * j);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) l[4 * j + v] = x[v];
+      } else {
+        scalar(j);
+      }
+    }
+  } else if (p.vec4) {
+    const uint16_t *q = (const uint16_t *)p.logits + at + 4 * lane;
+    uint2 x[I];
+#pragma unroll
+    for (int j = 0; j < I; ++j)
+      if (64 * j + 4 * lane + 4 <= p.E) x[j] = *(const uint2 *)(q + 64 * j);
+#pragma unroll
+    for (int j = 0; j < I; ++j) {
+      if (64 * j + 4 * lane + 4 <= p.E) {
+        const uint32_t w[2] = {x[j].x, x[j].y};
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const uint16_t b = (uint16_t)(w[v >> 1] >> (16 * (v & 1)));
+          l[4 * j + v] = p.logits_dtype == 2 ? bf16_bits_to_f32(b) : f16_bits_to_f32(b);
+        }
+      } else {
+        scalar(j);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < I; ++j) scalar(j);
+  }
+#pragma unroll
+  for (int j = 0; j < 4 * I; ++j) l[j] = clean(l[j]);
+}
+
+template <int N>
+__device__ __forceinline__ float max_of(const float (&l)[N]) {
+  float m = l[0];
+#pragma unroll
+  for (int j = 1; j < N; ++j) m = fmaxf(m, l[j]);
+  return m;
+}
+
+// ------------------------------------------------------------------ scores
+// A row's t_e up to one factor per row (it cancels wherever t is divided by a
+// sum of t). Softmax: exp(l - m), m the row's largest logit. Sigmoid:
+// 1 / (1 + exp(-l)) times exp(-m), m = min(0, largest logit), as
+// exp(l - m) / (1 + exp(l)) for l < 0 (m = 0 where any l is not): the largest
+// t is at least 1/2, so no sum of t underflows however far below zero the
+// logits lie. shift() maps the largest logit to m; a row without experts
+// (largest logit -inf) gets m = 0 and t = 0 throughout.
+__device__ __forceinline__ float shift(bool sigmoid, float largest) {
+  if (largest == kNegInf) return 0.0f;
+  return sigmoid ? fminf(0.0f, largest) : largest;
+}
+__device__ __forceinline__ float strength(bool sigmoid, float l, float m) {
+  if (!sigmoid) return expf(l - m);
+  const float z = expf(-fabsf(l));
+  return (l < 0.0f ? expf(l - m) : 1.0f) / (1.0f + z);
+}
+// d log t / d l: 1, or 1 - sigmoid(l) computed without cancellation.
+__device__ __forceinline__ float slope(bool sigmoid, float l) {
+  if (!sigmoid) return 1.0f;
+  const float z = expf(-fabsf(l));
+  return (l < 0.0f ? 1.0f : z) / (1.0f + z);
+}
+// 1 / x, 0 for an empty sum.
+__device__ __forceinline__ float inv_or_0(float x) { return x > 0.0f ? 1.0f / x : 0.0f; }
+
+__device__ __forceinline__ void store_as(void *p, int dtype, int64_t i, float v) {
+  if (dtype == 3) ((float *)p)[i] = v;
+  else ((uint16_t *)p)[i] = f32_to_out16(v, dtype == 2);
+}
+
+// ------------------------------------------------------------------- top-k
+// Selection keys: the logit itself, or with a bias sigmoid(l) + bias in fp64.
+// fp32 would round the sum to 2^-24 and order near-equal experts by their
+// index rather than their score.
+template <bool BIAS>
+struct Key {
+  typedef float type;
+};
+template <>
+struct Key<true> {
+  typedef double type;
+};
+
+template <int I, bool BIAS>
+__global__ void __launch_bounds__(256) route_topk_kernel(RouterParams p) {
+  typedef typename Key<BIAS>::type key_t;
+  const int lane = threadIdx.x & 15;
+  const int64_t row = (int64_t)blockIdx.x * kRowsPerWg + (threadIdx.x >> 4);
+  const bool in = row < p.rows;
+  const bool live = in && (!p.row_mask || p.row_mask[row] != 0);
+  const int64_t at = (live ? row : 0) * p.ld_logits;
+  float l[4 * I];
+  load_row<I>(p, at, lane, l);
+  if (!live) {
+#pragma unroll
+    for (int j = 0; j < 4 * I; ++j) l[j] = kNegInf;
+  }
+  const bool sig = p.sigmoid;
+  // softmax over all experts: its sum, while the logits are at hand
+  const float m_all = shift(sig, row_max(max_of(l)));
+  float total = 0.0f;
+  if (!sig && !p.renorm) {
+#pragma unroll
+    for (int j = 0; j < 4 * I; ++j) total += strength(false, l[j], m_all);
+    total = row_sum(total);
+  }
+  key_t s[4 * I];
+#pragma unroll
+  for (int j = 0; j < 4 * I; ++j) {
+    const int e = 64 * (j >> 2) + 4 * lane + (j & 3);
+    if constexpr (BIAS) {
+      const double b = e < p.E ? (double)p.bias[e] : 0.0;
+      const double v = 1.0 / (1.0 + exp(-(double)l[j])) + b;
+      s[j] = l[j] > kNegInf && v == v ? v : (double)kNegInf;
+    } else {
+      s[j] = l[j];
+    }
+  }
+  // k times: the largest key of the row, then the lowest expert holding it.
+  // Lane j keeps picks j and j + 16.
+  int pick[2] = {-1, -1};
+  for (int k = 0; k < p.topk; ++k) {
+    key_t best = s[0];
+#pragma unroll
+    for (int j = 1; j < 4 * I; ++j) best = kmax(best, s[j]);
+    best = row_max(best);
+    int e = 0x7fffffff;
+#pragma unroll
+    for (int j = 4 * I - 1; j >= 0; --j)
+      e = s[j] == best ? 64 * (j >> 2) + 4 * lane + (j & 3) : e;
+    e = row_min(e);
+    const bool some = best > (key_t)kNegInf;
+#pragma unroll
+    for (int j = 0; j < 4 * I; ++j)
+      s[j] = 64 * (j >> 2) + 4 * lane + (j & 3) == e ? (key_t)kNegInf : s[j];
+    if ((k & 15) == lane) pick[k >> 4] = some ? e : -1;
+  }
+  // weights of the picks, from their logits
+  float lp[2], t[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    lp[h] = pick[h] >= 0 ? clean(load_as_f32(p.logits, p.logits_dtype, at + pick[h])) : kNegInf;
+  const float m = p.renorm ? shift(sig, row_max(fmaxf(lp[0], lp[1]))) : sig ? 0.0f : m_all;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) t[h] = pick[h] >= 0 ? strength(sig, lp[h], m) : 0.0f;
+  if (p.renorm) total = row_sum(t[0] + t[1]);
+  if (!in) return;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int k = lane + 16 * h;
+    if (k >= p.topk) continue;
+    const int64_t o = row * p.topk + k;
+    const float w = pick[h] < 0 ? 0.0f : (sig && !p.renorm) ? p.scale * t[h]
+                                                            : p.scale * (t[h] / total);
+    if (p.ids_i64) ((int64_t *)p.ids)[o] = pick[h];
+    else ((int32_t *)p.ids)[o] = pick[h];
+    store_as(p.w, p.w_dtype, o, w);
+  }
+}
+
+// The row's IDs j = lane and lane + 16: the expert, or -1 (none, outside
+// [0, E), or past the row's topk).
+__device__ __forceinline__ void load_ids(const RouterParams &p, int64_t row, bool in, int lane,
+                                         int (&id)[2]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int k = lane + 16 * h;
+    id[h] = -1;
+    if (in && k < p.topk) {
+      const int64_t v = load_id(p.ids, p.ids_i64, row * p.topk + k);
+      if (v >= 0 && v < p.E) id[h] = (int)v;
+    }
+  }
+}
+
+// ----------------------------------------------------------------- balance
+// Workgroup b sums rows 16 b + 16 gridDim n + its 16 row groups: probabilities
+// in registers, counts by LDS integer atomics (exact in any order). Its sums
+// go to part_prob[b][E], part_count[b][E] and part_tokens[b]; they are added
+// in the order of b by balance_sum_kernel, so the same call gives the same
+// bytes.
+template <int I>
+__global__ void __launch_bounds__(256) balance_kernel(RouterParams p) {
+  __shared__ int s_count[64 * I];
+  __shared__ float s_prob[4][64 * I];
+  __shared__ int s_tokens;
+  const int lane = threadIdx.x & 15, wave = threadIdx.x >> 6;
+  for (int e = threadIdx.x; e < 64 * I; e += 256) s_count[e] = 0;
+  if (threadIdx.x == 0) s_tokens = 0;
+  __syncthreads();
+  float acc[4 * I];
+#pragma unroll
+  for (int j = 0; j < 4 * I; ++j) acc[j] = 0.0f;
+  const bool sig = p.sigmoid;
+  for (int64_t r0 = (int64_t)blockIdx.x * kRowsPerWg; r0 < p.rows;
+       r0 += (int64_t)gridDim.x * kRowsPerWg) {
+    const int64_t row = r0 + (threadIdx.x >> 4);
+    const bool in = row < p.rows;
+    int id[2];
+    load_ids(p, row, in, lane, id);
+    float l[4 * I];
+    load_row<I>(p, (in ? row : 0) * p.ld_logits, lane, l);
+    const bool live = row_any(id[0] >= 0 || id[1] >= 0);
+    const float m = shift(sig, row_max(max_of(l)));
+    float t[4 * I], sum = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 4 * I; ++j) {
+      t[j] = strength(sig, l[j], m);
+      sum += t[j];
+    }
+    const float inv = live ? inv_or_0(row_sum(sum)) : 0.0f;
+#pragma unroll
+    for (int j = 0; j < 4 * I; ++j) acc[j] += t[j] * inv;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (id[h] >= 0) atomicAdd(&s_count[id[h]], 1);
+    if (lane == 0 && live) atomicAdd(&s_tokens, 1);
+  }
+  // the wave's four rows, then the four waves
+#pragma unroll
+  for (int j = 0; j < 4 * I; ++j) {
+    acc[j] += __shfl_xor(acc[j], 16, 64);
+    acc[j] += __shfl_xor(acc[j], 32, 64);
+    if ((threadIdx.x & 48) == 0) s_prob[wave][64 * (j >> 2) + 4 * lane + (j & 3)] = acc[j];
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < p.E; e += 256) {
+    p.part_prob[(int64_t)blockIdx.x * p.E + e] =
+        (s_prob[0][e] + s_prob[1][e]) + (s_prob[2][e] + s_prob[3][e]);
+    p.part_count[(int64_t)blockIdx.x * p.E + e] = s_count[e];
+  }
+  if (threadIdx.x == 0) p.part_tokens[blockIdx.x] = s_tokens;
+}
+
+// One workgroup: adds the partial sums and forms the loss.
+__global__ void __launch_bounds__(1024) balance_sum_kernel(RouterParams p) {
+  __shared__ float s_f[1024];
+  __shared__ int s_tokens;
+  if (threadIdx.x == 0) s_tokens = 0;
+  __syncthreads();
+  for (int b = threadIdx.x; b < p.nblk; b += 1024) atomicAdd(&s_tokens, p.part_tokens[b]);
+  __syncthreads();
+  const int T = s_tokens;
+  const int e = threadIdx.x;
+  float prob = 0.0f;
+  int count = 0;
+  if (e < p.E) {
+    for (int b = 0; b < p.nblk; ++b) {
+      prob += p.part_prob[(int64_t)b * p.E + e];
+      count += p.part_count[(int64_t)b * p.E + e];
+    }
+    prob = T > 0 ? prob / (float)T : 0.0f;
+    p.count[e] = count;
+    p.prob[e] = prob;
+  }
+  const float pairs = (float)T * (float)p.topk;
+  s_f[e] = e < p.E && T > 0 ? (float)count / pairs * prob : 0.0f;
+  for (int d = 512; d > 0; d >>= 1) {
+    __syncthreads();
+    if (e < d) s_f[e] += s_f[e + d];
+  }
+  if (e == 0) {
+    p.tokens[0] = T;
+    p.loss[0] = p.coef * (float)p.E * s_f[0];
+  }
+}
+
+// ---------------------------------------------------------------- backward
+// With g the incoming gradient and p, q = t over its sum over all experts,
+// over the chosen:
+//   weights  renorm         dl_e = scale q_e h_e (g_e - sum q g)
+//            softmax, all   dl_e = scale p_e (g_e - sum p g)
+//            sigmoid        dl_e = scale t_e h_e g_e
+//   balance  dl_e = c p_e h_e (f_e - sum f p),  c = dloss coef E / T
+// (h = slope, g = 0 where not chosen). Both in one pass over the row.
+template <int I>
+__global__ void __launch_bounds__(256) route_backward_kernel(RouterParams p) {
+  const int lane = threadIdx.x & 15;
+  const int64_t row = (int64_t)blockIdx.x * kRowsPerWg + (threadIdx.x >> 4);
+  const bool in = row < p.rows;
+  int id[2];
+  load_ids(p, row, in, lane, id);
+  const int64_t at = (in ? row : 0) * p.ld_logits;
+  float l[4 * I];
+  load_row<I>(p, at, lane, l);
+  const bool sig = p.sigmoid;
+  const bool live = row_any(id[0] >= 0 || id[1] >= 0);
+
+  // the chosen entries: logit, strength, weight gradient
+  float lp[2], g[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const bool ok = id[h] >= 0;
+    lp[h] = ok ? clean(load_as_f32(p.logits, p.logits_dtype, at + id[h])) : kNegInf;
+    g[h] = ok && p.dw ? load_as_f32(p.dw, p.dw_dtype, row * p.topk + lane + 16 * h) : 0.0f;
+    if (lp[h] == kNegInf) g[h] = 0.0f;  // an expert that takes no part
+  }
+  const float m = shift(sig, row_max(max_of(l)));
+  const bool need_all = p.count != nullptr || (!sig && !p.renorm);
+  float pe[4 * I], total = 0.0f;  // p_e
+#pragma unroll
+  for (int j = 0; j < 4 * I; ++j) pe[j] = 0.0f;
+  if (need_all) {
+#pragma unroll
+    for (int j = 0; j < 4 * I; ++j) {
+      pe[j] = strength(sig, l[j], m);
+      total += pe[j];
+    }
+  }
+  const float inv = inv_or_0(row_sum(total));
+#pragma unroll
+  for (int j = 0; j < 4 * I; ++j) pe[j] *= inv;
+
+  // v: what each chosen entry adds to its expert's gradient
+  float v[2], common = 0.0f;  // softmax over all: dl_e -= p_e * common
+  if (p.renorm) {
+    const float mc = shift(sig, row_max(fmaxf(lp[0], lp[1])));
+    float q[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) q[h] = strength(sig, lp[h], mc);
+    const float iq = inv_or_0(row_sum(q[0] + q[1]));
+    const float mean = row_sum(q[0] * g[0] + q[1] * g[1]) * iq;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      v[h] = lp[h] > kNegInf ? p.scale * (q[h] * iq) * slope(sig, lp[h]) * (g[h] - mean) : 0.0f;
+  } else if (sig) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      v[h] = p.scale * strength(true, lp[h], 0.0f) * slope(true, lp[h]) * g[h];
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) v[h] = p.scale * (strength(false, lp[h], m) * inv) * g[h];
+    common = row_sum(v[0] + v[1]);
+  }
+
+  // the balance loss: c f_e and c sum f p
+  float cf[4 * I], cmean = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 4 * I; ++j) cf[j] = 0.0f;
+  if (p.count) {
+    const float T = (float)*p.tokens;
+    const float c = T > 0.0f ? (p.dloss ? *p.dloss : 1.0f) * p.coef * (float)p.E / T : 0.0f;
+    const float cn = T > 0.0f ? c / (T * (float)p.topk) : 0.0f;
+#pragma unroll
+    for (int j = 0; j < 4 * I; ++j) {
+      const int e = 64 * (j >> 2) + 4 * lane + (j & 3);
+      cf[j] = e < p.E ? cn * (float)p.count[e] : 0.0f;
+      cmean += cf[j] * pe[j];
+    }
+    cmean = row_sum(cmean);
+  }
+  float d[4 * I];
+#pragma unroll
+  for (int j = 0; j < 4 * I; ++j) d[j] = pe[j] * (slope(sig, l[j]) * (cf[j] - cmean) - common);
+  // the chosen entries in the order of the row's IDs
+  for (int k = 0; k < p.topk; ++k) {
+    const int src = (threadIdx.x & 48) | (k & 15);
+    const int e = __shfl(k < 16 ? id[0] : id[1], src, 64);
+    const float a = __shfl(k < 16 ? v[0] : v[1], src, 64);
+#pragma unroll
+    for (int j = 0; j < 4 * I; ++j)
+      d[j] += 64 * (j >> 2) + 4 * lane + (j & 3) == e ? a : 0.0f;
+  }
+  if (!in) return;
+  const int64_t to = row * p.ld_dlogits;
+#pragma unroll
+  for (int j = 0; j < 4 * I; ++j) {
+    const int e = 64 * (j >> 2) + 4 * lane + (j & 3);
+    // a row or an expert that takes no part has gradient 0
+    if (e < p.E)
+      store_as(p.dlogits, p.dlogits_dtype, to + e, live && l[j] > kNegInf ? d[j] : 0.0f);
+  }
+}
+
+// Blocks of 64 experts a kernel instance holds per row.
+template <typename F>
+hipError_t by_blocks(int E, F f) {
+  const int blocks = (E + 63) / 64;
+  if (blocks <= 1) f(std::integral_constant<int, 1>());
+  else if (blocks <= 2) f(std::integral_constant<int, 2>());
+  else if (blocks <= 3) f(std::integral_constant<int, 3>());
+  else if (blocks <= 4) f(std::integral_constant<int, 4>());
+  else if (blocks <= 8) f(std::integral_constant<int, 8>());
+  else if (blocks <= 16) f(std::integral_constant<int, 16>());
+  else return hipErrorInvalidValue;
+  return hipGetLastError();
+}
+
+unsigned row_groups(int rows) { return (unsigned)((rows + kRowsPerWg - 1) / kRowsPerWg); }
+
+}  // namespace
+
+hipError_t launch_route_topk(const RouterParams &p, hipStream_t s) {
+  return by_blocks(p.E, [&](auto I) {
+    if (p.bias)
+      hipLaunchKernelGGL((route_topk_kernel<decltype(I)::value, true>), dim3(row_groups(p.rows)),
+                         dim3(256), 0, s, p);
+    else
+      hipLaunchKernelGGL((route_topk_kernel<decltype(I)::value, false>), dim3(row_groups(p.rows)),
+                         dim3(256), 0, s, p);
+  });
+}
+
+int balance_blocks(int rows) { return rows > 0 ? (int)min(row_groups(rows), 256u) : 0; }
+
+hipError_t launch_balance(const RouterParams &p, hipStream_t s) {
+  return by_blocks(p.E, [&](auto I) {
+    hipLaunchKernelGGL((balance_kernel<decltype(I)::value>), dim3(p.nblk), dim3(256), 0, s, p);
+  });
+}
+
+hipError_t launch_balance_sum(const RouterParams &p, hipStream_t s) {
+  hipLaunchKernelGGL(balance_sum_kernel, dim3(1), dim3(1024), 0, s, p);
+  return hipGetLastError();
+}
+
+hipError_t launch_route_backward(const RouterParams &p, hipStream_t s) {
+  return by_blocks(p.E, [&](auto I) {
+    hipLaunchKernelGGL((route_backward_kernel<decltype(I)::value>), dim3(row_groups(p.rows)),
+                       dim3(256), 0, s, p);
+  });
+}
+
+}  // namespace exl3

@@ -49,6 +49,21 @@ class ProfileC(ctypes.Structure):
                 ("cap", ctypes.c_int32), ("n", ctypes.c_int32)]
 
 
+class RouterC(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("num_experts", "topk", "scoring", "renorm")] + [
+        ("scale", ctypes.c_float), ("bias", ctypes.c_void_p)]
+
+
+class BalanceC(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("count", "tokens", "prob", "loss")]
+
+
+class LoraC(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("in_features", "out_features", "rank", "num_adapters")] + [
+        (n, ctypes.c_void_p) for n in ("a", "b", "scale", "ranks")]
+
+
 class LayoutC(ctypes.Structure):
     _fields_ = [(n, ctypes.c_size_t) for n in
                 ("ctrl", "meta", "expert_of_pos", "plan", "xt", "at", "d", "yacc",
@@ -58,6 +73,7 @@ class LayoutC(ctypes.Structure):
 
 _lib = None
 _i32, _sz, _vp = ctypes.c_int32, ctypes.c_size_t, ctypes.c_void_p
+_i64, _f32 = ctypes.c_int64, ctypes.c_float
 _PP = ctypes.POINTER(ProfileC)
 _SIGS = {
     "exl3_abi_version": (_i32, []),
@@ -81,13 +97,26 @@ _SIGS = {
                                  ctypes.POINTER(ProjC), _vp, _i32, _i32, _i32, _vp, _sz,
                                  _vp, _PP]),
     "exl3_moe_layout": (_i32, [_i32] * 6 + [ctypes.POINTER(LayoutC)]),
+    "exl3_route_topk": (_i32, [ctypes.POINTER(RouterC), _vp, _i32, _i64, _i32, _vp, _vp, _i32,
+                               _vp, _i32, _vp, _PP]),
+    "exl3_balance_workspace_size": (_sz, [_i32, _i32]),
+    "exl3_balance_loss": (_i32, [ctypes.POINTER(RouterC), _vp, _i32, _i64, _i32, _vp, _i32, _f32,
+                                 ctypes.POINTER(BalanceC), _vp, _sz, _vp, _PP]),
+    "exl3_route_backward": (_i32, [ctypes.POINTER(RouterC), _vp, _i32, _i64, _i32, _vp, _i32, _vp,
+                                   _i32, ctypes.POINTER(BalanceC), _f32, _vp, _vp, _i32, _i64,
+                                   _vp, _PP]),
+    "exl3_lora_workspace_size": (_sz, [_i32, _i32, _i32]),
+    "exl3_lora": (_i32, [ctypes.POINTER(LoraC), _vp, _i32, _i64, _i32, _vp, _i32, _vp, _i32, _i64,
+                         _vp, _i32, _i64, _vp, _sz, _vp, _PP]),
     "exl3_decode_tiles": (_i32, [_vp, _i32, _i32, _vp, _vp, _PP]),
     "exl3_events_create": (_i32, [_i32, ctypes.POINTER(ctypes.c_void_p)]),
     "exl3_events_destroy": (_i32, [_i32, ctypes.POINTER(ctypes.c_void_p)]),
     "exl3_profile_read": (_i32, [_PP, ctypes.POINTER(ctypes.c_float)]),
 }
 KERNEL_NAMES = {1: "route_pack", 2: "rotate", 3: "gemm_gateup", 4: "gemm_down",
-                5: "combine", 6: "gemm_linear", 7: "decode_tiles", 8: "gemm_experts"}
+                5: "combine", 6: "gemm_linear", 7: "decode_tiles", 8: "gemm_experts",
+                9: "route_topk", 10: "balance", 11: "balance_sum", 12: "route_backward",
+                13: "lora_a", 14: "lora_b"}
 
 
 def lib():
@@ -289,6 +318,183 @@ def exl3_moe_additive(x, topk, meta, gate, up, down, capacity, out_dtype=torch.f
                                    ctypes.byref(g), ctypes.byref(u), ctypes.byref(d), _p(out),
                                    _DT[out.dtype], capacity, num_active_hint, _p(ws), ws.numel(), _stream(),
                                    _prof()))
+    return out
+
+
+# ------------------------------------------------------- router operators
+SCORING = {"softmax": 0, "sigmoid": 1}
+
+
+def _need(ok, what):
+    """Shape and layout checks that the C ABI, given bare pointers, cannot make."""
+    if not ok:
+        raise Exl3Error(what)
+
+
+def _matrix(t, rows, cols, name):
+    """Row distance of a [rows][cols] tensor whose rows are contiguous."""
+    _need(t.dim() == 2 and t.shape[0] == rows and t.shape[1] == cols,
+          "%s must be [%d, %d], got %s" % (name, rows, cols, list(t.shape)))
+    _need(cols == 1 or t.stride(1) == 1, "%s must have contiguous rows" % name)
+    return t.stride(0) if rows > 1 else cols
+
+
+def _vector(t, n, dtype, name):
+    _need(t.dtype == dtype and t.numel() == n and t.is_contiguous(),
+          "%s must be %d contiguous values of %s" % (name, n, dtype))
+
+
+def _pairs(t, rows, topk, name):
+    _need(t.dim() == 2 and t.shape[0] == rows and t.shape[1] == topk and t.is_contiguous(),
+          "%s must be contiguous [%d, %d], got %s" % (name, rows, topk, list(t.shape)))
+
+
+def _router_c(E, topk, scoring, renorm=True, scale=1.0, bias=None):
+    _need(scoring in SCORING, "scoring must be 'softmax' or 'sigmoid', got %r" % (scoring,))
+    return RouterC(E, topk, SCORING[scoring], 1 if renorm else 0, scale,
+                   None if bias is None else bias.data_ptr())
+
+
+def exl3_route_topk(logits, topk, scoring="softmax", renorm=True, scale=1.0, bias=None,
+                    row_mask=None, ids_dtype=torch.int32, w_dtype=torch.float32, ids=None, w=None):
+    """Router logits [rows, experts] -> (ids, w), both [rows, topk]: the topk
+    best experts of every row and their route weights, as exl3_moe_forward
+    takes them. ``bias`` (fp32 [experts]) moves the choice only; rows whose
+    ``row_mask`` (bool or uint8 [rows]) is 0 get ID -1 and weight 0."""
+    _need(logits.dim() == 2, "logits must be [rows, experts]")
+    rows, E = logits.shape
+    ld = _matrix(logits, rows, E, "logits")
+    if bias is not None:
+        _vector(bias, E, torch.float32, "bias")
+    if row_mask is not None:
+        _need(row_mask.dtype in (torch.bool, torch.uint8), "row_mask must be bool or uint8")
+        _vector(row_mask, rows, row_mask.dtype, "row_mask")
+    if ids is None:
+        ids = torch.empty(rows, topk, dtype=ids_dtype, device=logits.device)
+    if w is None:
+        w = torch.empty(rows, topk, dtype=w_dtype, device=logits.device)
+    _pairs(ids, rows, topk, "ids")
+    _pairs(w, rows, topk, "w")
+    rc = _router_c(E, topk, scoring, renorm, scale, bias)
+    _check(lib().exl3_route_topk(ctypes.byref(rc), _p(logits), _dt(logits), ld, rows,
+                                 _p(row_mask), _p(ids), _dt(ids), _p(w), _dt(w), _stream(),
+                                 _prof()))
+    return ids, w
+
+
+def alloc_balance(num_experts, device="cuda"):
+    return {
+        "count": torch.empty(num_experts, dtype=torch.int32, device=device),
+        "tokens": torch.empty(1, dtype=torch.int32, device=device),
+        "prob": torch.empty(num_experts, dtype=torch.float32, device=device),
+        "loss": torch.empty(1, dtype=torch.float32, device=device),
+    }
+
+
+def balance_workspace_size(rows, num_experts):
+    return lib().exl3_balance_workspace_size(rows, num_experts)
+
+
+def exl3_balance_loss(logits, ids, scoring="softmax", coef=1.0, balance=None, ws=None):
+    """Balance loss of a routing and its per-expert statistics: a dict with
+    "loss" [1], "count" [experts], "prob" [experts] and "tokens" [1]."""
+    _need(logits.dim() == 2 and ids.dim() == 2, "logits and ids must have two dimensions")
+    rows, E = logits.shape
+    ld = _matrix(logits, rows, E, "logits")
+    topk = ids.shape[1]
+    _pairs(ids, rows, topk, "ids")
+    if balance is None:
+        balance = alloc_balance(E, logits.device)
+    for n, size, dt in (("count", E, torch.int32), ("tokens", 1, torch.int32),
+                        ("prob", E, torch.float32), ("loss", 1, torch.float32)):
+        _vector(balance[n], size, dt, n)
+    if ws is None:
+        ws = torch.empty(max(balance_workspace_size(rows, E), 256), dtype=torch.uint8,
+                         device=logits.device)
+    rc = _router_c(E, topk, scoring)
+    bc = BalanceC(*[balance[n].data_ptr() for n in ("count", "tokens", "prob", "loss")])
+    _check(lib().exl3_balance_loss(ctypes.byref(rc), _p(logits), _dt(logits), ld, rows, _p(ids),
+                                   _dt(ids), coef, ctypes.byref(bc), _p(ws), ws.numel(),
+                                   _stream(), _prof()))
+    return balance
+
+
+def exl3_route_backward(logits, ids, dw=None, scoring="softmax", renorm=True, scale=1.0,
+                        balance=None, coef=1.0, dloss=None, dlogits_dtype=None, dlogits=None):
+    """Gradient with respect to the router's logits: of the route weights
+    (``dw`` [rows, topk]), of the balance loss (``balance`` as
+    exl3_balance_loss returned it, with ``dloss`` fp32 [1] or None for 1), or
+    of both together."""
+    _need(logits.dim() == 2 and ids.dim() == 2, "logits and ids must have two dimensions")
+    rows, E = logits.shape
+    ld = _matrix(logits, rows, E, "logits")
+    topk = ids.shape[1]
+    _pairs(ids, rows, topk, "ids")
+    if dw is not None:
+        _pairs(dw, rows, topk, "dw")
+    if dlogits is None:
+        dlogits = torch.empty(rows, E, dtype=dlogits_dtype or logits.dtype, device=logits.device)
+    ldd = _matrix(dlogits, rows, E, "dlogits")
+    bc = None
+    if balance is not None:
+        _vector(balance["count"], E, torch.int32, "count")
+        _vector(balance["tokens"], 1, torch.int32, "tokens")
+        if dloss is not None:
+            _vector(dloss, 1, torch.float32, "dloss")
+        bc = ctypes.byref(BalanceC(balance["count"].data_ptr(), balance["tokens"].data_ptr(),
+                                   None, None))
+    rc = _router_c(E, topk, scoring, renorm, scale)
+    _check(lib().exl3_route_backward(ctypes.byref(rc), _p(logits), _dt(logits), ld, rows, _p(ids),
+                                     _dt(ids), _p(dw), _dt(dw) if dw is not None else 0, bc, coef,
+                                     _p(dloss), _p(dlogits), _dt(dlogits), ldd, _stream(),
+                                     _prof()))
+    return dlogits
+
+
+def lora_workspace_size(rows, in_f, rank):
+    return lib().exl3_lora_workspace_size(rows, in_f, rank)
+
+
+def exl3_lora(x, a, b, ids, scale=None, ranks=None, base=None, out_dtype=None, out=None, ws=None):
+    """Low-rank adapters beside a shared projection: row t gets
+    ``base[t] + scale[i] * (x[t] @ a[i].T) @ b[i].T`` with i = ids[t], or
+    ``base[t]`` (zeros without a base) where ids[t] names no adapter.
+
+    x [rows, in], a [adapters, rank, in] and b [adapters, out, rank] share one
+    16-bit dtype; ``scale`` (fp32) and ``ranks`` (int32, the ranks in use) hold
+    one value per adapter. ``base`` and ``out`` [rows, out] may be column
+    slices of wider tensors; ``out=base`` adds in place. Without ``out`` the
+    result has ``out_dtype``, by default that of ``base`` or else of ``x``."""
+    _need(x.dim() == 2 and a.dim() == 3 and b.dim() == 3,
+          "x must have two dimensions, a and b three")
+    rows, K = x.shape
+    n, R, _ = a.shape
+    N = b.shape[1]
+    _need(a.shape[2] == K and tuple(b.shape) == (n, N, R),
+          "a must be [adapters, rank, in] and b [adapters, out, rank]")
+    _need(a.dtype == x.dtype and b.dtype == x.dtype, "x, a and b must share one dtype")
+    _need(a.is_contiguous() and b.is_contiguous(), "a and b must be contiguous")
+    _need(ids.dim() == 1 and ids.shape[0] == rows and ids.is_contiguous(),
+          "ids must be contiguous [%d]" % rows)
+    ldx = _matrix(x, rows, K, "x")
+    if scale is not None:
+        _vector(scale, n, torch.float32, "scale")
+    if ranks is not None:
+        _vector(ranks, n, torch.int32, "ranks")
+    ldb = _matrix(base, rows, N, "base") if base is not None else 0
+    if out is None:
+        out = torch.empty(rows, N, device=x.device,
+                          dtype=out_dtype or (base.dtype if base is not None else x.dtype))
+    ldo = _matrix(out, rows, N, "out")
+    if ws is None:
+        ws = torch.empty(max(lora_workspace_size(rows, K, R), 256), dtype=torch.uint8,
+                         device=x.device)
+    lc = LoraC(K, N, R, n, a.data_ptr(), b.data_ptr(),
+               None if scale is None else scale.data_ptr(),
+               None if ranks is None else ranks.data_ptr())
+    _check(lib().exl3_lora(ctypes.byref(lc), _p(x), _dt(x), ldx, rows, _p(ids), _dt(ids),
+                           _p(base), _dt(base) if base is not None else 0, ldb, _p(out), _dt(out),
+                           ldo, _p(ws), ws.numel(), _stream(), _prof()))
     return out
 
 
