@@ -935,7 +935,7 @@ RouterParams router_params(const exl3_router *r, const void *logits, int32_t log
 }
 
 struct BalanceLayout {
-  size_t count, tokens, total;  // the probabilities come first
+  size_t count, tokens, share, total;  // the probabilities come first
   int nblk;
 };
 BalanceLayout balance_layout(int32_t rows, int32_t E) {
@@ -943,7 +943,8 @@ BalanceLayout balance_layout(int32_t rows, int32_t E) {
   L.nblk = balance_blocks(rows);
   L.count = align_up(4 * (size_t)L.nblk * E);
   L.tokens = L.count + align_up(4 * (size_t)L.nblk * E);
-  L.total = L.tokens + align_up(4 * (size_t)L.nblk);
+  L.share = L.tokens + align_up(4 * (size_t)L.nblk);
+  L.total = L.share + align_up(4 * (size_t)((E + 15) / 16 + 1));
   return L;
 }
 
@@ -977,7 +978,7 @@ int32_t exl3_route_topk(const exl3_router *router, const void *logits, int32_t l
 
 size_t exl3_balance_workspace_size(int32_t rows, int32_t num_experts) {
   if (rows < 0 || num_experts < 1 || num_experts > EXL3_MAX_EXPERTS) return 0;
-  return std::max(kAlign, balance_layout(rows, num_experts).total);
+  return balance_layout(rows, num_experts).total;
 }
 
 int32_t exl3_balance_loss(const exl3_router *router, const void *logits, int32_t logits_dtype,
@@ -1008,12 +1009,14 @@ int32_t exl3_balance_loss(const exl3_router *router, const void *logits, int32_t
   p.part_prob = at<float>(ws, 0);
   p.part_count = at<int32_t>(ws, L.count);
   p.part_tokens = at<int32_t>(ws, L.tokens);
+  p.part_share = at<float>(ws, L.share);
+  p.part_arrived = at<int32_t>(ws, L.share) + (router->num_experts + 15) / 16;
   p.coef = coef;
   p.count = balance->count;
   p.tokens = balance->tokens;
   p.prob = balance->prob;
   p.loss = balance->loss;
-  if (rows > 0) {
+  {
     ProfScope ps(prof, st, EXL3_K_BALANCE);
     if (launch_balance(p, st) != hipSuccess) return EXL3_E_LAUNCH;
   }

@@ -137,6 +137,8 @@ struct RouterParams {
   float *part_prob;      // [nblk][E]
   int32_t *part_count;   // [nblk][E]
   int32_t *part_tokens;  // [nblk]
+  float *part_share;     // [E / 16, rounded up]: shares of the loss
+  int32_t *part_arrived;  // [1]: workgroups that wrote theirs
   int nblk;
   float coef;
   int32_t *count, *tokens;  // backward reads them (count null: no balance loss)

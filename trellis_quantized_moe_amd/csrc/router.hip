@@ -333,39 +333,78 @@ __global__ void __launch_bounds__(256) balance_kernel(RouterParams p) {
         (s_prob[0][e] + s_prob[1][e]) + (s_prob[2][e] + s_prob[3][e]);
     p.part_count[(int64_t)blockIdx.x * p.E + e] = s_count[e];
   }
-  if (threadIdx.x == 0) p.part_tokens[blockIdx.x] = s_tokens;
+  if (threadIdx.x == 0) {
+    p.part_tokens[blockIdx.x] = s_tokens;
+    if (blockIdx.x == 0) *p.part_arrived = 0;
+  }
 }
 
-// One workgroup: adds the partial sums and forms the loss.
-__global__ void __launch_bounds__(1024) balance_sum_kernel(RouterParams p) {
-  __shared__ float s_f[1024];
-  __shared__ int s_tokens;
+// Adds the partial sums and forms the loss. Workgroup b takes experts 16 b ..
+// 16 b + 15: 16 threads to an expert, each over every 16th partial sum, then
+// the 16 in order. The workgroup that arrives last (part_arrived, zeroed by
+// balance_kernel) adds the workgroups' shares of the loss in their order.
+// One workgroup for all experts took 66 us on 256 partial sums of 256 experts,
+// a chain of dependent loads; spread out, 6.6.
+__global__ void __launch_bounds__(256) balance_sum_kernel(RouterParams p) {
+  __shared__ float s_prob[16][17];
+  __shared__ int s_count[16][17];
+  __shared__ float s_share[16];
+  __shared__ int s_tokens, s_last;
+  const int c = threadIdx.x & 15, slice = threadIdx.x >> 4;
+  const int e = blockIdx.x * 16 + c;
   if (threadIdx.x == 0) s_tokens = 0;
   __syncthreads();
-  for (int b = threadIdx.x; b < p.nblk; b += 1024) atomicAdd(&s_tokens, p.part_tokens[b]);
-  __syncthreads();
-  const int T = s_tokens;
-  const int e = threadIdx.x;
   float prob = 0.0f;
-  int count = 0;
+  int count = 0, tokens = 0;
+  for (int b = threadIdx.x; b < p.nblk; b += 256) tokens += p.part_tokens[b];
   if (e < p.E) {
-    for (int b = 0; b < p.nblk; ++b) {
+#pragma unroll 8
+    for (int b = slice; b < p.nblk; b += 16) {
       prob += p.part_prob[(int64_t)b * p.E + e];
       count += p.part_count[(int64_t)b * p.E + e];
     }
+  }
+  if (tokens) atomicAdd(&s_tokens, tokens);
+  s_prob[slice][c] = prob;
+  s_count[slice][c] = count;
+  __syncthreads();
+  const int T = s_tokens;
+  if (threadIdx.x < 16) {
+    prob = 0.0f;
+    count = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      prob += s_prob[i][c];
+      count += s_count[i][c];
+    }
     prob = T > 0 ? prob / (float)T : 0.0f;
-    p.count[e] = count;
-    p.prob[e] = prob;
+    if (e < p.E) {
+      p.count[e] = count;
+      p.prob[e] = prob;
+    }
+    s_share[c] = T > 0 ? (float)count / ((float)T * (float)p.topk) * prob : 0.0f;
   }
-  const float pairs = (float)T * (float)p.topk;
-  s_f[e] = e < p.E && T > 0 ? (float)count / pairs * prob : 0.0f;
-  for (int d = 512; d > 0; d >>= 1) {
-    __syncthreads();
-    if (e < d) s_f[e] += s_f[e + d];
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    float share = 0.0f;
+    for (int i = 0; i < 16; ++i) share += s_share[i];
+    __hip_atomic_store(p.part_share + blockIdx.x, share, __ATOMIC_RELAXED,
+                       __HIP_MEMORY_SCOPE_AGENT);
+    s_last = __hip_atomic_fetch_add(p.part_arrived, 1, __ATOMIC_ACQ_REL,
+                                    __HIP_MEMORY_SCOPE_AGENT) == (int)gridDim.x - 1;
   }
-  if (e == 0) {
+  __syncthreads();
+  if (!s_last || threadIdx.x >= 64) return;
+  // at most 64 shares (1024 experts): one to a lane
+  float v = threadIdx.x < gridDim.x ? __hip_atomic_load(p.part_share + threadIdx.x,
+                                                        __ATOMIC_RELAXED,
+                                                        __HIP_MEMORY_SCOPE_AGENT)
+                                    : 0.0f;
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d, 64);
+  if (threadIdx.x == 0) {
     p.tokens[0] = T;
-    p.loss[0] = p.coef * (float)p.E * s_f[0];
+    p.loss[0] = p.coef * (float)p.E * v;
   }
 }
 
@@ -505,7 +544,7 @@ hipError_t launch_route_topk(const RouterParams &p, hipStream_t s) {
   });
 }
 
-int balance_blocks(int rows) { return rows > 0 ? (int)min(row_groups(rows), 256u) : 0; }
+int balance_blocks(int rows) { return (int)max(1u, min(row_groups(rows), 256u)); }
 
 hipError_t launch_balance(const RouterParams &p, hipStream_t s) {
   return by_blocks(p.E, [&](auto I) {
@@ -514,7 +553,7 @@ hipError_t launch_balance(const RouterParams &p, hipStream_t s) {
 }
 
 hipError_t launch_balance_sum(const RouterParams &p, hipStream_t s) {
-  hipLaunchKernelGGL(balance_sum_kernel, dim3(1), dim3(1024), 0, s, p);
+  hipLaunchKernelGGL(balance_sum_kernel, dim3((p.E + 15) / 16), dim3(256), 0, s, p);
   return hipGetLastError();
 }
 
