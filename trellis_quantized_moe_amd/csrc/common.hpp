@@ -389,6 +389,15 @@ __device__ __forceinline__ uint16_t f32_to_bf16_bits(float x) {
 __device__ __forceinline__ float bf16_bits_to_f32(uint16_t b) {
   return __builtin_bit_cast(float, (uint32_t)b << 16);
 }
+// Two of them in one dword, by the packed conversions (a NaN stays one; its
+// payload may differ from the scalar conversion's).
+__device__ __forceinline__ uint32_t f32x2_to_out16(float a, float b, int bf16) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  const f32x2 f = {a, b};
+  return bf16 ? __builtin_bit_cast(uint32_t, __builtin_convertvector(f, bf16x2))
+              : __builtin_bit_cast(uint32_t, __builtin_convertvector(f, f16x2));
+}
 // A 16-bit output value: bf16 or fp16, both round to nearest even.
 __device__ __forceinline__ uint16_t f32_to_out16(float x, int bf16) {
   return bf16 ? f32_to_bf16_bits(x) : f32_to_f16_bits(x);

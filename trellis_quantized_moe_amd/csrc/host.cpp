@@ -1064,6 +1064,7 @@ int32_t exl3_route_backward(const exl3_router *router, const void *logits, int32
   }
   p.dlogits = dlogits;
   p.dlogits_dtype = dlogits_dtype;
+  p.dvec4 = ld_dlogits % 4 == 0 && aligned_to(dlogits, 4 * float_size(dlogits_dtype));
   p.ld_dlogits = ld_dlogits;
   ProfScope ps(prof, (hipStream_t)stream, EXL3_K_ROUTE_BACKWARD);
   return launch_route_backward(p, (hipStream_t)stream) == hipSuccess ? EXL3_OK : EXL3_E_LAUNCH;

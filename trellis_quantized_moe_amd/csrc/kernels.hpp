@@ -149,6 +149,7 @@ struct RouterParams {
   const float *dloss;  // [1] or null (1)
   void *dlogits;
   int dlogits_dtype;
+  int dvec4;  // each group of four can be one store
   int64_t ld_dlogits;
 };
 

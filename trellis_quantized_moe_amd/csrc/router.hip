@@ -80,57 +80,64 @@ __device__ __forceinline__ int64_t load_id(const void *p, int i64, int64_t i) {
   return i64 ? ((const int64_t *)p)[i] : (int64_t)((const int32_t *)p)[i];
 }
 
-// The lane's logits of the row whose first element has index `at`. vec4:
+// The lane's share of a row as loaded: four fp32 or four 16-bit logits a block.
+template <int DT>
+struct Raw {
+  typedef uint2 type;
+};
+template <>
+struct Raw<3> {
+  typedef u32x4 type;
+};
+template <int I, int DT>
+using RawRow = typename Raw<DT>::type[I];
+
+// Loads of the row whose first element has index `at` (not waited for). vec4:
 // every group of four starts on a multiple of four elements and is one load; a
-// group that runs past E is read element by element. The type is tested once
-// around each loop, so all loads of a row are in flight together.
-template <int I>
-__device__ __forceinline__ void load_row(const RouterParams &p, int64_t at, int lane,
-                                         float (&l)[4 * I]) {
-  auto scalar = [&](int j) {
+// group that runs past E is read element by element, -inf behind the end.
+template <int I, int DT>
+__device__ __forceinline__ void load_raw(const RouterParams &p, int64_t at, int lane,
+                                         RawRow<I, DT> &raw) {
+  typedef typename Raw<DT>::type raw_t;
+  const raw_t *q = (const raw_t *)((const char *)p.logits + (at + 4 * lane) * (DT == 3 ? 4 : 2));
+#pragma unroll
+  for (int j = 0; j < I; ++j) {
     const int e0 = 64 * j + 4 * lane;
+    if (p.vec4 && (64 * (j + 1) <= p.E || e0 + 4 <= p.E)) {
+      raw[j] = q[16 * j];
+    } else if constexpr (DT == 3) {
 #pragma unroll
-    for (int v = 0; v < 4; ++v)
-      l[4 * j + v] =
-          e0 + v < p.E ? load_as_f32(p.logits, p.logits_dtype, at + e0 + v) : kNegInf;
-  };
-  if (p.vec4 && p.logits_dtype == 3) {
-    const float *q = (const float *)p.logits + at + 4 * lane;
+      for (int v = 0; v < 4; ++v)
+        raw[j][v] = e0 + v < p.E ? ((const uint32_t *)p.logits)[at + e0 + v] : 0xff800000u;
+    } else {
+      uint32_t w[4];
 #pragma unroll
-    for (int j = 0; j < I; ++j) {
-      if (64 * j + 4 * lane + 4 <= p.E) {
-        const f32x4 x = *(const f32x4 *)(q + 64 * j);
-#pragma unroll
-        for (int v = 0; v < 4; ++v) l[4 * j + v] = x[v];
-      } else {
-        scalar(j);
-      }
+      for (int v = 0; v < 4; ++v)
+        w[v] = e0 + v < p.E ? ((const uint16_t *)p.logits)[at + e0 + v]
+                            : DT == 2 ? 0xff80u : 0xfc00u;
+      raw[j] = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
     }
-  } else if (p.vec4) {
-    const uint16_t *q = (const uint16_t *)p.logits + at + 4 * lane;
-    uint2 x[I];
-#pragma unroll
-    for (int j = 0; j < I; ++j)
-      if (64 * j + 4 * lane + 4 <= p.E) x[j] = *(const uint2 *)(q + 64 * j);
-#pragma unroll
-    for (int j = 0; j < I; ++j) {
-      if (64 * j + 4 * lane + 4 <= p.E) {
-        const uint32_t w[2] = {x[j].x, x[j].y};
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const uint16_t b = (uint16_t)(w[v >> 1] >> (16 * (v & 1)));
-          l[4 * j + v] = p.logits_dtype == 2 ? bf16_bits_to_f32(b) : f16_bits_to_f32(b);
-        }
-      } else {
-        scalar(j);
-      }
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < I; ++j) scalar(j);
   }
+}
+template <int I, int DT>
+__device__ __forceinline__ void unpack_row(const RawRow<I, DT> &raw, float (&l)[4 * I]) {
 #pragma unroll
-  for (int j = 0; j < 4 * I; ++j) l[j] = clean(l[j]);
+  for (int j = 0; j < I; ++j) {
+    if constexpr (DT == 3) {
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const uint32_t b = raw[j][v];
+        l[4 * j + v] = clean(__builtin_bit_cast(float, b));
+      }
+    } else {
+      const uint32_t w[2] = {raw[j].x, raw[j].y};
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const uint16_t b = (uint16_t)(w[v >> 1] >> (16 * (v & 1)));
+        l[4 * j + v] = clean(DT == 2 ? bf16_bits_to_f32(b) : f16_bits_to_f32(b));
+      }
+    }
+  }
 }
 
 template <int N>
@@ -157,6 +164,33 @@ __device__ __forceinline__ float strength(bool sigmoid, float l, float m) {
   if (!sigmoid) return expf(l - m);
   const float z = expf(-fabsf(l));
   return (l < 0.0f ? expf(l - m) : 1.0f) / (1.0f + z);
+}
+// t of every expert of a row, for sums, probabilities and gradients: the
+// hardware's exp2 and reciprocal (1 ulp each) instead of the full functions.
+// (l - m) log2(e) is rounded once more than l - m is, so t is off by
+// 2 |l - m| 2^-24 rather than |l - m| 2^-24 at most; a t below 2^-126 counts
+// as 0. Chosen experts' weights, two to a lane, take strength().
+__device__ __forceinline__ float fast_exp(float x) {
+  return __builtin_amdgcn_exp2f(x * 1.44269504088896340736f);
+}
+template <int N>
+__device__ __forceinline__ void fast_strengths(bool sigmoid, const float (&l)[N], float m,
+                                               float (&t)[N]) {
+  if (!sigmoid) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) t[j] = fast_exp(l[j] - m);
+  } else if (!__any(m != 0.0f)) {  // no row of the wave lies below zero throughout
+#pragma unroll
+    for (int j = 0; j < N; ++j) t[j] = __builtin_amdgcn_rcpf(1.0f + fast_exp(-l[j]));
+  } else {
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      t[j] = fast_exp(fminf(l[j], 0.0f) - m) * __builtin_amdgcn_rcpf(1.0f + fast_exp(-fabsf(l[j])));
+  }
+}
+__device__ __forceinline__ float fast_slope(float l) {  // sigmoid
+  const float z = fast_exp(-fabsf(l));
+  return (l < 0.0f ? 1.0f : z) * __builtin_amdgcn_rcpf(1.0f + z);
 }
 // d log t / d l: 1, or 1 - sigmoid(l) computed without cancellation.
 __device__ __forceinline__ float slope(bool sigmoid, float l) {
@@ -185,7 +219,7 @@ struct Key<true> {
   typedef double type;
 };
 
-template <int I, bool BIAS>
+template <int I, int DT, bool BIAS>
 __global__ void __launch_bounds__(256) route_topk_kernel(RouterParams p) {
   typedef typename Key<BIAS>::type key_t;
   const int lane = threadIdx.x & 15;
@@ -193,8 +227,10 @@ __global__ void __launch_bounds__(256) route_topk_kernel(RouterParams p) {
   const bool in = row < p.rows;
   const bool live = in && (!p.row_mask || p.row_mask[row] != 0);
   const int64_t at = (live ? row : 0) * p.ld_logits;
+  RawRow<I, DT> raw;
+  load_raw<I, DT>(p, at, lane, raw);
   float l[4 * I];
-  load_row<I>(p, at, lane, l);
+  unpack_row<I, DT>(raw, l);
   if (!live) {
 #pragma unroll
     for (int j = 0; j < 4 * I; ++j) l[j] = kNegInf;
@@ -205,7 +241,7 @@ __global__ void __launch_bounds__(256) route_topk_kernel(RouterParams p) {
   float total = 0.0f;
   if (!sig && !p.renorm) {
 #pragma unroll
-    for (int j = 0; j < 4 * I; ++j) total += strength(false, l[j], m_all);
+    for (int j = 0; j < 4 * I; ++j) total += fast_exp(l[j] - m_all);
     total = row_sum(total);
   }
   key_t s[4 * I];
@@ -243,7 +279,7 @@ __global__ void __launch_bounds__(256) route_topk_kernel(RouterParams p) {
   float lp[2], t[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h)
-    lp[h] = pick[h] >= 0 ? clean(load_as_f32(p.logits, p.logits_dtype, at + pick[h])) : kNegInf;
+    lp[h] = pick[h] >= 0 ? clean(load_as_f32(p.logits, DT, at + pick[h])) : kNegInf;
   const float m = p.renorm ? shift(sig, row_max(fmaxf(lp[0], lp[1]))) : sig ? 0.0f : m_all;
 #pragma unroll
   for (int h = 0; h < 2; ++h) t[h] = pick[h] >= 0 ? strength(sig, lp[h], m) : 0.0f;
@@ -263,16 +299,23 @@ __global__ void __launch_bounds__(256) route_topk_kernel(RouterParams p) {
 }
 
 // The row's IDs j = lane and lane + 16: the expert, or -1 (none, outside
-// [0, E), or past the row's topk).
+// [0, E), or past the row's topk). At most 16 IDs leave the second one out.
 __device__ __forceinline__ void load_ids(const RouterParams &p, int64_t row, bool in, int lane,
                                          int (&id)[2]) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int k = lane + 16 * h;
     id[h] = -1;
+    if (h == 1 && p.topk <= 16) break;
     if (in && k < p.topk) {
-      const int64_t v = load_id(p.ids, p.ids_i64, row * p.topk + k);
-      if (v >= 0 && v < p.E) id[h] = (int)v;
+      const int64_t o = row * p.topk + k;
+      if (p.ids_i64) {
+        const int64_t v = ((const int64_t *)p.ids)[o];
+        id[h] = v >= 0 && v < p.E ? (int)v : -1;
+      } else {
+        const int v = ((const int32_t *)p.ids)[o];
+        id[h] = (uint32_t)v < (uint32_t)p.E ? v : -1;
+      }
     }
   }
 }
@@ -283,7 +326,8 @@ __device__ __forceinline__ void load_ids(const RouterParams &p, int64_t row, boo
 // go to part_prob[b][E], part_count[b][E] and part_tokens[b]; they are added
 // in the order of b by balance_sum_kernel, so the same call gives the same
 // bytes.
-template <int I>
+// The next rows' loads are under way while a row is summed up.
+template <int I, int DT>
 __global__ void __launch_bounds__(256) balance_kernel(RouterParams p) {
   __shared__ int s_count[64 * I];
   __shared__ float s_prob[4][64 * I];
@@ -296,30 +340,41 @@ __global__ void __launch_bounds__(256) balance_kernel(RouterParams p) {
 #pragma unroll
   for (int j = 0; j < 4 * I; ++j) acc[j] = 0.0f;
   const bool sig = p.sigmoid;
-  for (int64_t r0 = (int64_t)blockIdx.x * kRowsPerWg; r0 < p.rows;
-       r0 += (int64_t)gridDim.x * kRowsPerWg) {
-    const int64_t row = r0 + (threadIdx.x >> 4);
-    const bool in = row < p.rows;
-    int id[2];
-    load_ids(p, row, in, lane, id);
+  int tokens = 0;
+  int64_t row = (int64_t)blockIdx.x * kRowsPerWg + (threadIdx.x >> 4);
+  const int64_t step = (int64_t)gridDim.x * kRowsPerWg;
+  const int64_t last = p.rows - 1;
+  int next_id[2];
+  RawRow<I, DT> next;
+  if (last >= 0) {
+    load_ids(p, row, row <= last, lane, next_id);
+    load_raw<I, DT>(p, min(row, last) * p.ld_logits, lane, next);
+  }
+  for (int64_t r0 = (int64_t)blockIdx.x * kRowsPerWg; r0 <= last; r0 += step, row += step) {
+    int id[2] = {next_id[0], next_id[1]};
     float l[4 * I];
-    load_row<I>(p, (in ? row : 0) * p.ld_logits, lane, l);
+    unpack_row<I, DT>(next, l);
+    if (r0 + step <= last) {
+      load_ids(p, row + step, row + step <= last, lane, next_id);
+      load_raw<I, DT>(p, min(row + step, last) * p.ld_logits, lane, next);
+    }
     const bool live = row_any(id[0] >= 0 || id[1] >= 0);
     const float m = shift(sig, row_max(max_of(l)));
     float t[4 * I], sum = 0.0f;
+    fast_strengths(sig, l, m, t);
 #pragma unroll
-    for (int j = 0; j < 4 * I; ++j) {
-      t[j] = strength(sig, l[j], m);
-      sum += t[j];
-    }
+    for (int j = 0; j < 4 * I; ++j) sum += t[j];
     const float inv = live ? inv_or_0(row_sum(sum)) : 0.0f;
 #pragma unroll
     for (int j = 0; j < 4 * I; ++j) acc[j] += t[j] * inv;
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < 2; ++h) {
+      if (h == 1 && p.topk <= 16) break;
       if (id[h] >= 0) atomicAdd(&s_count[id[h]], 1);
-    if (lane == 0 && live) atomicAdd(&s_tokens, 1);
+    }
+    tokens += live ? 1 : 0;
   }
+  if (lane == 0 && tokens) atomicAdd(&s_tokens, tokens);
   // the wave's four rows, then the four waves
 #pragma unroll
   for (int j = 0; j < 4 * I; ++j) {
@@ -416,68 +471,19 @@ __global__ void __launch_bounds__(256) balance_sum_kernel(RouterParams p) {
 //            sigmoid        dl_e = scale t_e h_e g_e
 //   balance  dl_e = c p_e h_e (f_e - sum f p),  c = dloss coef E / T
 // (h = slope, g = 0 where not chosen). Both in one pass over the row.
-template <int I>
+//
+// The chosen entries reach the lanes that hold their experts through LDS, one
+// [E] row per 16 lanes, zeroed and filled by the row's own lanes (LDS
+// operations of a wave stay in order, so no barrier is needed). Comparing
+// every chosen expert with every lane's experts took 24 of 45 instructions
+// per logit and 28 us on 32768 x 256, against 9.
+template <int I, int DT>
 __global__ void __launch_bounds__(256) route_backward_kernel(RouterParams p) {
+  __shared__ __align__(16) float s_add[kRowsPerWg][64 * I];
   const int lane = threadIdx.x & 15;
-  const int64_t row = (int64_t)blockIdx.x * kRowsPerWg + (threadIdx.x >> 4);
-  const bool in = row < p.rows;
-  int id[2];
-  load_ids(p, row, in, lane, id);
-  const int64_t at = (in ? row : 0) * p.ld_logits;
-  float l[4 * I];
-  load_row<I>(p, at, lane, l);
   const bool sig = p.sigmoid;
-  const bool live = row_any(id[0] >= 0 || id[1] >= 0);
-
-  // the chosen entries: logit, strength, weight gradient
-  float lp[2], g[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const bool ok = id[h] >= 0;
-    lp[h] = ok ? clean(load_as_f32(p.logits, p.logits_dtype, at + id[h])) : kNegInf;
-    g[h] = ok && p.dw ? load_as_f32(p.dw, p.dw_dtype, row * p.topk + lane + 16 * h) : 0.0f;
-    if (lp[h] == kNegInf) g[h] = 0.0f;  // an expert that takes no part
-  }
-  const float m = shift(sig, row_max(max_of(l)));
-  const bool need_all = p.count != nullptr || (!sig && !p.renorm);
-  float pe[4 * I], total = 0.0f;  // p_e
-#pragma unroll
-  for (int j = 0; j < 4 * I; ++j) pe[j] = 0.0f;
-  if (need_all) {
-#pragma unroll
-    for (int j = 0; j < 4 * I; ++j) {
-      pe[j] = strength(sig, l[j], m);
-      total += pe[j];
-    }
-  }
-  const float inv = inv_or_0(row_sum(total));
-#pragma unroll
-  for (int j = 0; j < 4 * I; ++j) pe[j] *= inv;
-
-  // v: what each chosen entry adds to its expert's gradient
-  float v[2], common = 0.0f;  // softmax over all: dl_e -= p_e * common
-  if (p.renorm) {
-    const float mc = shift(sig, row_max(fmaxf(lp[0], lp[1])));
-    float q[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) q[h] = strength(sig, lp[h], mc);
-    const float iq = inv_or_0(row_sum(q[0] + q[1]));
-    const float mean = row_sum(q[0] * g[0] + q[1] * g[1]) * iq;
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      v[h] = lp[h] > kNegInf ? p.scale * (q[h] * iq) * slope(sig, lp[h]) * (g[h] - mean) : 0.0f;
-  } else if (sig) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      v[h] = p.scale * strength(true, lp[h], 0.0f) * slope(true, lp[h]) * g[h];
-  } else {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) v[h] = p.scale * (strength(false, lp[h], m) * inv) * g[h];
-    common = row_sum(v[0] + v[1]);
-  }
-
-  // the balance loss: c f_e and c sum f p
-  float cf[4 * I], cmean = 0.0f;
+  // the balance loss: c f_e
+  float cf[4 * I];
 #pragma unroll
   for (int j = 0; j < 4 * I; ++j) cf[j] = 0.0f;
   if (p.count) {
@@ -488,45 +494,180 @@ __global__ void __launch_bounds__(256) route_backward_kernel(RouterParams p) {
     for (int j = 0; j < 4 * I; ++j) {
       const int e = 64 * (j >> 2) + 4 * lane + (j & 3);
       cf[j] = e < p.E ? cn * (float)p.count[e] : 0.0f;
-      cmean += cf[j] * pe[j];
     }
-    cmean = row_sum(cmean);
   }
-  float d[4 * I];
+  const bool need_all = p.count != nullptr || (!sig && !p.renorm);
+  const bool two = p.topk > 16;  // else no lane has a second entry
+  float *add = s_add[threadIdx.x >> 4];
+
+  int64_t row = (int64_t)blockIdx.x * kRowsPerWg + (threadIdx.x >> 4);
+  const int64_t step = (int64_t)gridDim.x * kRowsPerWg;
+  const int64_t last = p.rows - 1;
+  // the next rows' loads are under way while a row is worked on
+  int next_id[2];
+  float next_g[2];
+  RawRow<I, DT> next;
+  auto fetch = [&](int64_t r) {
+    load_ids(p, r, r <= last, lane, next_id);
 #pragma unroll
-  for (int j = 0; j < 4 * I; ++j) d[j] = pe[j] * (slope(sig, l[j]) * (cf[j] - cmean) - common);
-  // the chosen entries in the order of the row's IDs
-  for (int k = 0; k < p.topk; ++k) {
-    const int src = (threadIdx.x & 48) | (k & 15);
-    const int e = __shfl(k < 16 ? id[0] : id[1], src, 64);
-    const float a = __shfl(k < 16 ? v[0] : v[1], src, 64);
+    for (int h = 0; h < 2; ++h) {
+      next_g[h] = 0.0f;
+      if (h == 1 && !two) break;
+      if (p.dw && r <= last && lane + 16 * h < p.topk)
+        next_g[h] = load_as_f32(p.dw, p.dw_dtype, r * p.topk + lane + 16 * h);
+    }
+    load_raw<I, DT>(p, min(r, last) * p.ld_logits, lane, next);
+  };
+  fetch(row);
+  for (int64_t r0 = (int64_t)blockIdx.x * kRowsPerWg; r0 <= last; r0 += step, row += step) {
+    int id[2] = {next_id[0], next_id[1]};
+    float g[2] = {next_g[0], next_g[1]};
+    float l[4 * I];
+    unpack_row<I, DT>(next, l);
+    if (r0 + step <= last) fetch(row + step);
+    const bool live = row_any(id[0] >= 0 || id[1] >= 0);
+    const float m = shift(sig, row_max(max_of(l)));
+    float pe[4 * I], inv = 0.0f;  // p_e
+    float mean = 0.0f;  // c sum f p, and for softmax over all experts scale sum p g
+    if (need_all) {
+      float total = 0.0f;
+      fast_strengths(sig, l, m, pe);
 #pragma unroll
-    for (int j = 0; j < 4 * I; ++j)
-      d[j] += 64 * (j >> 2) + 4 * lane + (j & 3) == e ? a : 0.0f;
-  }
-  if (!in) return;
-  const int64_t to = row * p.ld_dlogits;
+      for (int j = 0; j < 4 * I; ++j) total += pe[j];
+      inv = live ? inv_or_0(row_sum(total)) : 0.0f;
 #pragma unroll
-  for (int j = 0; j < 4 * I; ++j) {
-    const int e = 64 * (j >> 2) + 4 * lane + (j & 3);
-    // a row or an expert that takes no part has gradient 0
-    if (e < p.E)
-      store_as(p.dlogits, p.dlogits_dtype, to + e, live && l[j] > kNegInf ? d[j] : 0.0f);
+      for (int j = 0; j < 4 * I; ++j) {
+        pe[j] *= inv;
+        mean += cf[j] * pe[j];
+      }
+      mean = row_sum(mean);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4 * I; ++j) pe[j] = 0.0f;
+    }
+
+    if (p.dw) {
+      // the chosen entries: logit (from the lane that holds it), strength,
+      // gradient; v: what each adds to its expert's gradient
+#pragma unroll
+      for (int j = 0; j < I; ++j)
+        *(f32x4 *)(add + 64 * j + 4 * lane) =
+            (f32x4){l[4 * j], l[4 * j + 1], l[4 * j + 2], l[4 * j + 3]};
+      float lp[2], v[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        lp[h] = kNegInf;
+        v[h] = 0.0f;
+        if (h == 1 && !two) break;
+        if (id[h] >= 0) lp[h] = add[id[h]];
+        if (lp[h] == kNegInf) g[h] = 0.0f;  // an expert that takes no part
+      }
+#pragma unroll
+      for (int j = 0; j < I; ++j)
+        *(f32x4 *)(add + 64 * j + 4 * lane) = (f32x4){0.f, 0.f, 0.f, 0.f};
+      if (p.renorm) {
+        const float mc = shift(sig, row_max(fmaxf(lp[0], lp[1])));
+        float q[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (h == 1 && !two) break;
+          q[h] = strength(sig, lp[h], mc);
+        }
+        const float iq = inv_or_0(row_sum(q[0] + q[1]));
+        const float gm = row_sum(q[0] * g[0] + q[1] * g[1]) * iq;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (h == 1 && !two) break;
+          if (lp[h] > kNegInf) v[h] = p.scale * (q[h] * iq) * slope(sig, lp[h]) * (g[h] - gm);
+        }
+      } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (h == 1 && !two) break;
+          v[h] = p.scale * g[h] *
+                 (sig ? strength(true, lp[h], 0.0f) * slope(true, lp[h]) : fast_exp(lp[h] - m) * inv);
+        }
+        if (!sig) mean += row_sum(v[0] + v[1]);
+      }
+      // an expert named twice: its entry holds the tag of only one of them
+      bool twice = false;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (h == 1 && !two) break;
+        if (id[h] >= 0) add[id[h]] = (float)(lane + 16 * h);
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (h == 1 && !two) break;
+        if (id[h] >= 0) twice |= add[id[h]] != (float)(lane + 16 * h);
+      }
+      if (!__any(twice)) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (h == 1 && !two) break;
+          if (id[h] >= 0) add[id[h]] = v[h];
+        }
+      } else {  // one entry after the other, in the order of the row's IDs
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (id[h] >= 0) add[id[h]] = 0.0f;
+        for (int k = 0; k < p.topk; ++k) {
+          const int i = k < 16 ? id[0] : id[1];
+          const float a = k < 16 ? v[0] : v[1];
+          if ((k & 15) == lane && i >= 0) add[i] += a;
+        }
+      }
+    }
+
+    // A row or an expert that takes no part has gradient 0: its p and its
+    // added value are 0, so only a row whose mean is not finite needs to look.
+    const bool odd = __any(!(fabsf(mean) < __builtin_inff()));
+    if (row > last) continue;
+    const int64_t to = row * p.ld_dlogits;
+#pragma unroll
+    for (int j = 0; j < I; ++j) {
+      const int e0 = 64 * j + 4 * lane;
+      f32x4 d = {0.f, 0.f, 0.f, 0.f};
+      if (p.dw) d = *(const f32x4 *)(add + e0);
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const float x = cf[4 * j + v] - mean;
+        d[v] += pe[4 * j + v] * (sig ? fast_slope(l[4 * j + v]) * x : x);
+        if (odd && (!live || l[4 * j + v] == kNegInf)) d[v] = 0.0f;
+      }
+      if (p.dvec4 && e0 + 4 <= p.E) {
+        if (p.dlogits_dtype == 3)
+          *(f32x4 *)((float *)p.dlogits + to + e0) = d;
+        else
+          *(uint2 *)((uint16_t *)p.dlogits + to + e0) =
+              make_uint2(f32x2_to_out16(d[0], d[1], p.dlogits_dtype == 2),
+                         f32x2_to_out16(d[2], d[3], p.dlogits_dtype == 2));
+      } else {
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          if (e0 + v < p.E) store_as(p.dlogits, p.dlogits_dtype, to + e0 + v, d[v]);
+      }
+    }
   }
 }
 
-// Blocks of 64 experts a kernel instance holds per row.
+// f(blocks of 64 experts a kernel instance holds per row, logit type)
 template <typename F>
-hipError_t by_blocks(int E, F f) {
-  const int blocks = (E + 63) / 64;
-  if (blocks <= 1) f(std::integral_constant<int, 1>());
-  else if (blocks <= 2) f(std::integral_constant<int, 2>());
-  else if (blocks <= 3) f(std::integral_constant<int, 3>());
-  else if (blocks <= 4) f(std::integral_constant<int, 4>());
-  else if (blocks <= 8) f(std::integral_constant<int, 8>());
-  else if (blocks <= 16) f(std::integral_constant<int, 16>());
-  else return hipErrorInvalidValue;
-  return hipGetLastError();
+hipError_t by_row(const RouterParams &p, F f) {
+  auto typed = [&](auto I) {
+    if (p.logits_dtype == 1) f(I, std::integral_constant<int, 1>());
+    else if (p.logits_dtype == 2) f(I, std::integral_constant<int, 2>());
+    else f(I, std::integral_constant<int, 3>());
+    return hipGetLastError();
+  };
+  const int blocks = (p.E + 63) / 64;
+  if (blocks <= 1) return typed(std::integral_constant<int, 1>());
+  if (blocks <= 2) return typed(std::integral_constant<int, 2>());
+  if (blocks <= 3) return typed(std::integral_constant<int, 3>());
+  if (blocks <= 4) return typed(std::integral_constant<int, 4>());
+  if (blocks <= 8) return typed(std::integral_constant<int, 8>());
+  if (blocks <= 16) return typed(std::integral_constant<int, 16>());
+  return hipErrorInvalidValue;
 }
 
 unsigned row_groups(int rows) { return (unsigned)((rows + kRowsPerWg - 1) / kRowsPerWg); }
@@ -534,21 +675,20 @@ unsigned row_groups(int rows) { return (unsigned)((rows + kRowsPerWg - 1) / kRow
 }  // namespace
 
 hipError_t launch_route_topk(const RouterParams &p, hipStream_t s) {
-  return by_blocks(p.E, [&](auto I) {
-    if (p.bias)
-      hipLaunchKernelGGL((route_topk_kernel<decltype(I)::value, true>), dim3(row_groups(p.rows)),
-                         dim3(256), 0, s, p);
-    else
-      hipLaunchKernelGGL((route_topk_kernel<decltype(I)::value, false>), dim3(row_groups(p.rows)),
-                         dim3(256), 0, s, p);
+  return by_row(p, [&](auto I, auto D) {
+    constexpr int i = decltype(I)::value, d = decltype(D)::value;
+    const dim3 grid(row_groups(p.rows));
+    if (p.bias) hipLaunchKernelGGL((route_topk_kernel<i, d, true>), grid, dim3(256), 0, s, p);
+    else hipLaunchKernelGGL((route_topk_kernel<i, d, false>), grid, dim3(256), 0, s, p);
   });
 }
 
-int balance_blocks(int rows) { return (int)max(1u, min(row_groups(rows), 256u)); }
+int balance_blocks(int rows) { return (int)max(1u, min(row_groups(rows), 512u)); }
 
 hipError_t launch_balance(const RouterParams &p, hipStream_t s) {
-  return by_blocks(p.E, [&](auto I) {
-    hipLaunchKernelGGL((balance_kernel<decltype(I)::value>), dim3(p.nblk), dim3(256), 0, s, p);
+  return by_row(p, [&](auto I, auto D) {
+    hipLaunchKernelGGL((balance_kernel<decltype(I)::value, decltype(D)::value>), dim3(p.nblk),
+                       dim3(256), 0, s, p);
   });
 }
 
@@ -558,9 +698,9 @@ hipError_t launch_balance_sum(const RouterParams &p, hipStream_t s) {
 }
 
 hipError_t launch_route_backward(const RouterParams &p, hipStream_t s) {
-  return by_blocks(p.E, [&](auto I) {
-    hipLaunchKernelGGL((route_backward_kernel<decltype(I)::value>), dim3(row_groups(p.rows)),
-                       dim3(256), 0, s, p);
+  return by_row(p, [&](auto I, auto D) {
+    hipLaunchKernelGGL((route_backward_kernel<decltype(I)::value, decltype(D)::value>),
+                       dim3(min(row_groups(p.rows), 1024u)), dim3(256), 0, s, p);
   });
 }
 
