@@ -428,11 +428,12 @@ typedef struct exl3_lora_adapters {
  * [rows][N] fp16, bf16 or fp32, ld_out apart. x, base, out: 16-byte aligned,
  * their row distances at least a row and a multiple of 16 bytes. out may be
  * base itself (same dtype and row distance), otherwise it overlaps no input.
- * ws: exl3_lora_workspace_size(rows, in_features, rank) bytes, 16-byte
- * aligned (the inner products); calls that share it must be ordered on one
- * stream.
+ * ws: exl3_lora_workspace_size(rows, in_features, rank, num_adapters) bytes,
+ * 16-byte aligned (the inner products and the row tiles); calls that share it
+ * must be ordered on one stream.
  */
-size_t exl3_lora_workspace_size(int32_t rows, int32_t in_features, int32_t rank);
+size_t exl3_lora_workspace_size(int32_t rows, int32_t in_features, int32_t rank,
+                                int32_t num_adapters);
 int32_t exl3_lora(const exl3_lora_adapters *adapters, const uint16_t *x, int32_t x_dtype,
                   int64_t ld_x, int32_t rows, const void *ids, int32_t ids_dtype,
                   const void *base, int32_t base_dtype, int64_t ld_base, void *out,

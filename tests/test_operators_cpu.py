@@ -206,11 +206,13 @@ def test_operator_workspace_sizes():
     assert L.exl3_balance_workspace_size(-1, 8) == 0
     assert L.exl3_balance_workspace_size(8, 1025) == 0
     assert L.exl3_balance_workspace_size(0, 8) >= 256
-    assert L.exl3_lora_workspace_size(7, 0, 8) == 0
-    assert L.exl3_lora_workspace_size(7, 4096, 129) == 0
-    assert L.exl3_lora_workspace_size(7, 4096, 9) >= 7 * 9 * 4
+    assert L.exl3_lora_workspace_size(7, 0, 8, 1) == 0
+    assert L.exl3_lora_workspace_size(7, 4096, 129, 1) == 0
+    assert L.exl3_lora_workspace_size(7, 4096, 8, 0) == 0
+    assert L.exl3_lora_workspace_size((1 << 26) + 1, 4096, 8, 1) == 0
+    assert L.exl3_lora_workspace_size(7, 4096, 9, 3) >= 7 * 9 * 4
     # 64-bit sizes: no overflow at the largest call
-    assert L.exl3_lora_workspace_size(1 << 26, 65536, 128) >= (1 << 26) * 128 * 4
+    assert L.exl3_lora_workspace_size(1 << 26, 65536, 128, 1024) >= (1 << 26) * 128 * 4
 
 
 def test_binding_refuses_wrong_shapes_and_layouts():

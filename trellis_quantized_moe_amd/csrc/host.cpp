@@ -1071,12 +1071,15 @@ int32_t exl3_route_backward(const exl3_router *router, const void *logits, int32
 }
 
 // ---------------------------------------------------------------- adapters
-size_t exl3_lora_workspace_size(int32_t rows, int32_t in_features, int32_t rank) {
-  if (rows < 0 || in_features < 1 || in_features > EXL3_MAX_FEATURES || rank < 1 ||
-      rank > EXL3_MAX_RANK)
+size_t exl3_lora_workspace_size(int32_t rows, int32_t in_features, int32_t rank,
+                                int32_t num_adapters) {
+  if (rows < 1 || rows > EXL3_LORA_MAX_ROWS || in_features < 1 ||
+      in_features > EXL3_MAX_FEATURES || rank < 1 || rank > EXL3_MAX_RANK || num_adapters < 1 ||
+      num_adapters > EXL3_MAX_ADAPTERS)
     return 0;
-  return std::max(kAlign, 4 * (size_t)lora_groups(in_features) * (size_t)rows *
-                              (size_t)lora_padded_rank(rank));
+  return align_up(4 * (size_t)lora_groups(in_features) * (size_t)rows *
+                  (size_t)lora_padded_rank(rank)) +
+         align_up(sizeof(LoraTile) * lora_tiles(rows, num_adapters));
 }
 
 int32_t exl3_lora(const exl3_lora_adapters *ad, const uint16_t *x, int32_t x_dtype, int64_t ld_x,
@@ -1106,7 +1109,7 @@ int32_t exl3_lora(const exl3_lora_adapters *ad, const uint16_t *x, int32_t x_dty
   if (!aligned_to(ids, ids_align(ids_dtype)) || !aligned_to(ad->scale, 4) ||
       !aligned_to(ad->ranks, 4))
     return EXL3_E_ALIGN;
-  if (ws_bytes < exl3_lora_workspace_size(rows, ad->in_features, ad->rank))
+  if (ws_bytes < exl3_lora_workspace_size(rows, ad->in_features, ad->rank, ad->num_adapters))
     return EXL3_E_WORKSPACE;
   for (const void *q : {(const void *)ad->a, (const void *)ad->b, (const void *)ad->scale,
                         (const void *)ad->ranks, (const void *)x, ids, base, (const void *)out,
@@ -1136,6 +1139,8 @@ int32_t exl3_lora(const exl3_lora_adapters *ad, const uint16_t *x, int32_t x_dty
   p.out_dtype = out_dtype;
   p.ldout = ld_out;
   p.part = (float *)ws;
+  p.tiles = at<LoraTile>(ws, align_up(4 * (size_t)lora_groups(p.K) * (size_t)rows *
+                                      (size_t)lora_padded_rank(p.R)));
   {
     ProfScope ps(prof, st, EXL3_K_LORA_A);
     if (launch_lora_a(p, st) != hipSuccess) return EXL3_E_LAUNCH;

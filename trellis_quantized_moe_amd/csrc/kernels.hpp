@@ -154,6 +154,11 @@ struct RouterParams {
 };
 
 // Low-rank adapters (lora.hip).
+struct LoraTile {  // up to 64 rows of one adapter
+  int32_t adapter;   // = LoraParams::adapters: rows without one; -1: no tile
+  int32_t nrows;
+  int32_t rows[64];  // entries past nrows repeat the last row
+};
 struct LoraParams {
   int K, N, R, adapters;
   const uint16_t *a, *b;  // [adapters][R][K], [adapters][N][R]
@@ -172,6 +177,7 @@ struct LoraParams {
   int out_dtype;
   int64_t ldout;
   float *part;  // x A^T: [lora_groups(K)][rows][lora_padded_rank(R)]
+  LoraTile *tiles;  // [lora_tiles(rows, adapters)]
 };
 
 hipError_t launch_gemm(int epi, const GemmParams &p, int tiles, int nblocks,
@@ -216,6 +222,7 @@ hipError_t launch_balance_sum(const RouterParams &p, hipStream_t s);
 hipError_t launch_route_backward(const RouterParams &p, hipStream_t s);
 int lora_groups(int K);
 int lora_padded_rank(int R);
+size_t lora_tiles(int rows, int adapters);
 hipError_t launch_lora_a(const LoraParams &p, hipStream_t s);
 hipError_t launch_lora_b(const LoraParams &p, hipStream_t s);
 

@@ -3,12 +3,13 @@
 // in two launches. lora_a writes s = x A^T (fp32, R values a row) to the
 // workspace; lora_b multiplies s by B^T, adds the base and stores.
 //
-// Tiles. A tile is up to 64 rows of one adapter. Every workgroup finds its
-// tile by itself: rows are taken in windows of 2048, and the workgroup counts
-// its window's IDs per adapter, scans the tile counts and collects its rows
-// (plan_tile). No launch and no table go before the products, and rows need
-// not be sorted. Rows without an adapter are one more bucket, whose tiles
-// lora_b copies.
+// Tiles. A tile is up to 64 rows of one adapter. Every workgroup of lora_a
+// finds its tile by itself: rows are taken in windows of 2048, and the
+// workgroup counts its window's IDs per adapter, scans the tile counts and
+// collects its rows (plan_tile), so that no planning launch goes before it and
+// rows need not be sorted. The first workgroup of a tile leaves it in the
+// workspace for lora_b. Rows without an adapter are one more bucket, whose
+// tiles lora_b copies.
 //
 // A row's bytes depend on that row alone: the K axis is cut the same way in
 // every call (512 inputs to a wave, four waves to a group, groups in
@@ -49,16 +50,27 @@ __device__ __forceinline__ int plan_tile(const LoraParams &p, int win, int tile,
   const int row0 = win * kWindow;
   const int n = min(p.rows - row0, kWindow);
   const int chunks = (n + 255) >> 8;
+  // lanes past the window read its last ID and drop it: loads without a branch
+  // around them are all in flight together
   int a[kWindow / 256];
+  if (p.ids_i64) {
+    int64_t id[kWindow / 256];
 #pragma unroll
-  for (int i = 0; i < kWindow / 256; ++i) {
-    a[i] = -1;
-    if (i * 256 + tid < n) {
-      const int64_t id = p.ids_i64 ? ((const int64_t *)p.ids)[row0 + i * 256 + tid]
-                                   : (int64_t)((const int32_t *)p.ids)[row0 + i * 256 + tid];
-      a[i] = id >= 0 && id < p.adapters ? (int)id : p.adapters;
-    }
+    for (int i = 0; i < kWindow / 256; ++i)
+      id[i] = ((const int64_t *)p.ids)[row0 + min(i * 256 + tid, n - 1)];
+#pragma unroll
+    for (int i = 0; i < kWindow / 256; ++i)
+      a[i] = id[i] >= 0 && id[i] < p.adapters ? (int)id[i] : p.adapters;
+  } else {
+#pragma unroll
+    for (int i = 0; i < kWindow / 256; ++i)
+      a[i] = ((const int32_t *)p.ids)[row0 + min(i * 256 + tid, n - 1)];
+#pragma unroll
+    for (int i = 0; i < kWindow / 256; ++i)
+      a[i] = (uint32_t)a[i] < (uint32_t)p.adapters ? a[i] : p.adapters;
   }
+#pragma unroll
+  for (int i = 0; i < kWindow / 256; ++i) a[i] = i * 256 + tid < n ? a[i] : -1;
   for (int b = tid; b <= p.adapters; b += 256) L.count[b] = 0;
   if (tid == 0) L.found[0] = -1;
   __syncthreads();
@@ -171,31 +183,62 @@ __device__ __forceinline__ void lora_a_tile(const LoraParams &p, const PlanLds &
 #pragma unroll
     for (int i = 0; i < RT; ++i)
       pa[i] = p.a + ((int64_t)ad * p.R + min(r0 + i * 16 + c, ra - 1)) * p.K + 8 * g;
+    // kStep K steps of 32 inputs are loaded while the kStep before them go
+    // through the matrix units
+    constexpr int kStep = TT + RT <= 5 ? 4 : 2;
+    u32x4 x[2][kStep][TT], a[2][kStep][RT];
+    auto fetch = [&](int buf, int k) {
+#pragma unroll
+      for (int u = 0; u < kStep; ++u) {
+#pragma unroll
+        for (int j = 0; j < TT; ++j) x[buf][u][j] = *(gu32x4p)(uintptr_t)(px[j] + k + 32 * u);
+#pragma unroll
+        for (int i = 0; i < RT; ++i) a[buf][u][i] = *(gu32x4p)(uintptr_t)(pa[i] + k + 32 * u);
+      }
+    };
+    auto multiply = [&](int buf) {
+#pragma unroll
+      for (int u = 0; u < kStep; ++u)
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+          for (int j = 0; j < TT; ++j)
+            acc[i][j] = mfma16<BF16>(a[buf][u][i], x[buf][u][j], acc[i][j]);
+    };
     int k = k0;
-#pragma unroll 4
-    for (; k + 32 <= k1; k += 32) {
-      u32x4 x[TT], a[RT];
+    if (k1 - k0 == kSlice) {
+      fetch(0, k0);
 #pragma unroll
-      for (int j = 0; j < TT; ++j) x[j] = *(gu32x4p)(uintptr_t)(px[j] + k);
+      for (int n = 0; n < kSlice / (32 * kStep); ++n) {
+        if (n + 1 < kSlice / (32 * kStep)) fetch((n + 1) & 1, k0 + (n + 1) * 32 * kStep);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(n & 1);
+      }
+      k = k1;
+    }
+    for (; k + 32 <= k1; k += 32) {  // the last slice of a K that is no multiple of kSlice
+      u32x4 xs[TT], as[RT];
 #pragma unroll
-      for (int i = 0; i < RT; ++i) a[i] = *(gu32x4p)(uintptr_t)(pa[i] + k);
+      for (int j = 0; j < TT; ++j) xs[j] = *(gu32x4p)(uintptr_t)(px[j] + k);
+#pragma unroll
+      for (int i = 0; i < RT; ++i) as[i] = *(gu32x4p)(uintptr_t)(pa[i] + k);
 #pragma unroll
       for (int i = 0; i < RT; ++i)
 #pragma unroll
-        for (int j = 0; j < TT; ++j) acc[i][j] = mfma16<BF16>(a[i], x[j], acc[i][j]);
+        for (int j = 0; j < TT; ++j) acc[i][j] = mfma16<BF16>(as[i], xs[j], acc[i][j]);
     }
     if (k < k1) {  // K is a multiple of 8: a lane's eight inputs are all there or none is
       const bool ok = k + 8 * g < k1;
       const u32x4 zero = {0, 0, 0, 0};
-      u32x4 x[TT], a[RT];
+      u32x4 xs[TT], as[RT];
 #pragma unroll
-      for (int j = 0; j < TT; ++j) x[j] = ok ? *(gu32x4p)(uintptr_t)(px[j] + k) : zero;
+      for (int j = 0; j < TT; ++j) xs[j] = ok ? *(gu32x4p)(uintptr_t)(px[j] + k) : zero;
 #pragma unroll
-      for (int i = 0; i < RT; ++i) a[i] = ok ? *(gu32x4p)(uintptr_t)(pa[i] + k) : zero;
+      for (int i = 0; i < RT; ++i) as[i] = ok ? *(gu32x4p)(uintptr_t)(pa[i] + k) : zero;
 #pragma unroll
       for (int i = 0; i < RT; ++i)
 #pragma unroll
-        for (int j = 0; j < TT; ++j) acc[i][j] = mfma16<BF16>(a[i], x[j], acc[i][j]);
+        for (int j = 0; j < TT; ++j) acc[i][j] = mfma16<BF16>(as[i], xs[j], acc[i][j]);
     }
   }
   // lane: ranks 4 g .. 4 g + 3 of row c
@@ -215,6 +258,14 @@ __global__ void __launch_bounds__(256) lora_a_kernel(LoraParams p, int chunks) {
   __shared__ __align__(16) float red[4 * kTileRows * kLd];
   int nrows = 0;
   const int ad = plan_tile(p, blockIdx.z, blockIdx.x, L, nrows);
+  if (blockIdx.y == 0) {
+    LoraTile *tile = p.tiles + (int64_t)blockIdx.z * gridDim.x + blockIdx.x;
+    if (threadIdx.x == 0) {
+      tile->adapter = ad;
+      tile->nrows = nrows;
+    }
+    if (threadIdx.x < kTileRows) tile->rows[threadIdx.x] = L.rows[min((int)threadIdx.x, max(nrows - 1, 0))];
+  }
   if (ad < 0 || ad == p.adapters) return;
   const int group = blockIdx.y / chunks;
   const int r0 = (blockIdx.y - group * chunks) * RT * 16;
@@ -245,21 +296,29 @@ __device__ __forceinline__ float from16(uint16_t b, bool bf16) {
   return bf16 ? bf16_bits_to_f32(b) : f16_bits_to_f32(b);
 }
 
-// Eight consecutive columns of a row as fp32, and back.
-__device__ __forceinline__ void load8(const void *p, int dtype, int64_t i, float (&v)[8]) {
+// Eight consecutive columns of a row: as loaded (fp32 takes two registers of
+// four, a 16-bit type one), as fp32, and stored.
+struct Raw8 {
+  u32x4 lo, hi;
+};
+__device__ __forceinline__ void load8(const void *p, int dtype, int64_t i, Raw8 &r) {
   if (dtype == 3) {
-    const f32x4 lo = *(const f32x4 *)((const float *)p + i);
-    const f32x4 hi = *(const f32x4 *)((const float *)p + i + 4);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[j] = lo[j];
-      v[4 + j] = hi[j];
-    }
+    r.lo = *(const u32x4 *)((const float *)p + i);
+    r.hi = *(const u32x4 *)((const float *)p + i + 4);
   } else {
-    const u32x4 q = *(const u32x4 *)((const uint16_t *)p + i);
+    r.lo = *(const u32x4 *)((const uint16_t *)p + i);
+  }
+}
+__device__ __forceinline__ void widen8(const Raw8 &r, int dtype, float (&v)[8]) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      v[j] = from16((uint16_t)(q[j >> 1] >> (16 * (j & 1))), dtype == 2);
+  for (int j = 0; j < 8; ++j) {
+    if (dtype == 3) {
+      const uint32_t w = j < 4 ? r.lo[j & 3] : r.hi[j & 3];
+      v[j] = __builtin_bit_cast(float, w);
+    } else {
+      const uint32_t w = r.lo[j >> 1];
+      v[j] = from16((uint16_t)(w >> (16 * (j & 1))), dtype == 2);
+    }
   }
 }
 __device__ __forceinline__ void store8(void *p, int dtype, int64_t i, const float (&v)[8]) {
@@ -269,9 +328,7 @@ __device__ __forceinline__ void store8(void *p, int dtype, int64_t i, const floa
   } else {
     u32x4 q;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      q[j] = (uint32_t)to16(v[2 * j], dtype == 2) |
-             ((uint32_t)to16(v[2 * j + 1], dtype == 2) << 16);
+    for (int j = 0; j < 4; ++j) q[j] = f32x2_to_out16(v[2 * j], v[2 * j + 1], dtype == 2);
     *(u32x4 *)((uint16_t *)p + i) = q;
   }
 }
@@ -295,26 +352,43 @@ struct SLds {
 };
 
 template <int RT, int TERMS, bool BF16>
-__device__ __forceinline__ void load_s(const LoraParams &p, const PlanLds &L, int nrows, int ad,
-                                       int ra, int groups, SLds<RT, TERMS> &S) {
+__device__ __forceinline__ void load_s(const LoraParams &p, const LoraTile *tile, int nrows,
+                                       int ad, int ra, int groups, SLds<RT, TERMS> &S) {
   const int t = threadIdx.x >> 2, q = threadIdx.x & 3;
   if (t >= nrows) return;  // columns of the tile past its rows are not used
   const int rp = (p.R + 15) & ~15;
   const float scale = p.scale ? p.scale[ad] : 1.0f;
-  const float *from = p.part + (int64_t)L.rows[t] * rp;
+  const float *from = p.part + (int64_t)tile->rows[t] * rp;
+  // kParts groups' sums at a time are asked for together; groups and ranks that
+  // are not there repeat one that is, and are not added
+  constexpr int kParts = RT <= 2 ? 4 : RT == 4 ? 2 : 1;
+  f32x4 sum[RT];
+#pragma unroll
+  for (int j = 0; j < RT; ++j) sum[j] = (f32x4){0.f, 0.f, 0.f, 0.f};
+  for (int i0 = 0; i0 < groups; i0 += kParts) {
+    f32x4 part[kParts][RT];
+#pragma unroll
+    for (int i = 0; i < kParts; ++i)
+#pragma unroll
+      for (int j = 0; j < RT; ++j) {
+        const int r = 4 * (q + 4 * j);
+        part[i][j] = *(const f32x4 *)(from + (int64_t)min(i0 + i, groups - 1) * p.rows * rp +
+                                      (r < ra ? r : 0));
+      }
+#pragma unroll
+    for (int i = 0; i < kParts; ++i)
+#pragma unroll
+      for (int j = 0; j < RT; ++j)
+        if (i0 + i < groups) sum[j] = i0 + i == 0 ? part[i][j] : sum[j] + part[i][j];
+  }
   float v[RT][4];
   float big = 0.0f;
 #pragma unroll
   for (int j = 0; j < RT; ++j) {
     const int r = 4 * (q + 4 * j);
-    f32x4 s = {0.f, 0.f, 0.f, 0.f};
-    if (r < ra) {  // written by lora_a: whole chunks of 16 ranks below ra
-      s = *(const f32x4 *)(from + r);
-      for (int i = 1; i < groups; ++i) s += *(const f32x4 *)(from + (int64_t)i * p.rows * rp + r);
-    }
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      v[j][u] = r + u < ra ? s[u] * scale : 0.0f;
+      v[j][u] = r + u < ra ? sum[j][u] * scale : 0.0f;
       big = fmaxf(big, fabsf(v[j][u]));
     }
   }
@@ -345,60 +419,78 @@ __device__ __forceinline__ void load_s(const LoraParams &p, const PlanLds &L, in
 }
 
 // B operand: eight ranks from r of output row n (rows of B past N repeat the
-// last one). Ranks at or above ra give zero whatever B holds there.
-template <bool VEC>
-__device__ __forceinline__ u32x4 load_b(const LoraParams &p, const uint16_t *b, int n, int r,
-                                        int ra) {
-  u32x4 v = {0, 0, 0, 0};
-  if (r >= ra) return v;
-  const uint16_t *at = b + (int64_t)min(n, p.N - 1) * p.R + r;
-  if constexpr (VEC) {  // R is a multiple of 8
-    v = *(gu32x4p)(uintptr_t)at;
-    if (r + 8 > ra) {
+// last one). Ranks at or above ra give zero whatever B holds there. With R a
+// multiple of 8 every load is one of 16 bytes, without a branch around it: one
+// that lies past R is moved inside and its values dropped.
+template <int RT>
+__device__ __forceinline__ void load_b(const LoraParams &p, const uint16_t *b, int n, int rg,
+                                       int ra, u32x4 (&v)[RT]) {
+  const uint16_t *at = b + (int64_t)min(n, p.N - 1) * p.R;
+  if (p.R % 8 == 0) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (r + j >= ra) v[j >> 1] &= j & 1 ? 0x0000ffffu : 0xffff0000u;
-    }
+    for (int rt = 0; rt < RT; ++rt)
+      v[rt] = *(gu32x4p)(uintptr_t)(at + min(rt * 16 + rg, p.R - 8));
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (r + j < ra) v[j >> 1] |= (uint32_t)at[j] << (16 * (j & 1));
+    for (int rt = 0; rt < RT; ++rt) {
+      v[rt] = (u32x4){0, 0, 0, 0};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int r = rt * 16 + rg + j;
+        if (r < ra) v[rt][j >> 1] |= (uint32_t)at[r] << (16 * (j & 1));
+      }
+    }
   }
-  return v;
+}
+template <int RT>
+__device__ __forceinline__ void mask_b(int rg, int ra, u32x4 (&v)[RT]) {
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (rt * 16 + rg + j >= ra) v[rt][j >> 1] &= j & 1 ? 0x0000ffffu : 0xffff0000u;
 }
 
 // One wave: 64 columns from n0 of TT * 16 rows. Columns are the MFMA rows:
-// row m of MFMA i is column n0 + 16 (m / 4) + 4 i + m % 4, so that a lane's
-// results of the four MFMAs are 16 consecutive columns of one row, and a row's
-// 64 columns are one run of 128 bytes (16-bit) or 256 (fp32).
-template <int RT, int TT, int TERMS, bool BF16, bool VEC>
-__device__ __forceinline__ void lora_b_block(const LoraParams &p, const PlanLds &L, int nrows,
+// row m of MFMA i is column n0 + 32 (i / 2) + 8 (m / 4) + 4 (i % 2) + m % 4,
+// so that a lane's results of MFMAs 2 h and 2 h + 1 are 8 consecutive columns
+// of one row, and the four lanes of a row 32: one run of 64 bytes (16-bit) or
+// 128 (fp32) to each load and store. The base is asked for first and B next;
+// both are on their way together.
+template <int RT, int TT, int TERMS, bool BF16>
+__device__ __forceinline__ void lora_b_block(const LoraParams &p, const int (&rows)[4], int nrows,
                                              const uint16_t *b, int ra, int n0,
                                              const SLds<RT, TERMS> &S) {
   const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
-  const int nc = n0 + 16 * (c >> 2) + (c & 3);
   const int rg = 8 * (g & 1);
+  const int nl = n0 + 8 * g;  // this lane's first column
+  Raw8 base[TT][2];
+  if (p.base) {
+#pragma unroll
+    for (int j = 0; j < TT; ++j)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)  // columns past N repeat the last ones
+        load8(p.base, p.base_dtype, (int64_t)rows[j] * p.ldbase + min(nl + 32 * h, p.N - 8),
+              base[j][h]);
+  }
   f32x4 acc[4][TT];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < TT; ++j) acc[i][j] = (f32x4){0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt) {
-    if (rt * 16 >= ra) break;
-    u32x4 bv[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) bv[i] = load_b<VEC>(p, b, nc + 4 * i, rt * 16 + rg, ra);
+  for (int i = 0; i < 4; ++i) {
+    u32x4 bv[RT];
+    load_b<RT>(p, b, n0 + 32 * (i >> 1) + 8 * (c >> 2) + 4 * (i & 1) + (c & 3), rg, ra, bv);
+    if (ra != RT * 16) mask_b<RT>(rg, ra, bv);
 #pragma unroll
     for (int j = 0; j < TT; ++j) {
-      const u32x4 s = *(const u32x4 *)&S.s[g >> 1][j * 16 + c][rt * 16 + rg];
+      acc[i][j] = (f32x4){0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[i][j] = mfma16<BF16>(bv[i], s, acc[i][j]);
-      if constexpr (TERMS == 3) {
-        u32x4 s3 = *(const u32x4 *)&S.s[2][j * 16 + c][rt * 16 + rg];
-        if (g >> 1) s3 = (u32x4){0, 0, 0, 0};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i][j] = mfma16<BF16>(bv[i], s3, acc[i][j]);
+      for (int rt = 0; rt < RT; ++rt) {
+        const u32x4 s = *(const u32x4 *)&S.s[g >> 1][j * 16 + c][rt * 16 + rg];
+        acc[i][j] = mfma16<BF16>(bv[rt], s, acc[i][j]);
+        if constexpr (TERMS == 3) {
+          u32x4 s3 = *(const u32x4 *)&S.s[2][j * 16 + c][rt * 16 + rg];
+          if (g >> 1) s3 = (u32x4){0, 0, 0, 0};
+          acc[i][j] = mfma16<BF16>(bv[rt], s3, acc[i][j]);
+        }
       }
     }
   }
@@ -406,71 +498,74 @@ __device__ __forceinline__ void lora_b_block(const LoraParams &p, const PlanLds 
   for (int j = 0; j < TT; ++j) {
     const int t = j * 16 + c;
     if (t >= nrows) continue;
-    const int64_t row = L.rows[t];
     const int e = S.e[t];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int n = n0 + 16 * g + 8 * h;
-      if (n >= p.N) continue;
-      float v[8];
-      if (p.base) load8(p.base, p.base_dtype, row * p.ldbase + n, v);
+      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (p.base) widen8(base[j][h], p.base_dtype, v);
 #pragma unroll
-      for (int u = 0; u < 8; ++u)
-        v[u] = ldexpf(acc[2 * h + (u >> 2)][j][u & 3], e) + (p.base ? v[u] : 0.0f);
-      store8(p.out, p.out_dtype, row * p.ldout + n, v);
+      for (int u = 0; u < 8; ++u) v[u] += ldexpf(acc[2 * h + (u >> 2)][j][u & 3], e);
+      const int n = nl + 32 * h;
+      if (n < p.N) store8(p.out, p.out_dtype, (int64_t)rows[j] * p.ldout + n, v);
     }
   }
 }
 
 // Rows without an adapter: out = base (or zeros).
-__device__ __forceinline__ void copy_rows(const LoraParams &p, const PlanLds &L, int nrows, int n0,
-                                          int n1) {
+__device__ __forceinline__ void copy_rows(const LoraParams &p, const LoraTile *tile, int nrows,
+                                          int n0, int n1) {
   if (p.base == p.out) return;
   const int per_row = (n1 - n0) / 8;
   for (int i = threadIdx.x; i < nrows * per_row; i += 256) {
     const int t = i / per_row, n = n0 + (i - t * per_row) * 8;
     float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (p.base) load8(p.base, p.base_dtype, (int64_t)L.rows[t] * p.ldbase + n, v);
-    store8(p.out, p.out_dtype, (int64_t)L.rows[t] * p.ldout + n, v);
+    if (p.base) {
+      Raw8 r;
+      load8(p.base, p.base_dtype, (int64_t)tile->rows[t] * p.ldbase + n, r);
+      widen8(r, p.base_dtype, v);
+    }
+    store8(p.out, p.out_dtype, (int64_t)tile->rows[t] * p.ldout + n, v);
   }
 }
 
 // Workgroup (tile, `cols` columns, window).
-template <int RT, int TERMS, bool BF16, bool VEC>
+template <int RT, int TERMS, bool BF16>
 __global__ void __launch_bounds__(256) lora_b_kernel(LoraParams p, int cols, int groups) {
-  __shared__ PlanLds L;
   __shared__ __align__(16) SLds<RT, TERMS> S;
-  int nrows = 0;
-  const int ad = plan_tile(p, blockIdx.z, blockIdx.x, L, nrows);
+  const LoraTile *tile = p.tiles + (int64_t)blockIdx.z * gridDim.x + blockIdx.x;
+  const int ad = uload_i32(&tile->adapter), nrows = uload_i32(&tile->nrows);
   if (ad < 0) return;
   const int c0 = blockIdx.y * cols, c1 = min(c0 + cols, p.N);
   const int ra = ad < p.adapters ? used_rank(p, ad) : 0;
   if (ra == 0) {
-    copy_rows(p, L, nrows, c0, c1);
+    copy_rows(p, tile, nrows, c0, c1);
     return;
   }
-  load_s<RT, TERMS, BF16>(p, L, nrows, ad, ra, groups, S);
+  int rows[4];  // tile row j * 16 + lane % 16; past the end the last row again
+#pragma unroll
+  for (int j = 0; j < 4; ++j) rows[j] = tile->rows[j * 16 + (threadIdx.x & 15)];
+  load_s<RT, TERMS, BF16>(p, tile, nrows, ad, ra, groups, S);
   __syncthreads();
   const uint16_t *b = p.b + (int64_t)ad * p.N * p.R;
   for (int n0 = c0 + 64 * wave_id(); n0 < c1; n0 += 256) {
-    if (nrows <= 16) lora_b_block<RT, 1, TERMS, BF16, VEC>(p, L, nrows, b, ra, n0, S);
-    else if (nrows <= 32) lora_b_block<RT, 2, TERMS, BF16, VEC>(p, L, nrows, b, ra, n0, S);
-    else lora_b_block<RT, 4, TERMS, BF16, VEC>(p, L, nrows, b, ra, n0, S);
+    if (nrows <= 16) lora_b_block<RT, 1, TERMS, BF16>(p, rows, nrows, b, ra, n0, S);
+    else if (nrows <= 32) lora_b_block<RT, 2, TERMS, BF16>(p, rows, nrows, b, ra, n0, S);
+    else lora_b_block<RT, 4, TERMS, BF16>(p, rows, nrows, b, ra, n0, S);
   }
 }
 
+int windows(int rows) { return (rows + kWindow - 1) / kWindow; }
 // Tiles a window can have: u buckets in use give at most u + (w - u) / 64.
-int tile_slots(const LoraParams &p) {
-  const int w = p.rows < kWindow ? p.rows : kWindow;
-  const int u = p.adapters + 1 < w ? p.adapters + 1 : w;
+int tile_slots(int rows, int adapters) {
+  const int w = rows < kWindow ? rows : kWindow;
+  const int u = adapters + 1 < w ? adapters + 1 : w;
   return u + (w - u) / kTileRows;
 }
-int windows(const LoraParams &p) { return (p.rows + kWindow - 1) / kWindow; }
 
 template <int RT>
 void run_a(const LoraParams &p, hipStream_t s) {
   const int chunks = (p.R + RT * 16 - 1) / (RT * 16);
-  const dim3 grid(tile_slots(p), lora_groups(p.K) * chunks, windows(p));
+  const dim3 grid(tile_slots(p.rows, p.adapters), lora_groups(p.K) * chunks, windows(p.rows));
   if (p.bf16) hipLaunchKernelGGL((lora_a_kernel<RT, true>), grid, dim3(256), 0, s, p, chunks);
   else hipLaunchKernelGGL((lora_a_kernel<RT, false>), grid, dim3(256), 0, s, p, chunks);
 }
@@ -478,14 +573,9 @@ void run_a(const LoraParams &p, hipStream_t s) {
 template <int RT, int TERMS, bool BF16>
 void run_b(const LoraParams &p, hipStream_t s) {
   const int cols = 256;
-  const dim3 grid(tile_slots(p), (p.N + cols - 1) / cols, windows(p));
-  const int groups = lora_groups(p.K);
-  if (p.R % 8 == 0)
-    hipLaunchKernelGGL((lora_b_kernel<RT, TERMS, BF16, true>), grid, dim3(256), 0, s, p, cols,
-                       groups);
-  else
-    hipLaunchKernelGGL((lora_b_kernel<RT, TERMS, BF16, false>), grid, dim3(256), 0, s, p, cols,
-                       groups);
+  const dim3 grid(tile_slots(p.rows, p.adapters), (p.N + cols - 1) / cols, windows(p.rows));
+  hipLaunchKernelGGL((lora_b_kernel<RT, TERMS, BF16>), grid, dim3(256), 0, s, p, cols,
+                     lora_groups(p.K));
 }
 
 template <int RT>
@@ -499,6 +589,9 @@ void run_b(const LoraParams &p, hipStream_t s) {
 
 int lora_groups(int K) { return (K + kGroup - 1) / kGroup; }
 int lora_padded_rank(int R) { return (R + 15) & ~15; }
+size_t lora_tiles(int rows, int adapters) {
+  return (size_t)windows(rows) * tile_slots(rows, adapters);
+}
 
 hipError_t launch_lora_a(const LoraParams &p, hipStream_t s) {
   if (p.R <= 16 || p.rows <= 256) run_a<1>(p, s);

@@ -298,26 +298,24 @@ __global__ void __launch_bounds__(256) route_topk_kernel(RouterParams p) {
   }
 }
 
-// The row's IDs j = lane and lane + 16: the expert, or -1 (none, outside
-// [0, E), or past the row's topk). At most 16 IDs leave the second one out.
-__device__ __forceinline__ void load_ids(const RouterParams &p, int64_t row, bool in, int lane,
-                                         int (&id)[2]) {
+// The row's IDs j = lane and lane + 16, as loaded (a lane without one reads
+// the row's last, so no branch stands around a load and the loads that follow
+// it) and as experts: -1 for none, outside [0, E), or past the row's topk. At
+// most 16 IDs leave the second one out.
+__device__ __forceinline__ void load_ids(const RouterParams &p, int64_t row, int lane,
+                                         int64_t (&raw)[2]) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const int k = lane + 16 * h;
-    id[h] = -1;
+    raw[h] = -1;
     if (h == 1 && p.topk <= 16) break;
-    if (in && k < p.topk) {
-      const int64_t o = row * p.topk + k;
-      if (p.ids_i64) {
-        const int64_t v = ((const int64_t *)p.ids)[o];
-        id[h] = v >= 0 && v < p.E ? (int)v : -1;
-      } else {
-        const int v = ((const int32_t *)p.ids)[o];
-        id[h] = (uint32_t)v < (uint32_t)p.E ? v : -1;
-      }
-    }
+    raw[h] = load_id(p.ids, p.ids_i64, row * p.topk + min(lane + 16 * h, p.topk - 1));
   }
+}
+__device__ __forceinline__ void take_ids(const RouterParams &p, bool in, int lane,
+                                         const int64_t (&raw)[2], int (&id)[2]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    id[h] = in && lane + 16 * h < p.topk && (uint64_t)raw[h] < (uint64_t)p.E ? (int)raw[h] : -1;
 }
 
 // ----------------------------------------------------------------- balance
@@ -344,18 +342,19 @@ __global__ void __launch_bounds__(256) balance_kernel(RouterParams p) {
   int64_t row = (int64_t)blockIdx.x * kRowsPerWg + (threadIdx.x >> 4);
   const int64_t step = (int64_t)gridDim.x * kRowsPerWg;
   const int64_t last = p.rows - 1;
-  int next_id[2];
+  int64_t next_id[2];
   RawRow<I, DT> next;
   if (last >= 0) {
-    load_ids(p, row, row <= last, lane, next_id);
+    load_ids(p, min(row, last), lane, next_id);
     load_raw<I, DT>(p, min(row, last) * p.ld_logits, lane, next);
   }
   for (int64_t r0 = (int64_t)blockIdx.x * kRowsPerWg; r0 <= last; r0 += step, row += step) {
-    int id[2] = {next_id[0], next_id[1]};
+    int id[2];
+    take_ids(p, row <= last, lane, next_id, id);
     float l[4 * I];
     unpack_row<I, DT>(next, l);
     if (r0 + step <= last) {
-      load_ids(p, row + step, row + step <= last, lane, next_id);
+      load_ids(p, min(row + step, last), lane, next_id);
       load_raw<I, DT>(p, min(row + step, last) * p.ld_logits, lane, next);
     }
     const bool live = row_any(id[0] >= 0 || id[1] >= 0);
@@ -504,27 +503,27 @@ __global__ void __launch_bounds__(256) route_backward_kernel(RouterParams p) {
   const int64_t step = (int64_t)gridDim.x * kRowsPerWg;
   const int64_t last = p.rows - 1;
   // the next rows' loads are under way while a row is worked on
-  int next_id[2];
-  float next_g[2];
+  int64_t next_id[2];
+  float next_g[2] = {0.0f, 0.0f};
   RawRow<I, DT> next;
   auto fetch = [&](int64_t r) {
-    load_ids(p, r, r <= last, lane, next_id);
+    load_raw<I, DT>(p, r * p.ld_logits, lane, next);
+    load_ids(p, r, lane, next_id);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      next_g[h] = 0.0f;
-      if (h == 1 && !two) break;
-      if (p.dw && r <= last && lane + 16 * h < p.topk)
-        next_g[h] = load_as_f32(p.dw, p.dw_dtype, r * p.topk + lane + 16 * h);
+      if (!p.dw || (h == 1 && !two)) break;
+      next_g[h] =
+          load_as_f32(p.dw, p.dw_dtype, r * p.topk + min(lane + 16 * h, p.topk - 1));
     }
-    load_raw<I, DT>(p, min(r, last) * p.ld_logits, lane, next);
   };
-  fetch(row);
+  fetch(min(row, last));
   for (int64_t r0 = (int64_t)blockIdx.x * kRowsPerWg; r0 <= last; r0 += step, row += step) {
-    int id[2] = {next_id[0], next_id[1]};
+    int id[2];
+    take_ids(p, row <= last, lane, next_id, id);
     float g[2] = {next_g[0], next_g[1]};
     float l[4 * I];
     unpack_row<I, DT>(next, l);
-    if (r0 + step <= last) fetch(row + step);
+    if (r0 + step <= last) fetch(min(row + step, last));
     const bool live = row_any(id[0] >= 0 || id[1] >= 0);
     const float m = shift(sig, row_max(max_of(l)));
     float pe[4 * I], inv = 0.0f;  // p_e

@@ -105,7 +105,7 @@ _SIGS = {
     "exl3_route_backward": (_i32, [ctypes.POINTER(RouterC), _vp, _i32, _i64, _i32, _vp, _i32, _vp,
                                    _i32, ctypes.POINTER(BalanceC), _f32, _vp, _vp, _i32, _i64,
                                    _vp, _PP]),
-    "exl3_lora_workspace_size": (_sz, [_i32, _i32, _i32]),
+    "exl3_lora_workspace_size": (_sz, [_i32] * 4),
     "exl3_lora": (_i32, [ctypes.POINTER(LoraC), _vp, _i32, _i64, _i32, _vp, _i32, _vp, _i32, _i64,
                          _vp, _i32, _i64, _vp, _sz, _vp, _PP]),
     "exl3_decode_tiles": (_i32, [_vp, _i32, _i32, _vp, _vp, _PP]),
@@ -460,8 +460,8 @@ def exl3_route_backward(logits, ids, dw=None, scoring="softmax", renorm=True, sc
     return dlogits
 
 
-def lora_workspace_size(rows, in_f, rank):
-    return lib().exl3_lora_workspace_size(rows, in_f, rank)
+def lora_workspace_size(rows, in_f, rank, num_adapters):
+    return lib().exl3_lora_workspace_size(rows, in_f, rank, num_adapters)
 
 
 def exl3_lora(x, a, b, ids, scale=None, ranks=None, base=None, out_dtype=None, out=None, ws=None):
@@ -498,7 +498,7 @@ def exl3_lora(x, a, b, ids, scale=None, ranks=None, base=None, out_dtype=None, o
         out = torch.empty(rows, N, device=x.device,
                           dtype=out_dtype or (base.dtype if base is not None else x.dtype))
     if ws is None:
-        ws = torch.empty(max(lora_workspace_size(rows, K, R), 256), dtype=torch.uint8,
+        ws = torch.empty(max(lora_workspace_size(rows, K, R, n), 256), dtype=torch.uint8,
                          device=x.device)
     lc = LoraC(K, N, R, n, a.data_ptr(), b.data_ptr(), scale, ranks)
     _check(lib().exl3_lora(ctypes.byref(lc), x.data_ptr(), _dt(x), _matrix(x, rows, K, "x"), rows,
