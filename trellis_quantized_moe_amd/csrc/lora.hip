@@ -12,7 +12,7 @@
 // tiles lora_b copies.
 //
 // A row's bytes depend on that row alone: the K axis is cut the same way in
-// every call (512 inputs to a wave, four waves to a group, groups in
+// every call (256 inputs to a wave, eight waves to a group, groups in
 // ascending order), a row is one column of the MFMA tiles whichever row it
 // shares them with, and the second product's scaling is per row.
 #include <type_traits>
@@ -26,118 +26,114 @@ namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
-constexpr int kWindow = 2048;     // rows planned together
-constexpr int kTileRows = 64;     // rows of a tile
-constexpr int kSlice = 512;       // inputs a wave of lora_a sums
-constexpr int kGroup = 4 * kSlice;  // inputs a workgroup of lora_a sums
+constexpr int kWindow = 2048;       // rows planned together
+constexpr int kTileRows = 64;       // rows of a tile
+constexpr int kWavesA = 8;          // waves of a workgroup of lora_a
+constexpr int kThreadsA = 64 * kWavesA;
+constexpr int kSlice = 256;         // inputs a wave of lora_a sums
+constexpr int kGroup = kWavesA * kSlice;  // inputs a workgroup of lora_a sums
 constexpr int kMaxBuckets = 1025;  // EXL3_MAX_ADAPTERS and "none"
-constexpr int kBucketsPerThread = (kMaxBuckets + 255) / 256;
+constexpr int kChunks = kWindow / kThreadsA;  // IDs of a thread
 
 struct PlanLds {
-  int count[256 * kBucketsPerThread];
-  int wave_tiles[4];
-  int4 rank[kWindow / 256];  // [chunk] -> per wave
+  int count[kMaxBuckets];
+  int hits[kChunks * kWavesA];  // rows of the bucket, by chunk and wave
   int rows[kTileRows];
-  int found[3];  // bucket (-1: none), tile within it, rows in the bucket
 };
+
+// Inclusive sum over the lanes of a wave: shifts inside the 16-lane rows, then
+// the rows' last lanes to the rows after them.
+__device__ __forceinline__ int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);  // row_shr:1
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // row_bcast:15
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);  // row_bcast:31
+  return v;
+}
 
 // Tile `tile` of window `win`: its adapter (p.adapters: rows without one; -1:
 // the window has fewer tiles) and its rows in L.rows[0 .. nrows). Called by
-// all 256 threads.
+// all kThreadsA threads.
 __device__ __forceinline__ int plan_tile(const LoraParams &p, int win, int tile, PlanLds &L,
                                          int &nrows) {
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = wave_id();
   const int row0 = win * kWindow;
   const int n = min(p.rows - row0, kWindow);
-  const int chunks = (n + 255) >> 8;
   // lanes past the window read its last ID and drop it: loads without a branch
   // around them are all in flight together
-  int a[kWindow / 256];
+  int a[kChunks];
   if (p.ids_i64) {
-    int64_t id[kWindow / 256];
+    int64_t id[kChunks];
 #pragma unroll
-    for (int i = 0; i < kWindow / 256; ++i)
-      id[i] = ((const int64_t *)p.ids)[row0 + min(i * 256 + tid, n - 1)];
+    for (int i = 0; i < kChunks; ++i)
+      id[i] = ((const int64_t *)p.ids)[row0 + min(i * kThreadsA + tid, n - 1)];
 #pragma unroll
-    for (int i = 0; i < kWindow / 256; ++i)
+    for (int i = 0; i < kChunks; ++i)
       a[i] = id[i] >= 0 && id[i] < p.adapters ? (int)id[i] : p.adapters;
   } else {
 #pragma unroll
-    for (int i = 0; i < kWindow / 256; ++i)
-      a[i] = ((const int32_t *)p.ids)[row0 + min(i * 256 + tid, n - 1)];
+    for (int i = 0; i < kChunks; ++i)
+      a[i] = ((const int32_t *)p.ids)[row0 + min(i * kThreadsA + tid, n - 1)];
 #pragma unroll
-    for (int i = 0; i < kWindow / 256; ++i)
+    for (int i = 0; i < kChunks; ++i)
       a[i] = (uint32_t)a[i] < (uint32_t)p.adapters ? a[i] : p.adapters;
   }
 #pragma unroll
-  for (int i = 0; i < kWindow / 256; ++i) a[i] = i * 256 + tid < n ? a[i] : -1;
-  for (int b = tid; b <= p.adapters; b += 256) L.count[b] = 0;
-  if (tid == 0) L.found[0] = -1;
+  for (int i = 0; i < kChunks; ++i) a[i] = i * kThreadsA + tid < n ? a[i] : -1;
+  for (int b = tid; b <= p.adapters; b += kThreadsA) L.count[b] = 0;
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kWindow / 256; ++i) {
-    if (i >= chunks) break;
+  for (int i = 0; i < kChunks; ++i) {
     // a prompt's rows share one adapter: one addition for the wave
     const int first = __builtin_amdgcn_readfirstlane(a[i]);
     const uint64_t same = __ballot(a[i] == first), valid = __ballot(a[i] >= 0);
     if (same == valid) {
-      if (lane == 0 && first >= 0) atomicAdd(&L.count[first], __popcll(same));
+      if (lane == 0) atomicAdd(&L.count[first], __popcll(same));
     } else if (a[i] >= 0) {
       atomicAdd(&L.count[a[i]], 1);
     }
   }
   __syncthreads();
-  // exclusive scan of the buckets' tiles
-  int cnt[kBucketsPerThread], mine = 0;
-#pragma unroll
-  for (int j = 0; j < kBucketsPerThread; ++j) {
-    const int b = tid * kBucketsPerThread + j;
-    cnt[j] = b <= p.adapters ? L.count[b] : 0;
-    mine += (cnt[j] + kTileRows - 1) / kTileRows;
-  }
-  int incl = mine;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int o = __shfl_up(incl, d, 64);
-    incl += lane >= d ? o : 0;
-  }
-  if (lane == 63) L.wave_tiles[wave] = incl;
-  __syncthreads();
-  int first_tile = incl - mine;
-  for (int w = 0; w < wave; ++w) first_tile += L.wave_tiles[w];
-#pragma unroll
-  for (int j = 0; j < kBucketsPerThread; ++j) {
-    const int t = (cnt[j] + kTileRows - 1) / kTileRows;
-    if (tile >= first_tile && tile < first_tile + t) {
-      L.found[0] = tid * kBucketsPerThread + j;
-      L.found[1] = tile - first_tile;
-      L.found[2] = cnt[j];
+  // the bucket the tile falls into; every wave looks for itself
+  int ad = -1, skip = 0, size = 0;
+  for (int b0 = 0, before = 0; b0 <= p.adapters; b0 += 64) {
+    const int rows = b0 + lane <= p.adapters ? L.count[b0 + lane] : 0;
+    const int tiles = (rows + kTileRows - 1) / kTileRows;
+    const int end = before + wave_scan(tiles);
+    const uint64_t past = __ballot(end > tile);
+    if (past) {
+      const int l = __ffsll((long long)past) - 1;
+      ad = b0 + l;
+      skip = (tile - (__shfl(end, l, 64) - __shfl(tiles, l, 64))) * kTileRows;
+      size = __shfl(rows, l, 64);
+      break;
     }
-    first_tile += t;
+    before = __shfl(end, 63, 64);
   }
-  __syncthreads();
-  const int ad = __builtin_amdgcn_readfirstlane(L.found[0]);
+  ad = __builtin_amdgcn_readfirstlane(ad);
   if (ad < 0) return -1;
-  const int skip = __builtin_amdgcn_readfirstlane(L.found[1]) * kTileRows;
-  nrows = min(kTileRows, __builtin_amdgcn_readfirstlane(L.found[2]) - skip);
+  skip = __builtin_amdgcn_readfirstlane(skip);
+  nrows = min(kTileRows, __builtin_amdgcn_readfirstlane(size) - skip);
   // the bucket's rows in order, from number `skip` on
+  uint64_t hit[kChunks];
 #pragma unroll
-  for (int i = 0; i < kWindow / 256; ++i) {
-    if (i >= chunks) break;
-    const uint64_t hit = __ballot(a[i] == ad);
-    if (lane == 0) ((int *)&L.rank[i])[wave] = __popcll(hit);
+  for (int i = 0; i < kChunks; ++i) {
+    hit[i] = __ballot(a[i] == ad);
+    if (lane == 0) L.hits[i * kWavesA + wave] = __popcll(hit[i]);
   }
   __syncthreads();
-  int before = 0;
+  // rows before this wave's of each chunk: lane i of the first kChunks *
+  // kWavesA lanes sums up to entry i
+  static_assert(kChunks * kWavesA <= 64, "one entry to a lane");
+  const int own = lane < kChunks * kWavesA ? L.hits[lane] : 0;
+  const int before = wave_scan(own) - own;
 #pragma unroll
-  for (int i = 0; i < kWindow / 256; ++i) {
-    if (i >= chunks) break;
-    const int4 r = L.rank[i];
-    const uint64_t hit = __ballot(a[i] == ad);
-    const int at = before + (wave > 0 ? r.x : 0) + (wave > 1 ? r.y : 0) + (wave > 2 ? r.z : 0) +
-                   __popcll(hit & ((1ull << lane) - 1)) - skip;
-    if (a[i] == ad && at >= 0 && at < kTileRows) L.rows[at] = row0 + i * 256 + tid;
-    before += r.x + r.y + r.z + r.w;
+  for (int i = 0; i < kChunks; ++i) {
+    const int at = __builtin_amdgcn_readlane(before, i * kWavesA + wave) +
+                   __popcll(hit[i] & ((1ull << lane) - 1)) - skip;
+    if (a[i] == ad && at >= 0 && at < kTileRows) L.rows[at] = row0 + i * kThreadsA + tid;
   }
   __syncthreads();
   return ad;
@@ -183,36 +179,33 @@ __device__ __forceinline__ void lora_a_tile(const LoraParams &p, const PlanLds &
 #pragma unroll
     for (int i = 0; i < RT; ++i)
       pa[i] = p.a + ((int64_t)ad * p.R + min(r0 + i * 16 + c, ra - 1)) * p.K + 8 * g;
-    // kStep K steps of 32 inputs are loaded while the kStep before them go
-    // through the matrix units
-    constexpr int kStep = TT + RT <= 5 ? 4 : 2;
-    u32x4 x[2][kStep][TT], a[2][kStep][RT];
-    auto fetch = [&](int buf, int k) {
+    // the loads of kBuf - 1 K steps of 32 inputs are on their way while one goes
+    // through the matrix units: about 120 registers, two waves to a SIMD
+    constexpr int kSteps = kSlice / 32;
+    constexpr int kWant = 30 / (TT + RT);
+    constexpr int kBuf = kWant < 3 ? 3 : kWant < kSteps ? kWant : kSteps;
+    u32x4 x[kBuf][TT], a[kBuf][RT];
+    auto fetch = [&](int n) {
 #pragma unroll
-      for (int u = 0; u < kStep; ++u) {
+      for (int j = 0; j < TT; ++j)
+        x[n % kBuf][j] = *(gu32x4p)(uintptr_t)(px[j] + k0 + 32 * n);
 #pragma unroll
-        for (int j = 0; j < TT; ++j) x[buf][u][j] = *(gu32x4p)(uintptr_t)(px[j] + k + 32 * u);
-#pragma unroll
-        for (int i = 0; i < RT; ++i) a[buf][u][i] = *(gu32x4p)(uintptr_t)(pa[i] + k + 32 * u);
-      }
+      for (int i = 0; i < RT; ++i)
+        a[n % kBuf][i] = *(gu32x4p)(uintptr_t)(pa[i] + k0 + 32 * n);
     };
-    auto multiply = [&](int buf) {
+    int k = k0;
+    if (k1 - k0 == kSlice) {
 #pragma unroll
-      for (int u = 0; u < kStep; ++u)
+      for (int n = 0; n < kBuf - 1; ++n) fetch(n);
+#pragma unroll
+      for (int n = 0; n < kSteps; ++n) {
+        if (n + kBuf - 1 < kSteps) fetch(n + kBuf - 1);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int i = 0; i < RT; ++i)
 #pragma unroll
           for (int j = 0; j < TT; ++j)
-            acc[i][j] = mfma16<BF16>(a[buf][u][i], x[buf][u][j], acc[i][j]);
-    };
-    int k = k0;
-    if (k1 - k0 == kSlice) {
-      fetch(0, k0);
-#pragma unroll
-      for (int n = 0; n < kSlice / (32 * kStep); ++n) {
-        if (n + 1 < kSlice / (32 * kStep)) fetch((n + 1) & 1, k0 + (n + 1) * 32 * kStep);
-        __builtin_amdgcn_sched_barrier(0);
-        multiply(n & 1);
+            acc[i][j] = mfma16<BF16>(a[n % kBuf][i], x[n % kBuf][j], acc[i][j]);
       }
       k = k1;
     }
@@ -241,18 +234,33 @@ __device__ __forceinline__ void lora_a_tile(const LoraParams &p, const PlanLds &
         for (int j = 0; j < TT; ++j) acc[i][j] = mfma16<BF16>(as[i], xs[j], acc[i][j]);
     }
   }
-  // lane: ranks 4 g .. 4 g + 3 of row c
-  float *to = red + (threadIdx.x >> 6) * kTileRows * kLd;
+  // lane: ranks 4 g .. 4 g + 3 of row c. Waves 4 .. 7 leave theirs in LDS, waves
+  // 0 .. 3 add their own; the kernel adds those four.
+  const int wave = wave_id();
+  float *at = red + (wave & 3) * kTileRows * kLd;
+  if (wave >= 4) {
 #pragma unroll
-  for (int i = 0; i < RT; ++i)
+    for (int i = 0; i < RT; ++i)
 #pragma unroll
-    for (int j = 0; j < TT; ++j)
-      *(f32x4 *)(to + (j * 16 + c) * kLd + i * 16 + 4 * g) = acc[i][j];
+      for (int j = 0; j < TT; ++j)
+        *(f32x4 *)(at + (j * 16 + c) * kLd + i * 16 + 4 * g) = acc[i][j];
+  }
+  __syncthreads();
+  if (wave < 4) {
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int j = 0; j < TT; ++j) {
+        f32x4 *to = (f32x4 *)(at + (j * 16 + c) * kLd + i * 16 + 4 * g);
+        *to = acc[i][j] + *to;
+      }
+  }
+  __syncthreads();
 }
 
 // Workgroup (tile, group and rank chunk, window).
 template <int RT, bool BF16>
-__global__ void __launch_bounds__(256) lora_a_kernel(LoraParams p, int chunks) {
+__global__ void __launch_bounds__(kThreadsA) lora_a_kernel(LoraParams p, int chunks) {
   constexpr int kLd = RT * 16 + 4;
   __shared__ PlanLds L;
   __shared__ __align__(16) float red[4 * kTileRows * kLd];
@@ -275,14 +283,13 @@ __global__ void __launch_bounds__(256) lora_a_kernel(LoraParams p, int chunks) {
   if (nrows <= 16) lora_a_tile<RT, 1, BF16>(p, L, nrows, ad, r0, ra, k0, red);
   else if (nrows <= 32) lora_a_tile<RT, 2, BF16>(p, L, nrows, ad, r0, ra, k0, red);
   else lora_a_tile<RT, 4, BF16>(p, L, nrows, ad, r0, ra, k0, red);
-  __syncthreads();
   const int rp = (p.R + 15) & ~15;
-  for (int i = threadIdx.x; i < nrows * RT * 4; i += 256) {
+  for (int i = threadIdx.x; i < nrows * RT * 4; i += kThreadsA) {
     const int t = i / (RT * 4), r = (i - t * RT * 4) * 4;
     const float *from = red + t * kLd + r;
-    f32x4 s = *(const f32x4 *)from;
-#pragma unroll
-    for (int w = 1; w < 4; ++w) s += *(const f32x4 *)(from + w * kTileRows * kLd);
+    constexpr int w = kTileRows * kLd;
+    const f32x4 s = (*(const f32x4 *)from + *(const f32x4 *)(from + w)) +
+                    (*(const f32x4 *)(from + 2 * w) + *(const f32x4 *)(from + 3 * w));
     if (r0 + r < rp)
       *(f32x4 *)(p.part + ((int64_t)group * p.rows + L.rows[t]) * rp + r0 + r) = s;
   }
@@ -296,28 +303,34 @@ __device__ __forceinline__ float from16(uint16_t b, bool bf16) {
   return bf16 ? bf16_bits_to_f32(b) : f16_bits_to_f32(b);
 }
 
-// Eight consecutive columns of a row: as loaded (fp32 takes two registers of
-// four, a 16-bit type one), as fp32, and stored.
+// Eight consecutive columns of a row: base as loaded (BASE: 0 none, 2 a 16-bit
+// type, 4 fp32; the size is a template argument so that no branch stands
+// between the loads), as fp32, and stored.
+template <int BASE>
 struct Raw8 {
-  u32x4 lo, hi;
+  u32x4 v[BASE == 4 ? 2 : 1];
 };
-__device__ __forceinline__ void load8(const void *p, int dtype, int64_t i, Raw8 &r) {
-  if (dtype == 3) {
-    r.lo = *(const u32x4 *)((const float *)p + i);
-    r.hi = *(const u32x4 *)((const float *)p + i + 4);
-  } else {
-    r.lo = *(const u32x4 *)((const uint16_t *)p + i);
+template <int BASE>
+__device__ __forceinline__ void load8(const void *p, int64_t i, Raw8<BASE> &r) {
+  if constexpr (BASE == 4) {
+    r.v[0] = *(gu32x4p)(uintptr_t)((const float *)p + i);
+    r.v[1] = *(gu32x4p)(uintptr_t)((const float *)p + i + 4);
+  } else if constexpr (BASE == 2) {
+    r.v[0] = *(gu32x4p)(uintptr_t)((const uint16_t *)p + i);
   }
 }
-__device__ __forceinline__ void widen8(const Raw8 &r, int dtype, float (&v)[8]) {
+template <int BASE>
+__device__ __forceinline__ void widen8(const Raw8<BASE> &r, int dtype, float (&v)[8]) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    if (dtype == 3) {
-      const uint32_t w = j < 4 ? r.lo[j & 3] : r.hi[j & 3];
+    if constexpr (BASE == 4) {
+      const uint32_t w = r.v[j >> 2][j & 3];
       v[j] = __builtin_bit_cast(float, w);
-    } else {
-      const uint32_t w = r.lo[j >> 1];
+    } else if constexpr (BASE == 2) {
+      const uint32_t w = r.v[0][j >> 1];
       v[j] = from16((uint16_t)(w >> (16 * (j & 1))), dtype == 2);
+    } else {
+      v[j] = 0.0f;
     }
   }
 }
@@ -333,6 +346,17 @@ __device__ __forceinline__ void store8(void *p, int dtype, int64_t i, const floa
   }
 }
 
+// Ranks go through the second product in chunks of eight. Chunk c holds ranks
+// 8 c .. 8 c + 7; where R is no multiple of 8 (and at least 8), the last one
+// starts at R - 8 instead, so that its load stays inside B's row, and leaves
+// out the ranks that the chunk before it has. Loads of 16 bytes need no
+// alignment here. First rank of a chunk:
+__device__ __forceinline__ int chunk_start(int R, int c) {
+  return R >= 8 ? min(8 * c, R - 8) : 8 * c;
+}
+typedef f32x4 f32x4_a4 __attribute__((aligned(4)));
+typedef const u32x4 __attribute__((address_space(1), aligned(2))) *gu32x4p_a2;
+
 // s as MFMA operands. The matrix cores take 16-bit inputs, so s is written as
 // a sum of 16-bit terms, each the rounded rest of the ones before: two fp16
 // terms hold 2^-23 of the row's largest entry, two bf16 terms 2^-17 (enough
@@ -344,21 +368,29 @@ __device__ __forceinline__ void store8(void *p, int dtype, int64_t i, const floa
 // One MFMA takes 32 inner values: the first term of 16 ranks and the second
 // term of the same 16, against B given twice. The third term, if any, is a
 // second MFMA with zeros in the other half.
-template <int RT, int TERMS>
+template <int RT>
 struct SLds {
   static constexpr int kLd = RT * 16 + 8;  // 16-byte rows, spread over the banks
-  uint16_t s[TERMS][kTileRows][kLd];
+  uint16_t s[3][kTileRows][kLd];
   int e[kTileRows];
 };
 
-template <int RT, int TERMS, bool BF16>
+template <int RT, bool BF16>
 __device__ __forceinline__ void load_s(const LoraParams &p, const LoraTile *tile, int nrows,
-                                       int ad, int ra, int groups, SLds<RT, TERMS> &S) {
+                                       int ad, int ra, int groups, SLds<RT> &S) {
   const int t = threadIdx.x >> 2, q = threadIdx.x & 3;
   if (t >= nrows) return;  // columns of the tile past its rows are not used
   const int rp = (p.R + 15) & ~15;
   const float scale = p.scale ? p.scale[ad] : 1.0f;
   const float *from = p.part + (int64_t)tile->rows[t] * rp;
+  // slots 4 (q + 4 j) .. + 3 hold ranks r0[j] .. + 3, those from lo[j] on
+  int r0[RT], lo[RT];
+#pragma unroll
+  for (int j = 0; j < RT; ++j) {
+    const int slot = 4 * (q + 4 * j);
+    lo[j] = slot & ~7;
+    r0[j] = chunk_start(p.R, slot >> 3) + (slot & 4);
+  }
   // kParts groups' sums at a time are asked for together; groups and ranks that
   // are not there repeat one that is, and are not added
   constexpr int kParts = RT <= 2 ? 4 : RT == 4 ? 2 : 1;
@@ -370,11 +402,9 @@ __device__ __forceinline__ void load_s(const LoraParams &p, const LoraTile *tile
 #pragma unroll
     for (int i = 0; i < kParts; ++i)
 #pragma unroll
-      for (int j = 0; j < RT; ++j) {
-        const int r = 4 * (q + 4 * j);
-        part[i][j] = *(const f32x4 *)(from + (int64_t)min(i0 + i, groups - 1) * p.rows * rp +
-                                      (r < ra ? r : 0));
-      }
+      for (int j = 0; j < RT; ++j)
+        part[i][j] = *(const f32x4_a4 *)(from + (int64_t)min(i0 + i, groups - 1) * p.rows * rp +
+                                         (lo[j] < ra ? r0[j] : 0));
 #pragma unroll
     for (int i = 0; i < kParts; ++i)
 #pragma unroll
@@ -384,14 +414,13 @@ __device__ __forceinline__ void load_s(const LoraParams &p, const LoraTile *tile
   float v[RT][4];
   float big = 0.0f;
 #pragma unroll
-  for (int j = 0; j < RT; ++j) {
-    const int r = 4 * (q + 4 * j);
+  for (int j = 0; j < RT; ++j)
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      v[j][u] = r + u < ra ? sum[j][u] * scale : 0.0f;
+      const int r = r0[j] + u;
+      v[j][u] = r >= lo[j] && r < ra ? sum[j][u] * scale : 0.0f;
       big = fmaxf(big, fabsf(v[j][u]));
     }
-  }
   big = fmaxf(big, __shfl_xor(big, 1, 64));
   big = fmaxf(big, __shfl_xor(big, 2, 64));
   // fmaxf passes over NaN; the row's finite entries are scaled by the largest
@@ -399,12 +428,12 @@ __device__ __forceinline__ void load_s(const LoraParams &p, const LoraTile *tile
   const int e = (int)((__builtin_bit_cast(uint32_t, big) >> 23) & 255u) - 140;
 #pragma unroll
   for (int j = 0; j < RT; ++j) {
-    uint32_t w[TERMS][2];
+    uint32_t w[3][2];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       float rest = ldexpf(v[j][u], -e);
 #pragma unroll
-      for (int m = 0; m < TERMS; ++m) {
+      for (int m = 0; m < (BF16 ? 3 : 2); ++m) {
         const uint16_t b = to16(rest, BF16);
         if (u & 1) w[m][u >> 1] |= (uint32_t)b << 16;
         else w[m][u >> 1] = b;
@@ -412,146 +441,176 @@ __device__ __forceinline__ void load_s(const LoraParams &p, const LoraTile *tile
       }
     }
 #pragma unroll
-    for (int m = 0; m < TERMS; ++m)
+    for (int m = 0; m < (BF16 ? 3 : 2); ++m)
       *(uint2 *)&S.s[m][t][4 * (q + 4 * j)] = make_uint2(w[m][0], w[m][1]);
   }
   if (q == 0) S.e[t] = e;
 }
 
-// B operand: eight ranks from r of output row n (rows of B past N repeat the
-// last one). Ranks at or above ra give zero whatever B holds there. With R a
-// multiple of 8 every load is one of 16 bytes, without a branch around it: one
-// that lies past R is moved inside and its values dropped.
-template <int RT>
-__device__ __forceinline__ void load_b(const LoraParams &p, const uint16_t *b, int n, int rg,
-                                       int ra, u32x4 (&v)[RT]) {
-  const uint16_t *at = b + (int64_t)min(n, p.N - 1) * p.R;
-  if (p.R % 8 == 0) {
+// What a wave loads for 32 columns of TT * 16 rows: the base and B. Columns
+// are the MFMA rows: row m of MFMA i is column n0 + 8 (m / 4) + 4 i + m % 4, so
+// that a lane's results of both MFMAs are 8 consecutive columns of one row, and
+// the four lanes of a row 32: one run of 64 bytes (16-bit) or 128 (fp32).
+template <int RT, int TT, int BASE>
+struct Columns {
+  Raw8<BASE> base[TT];
+  u32x4 b[2][RT];
+};
+
+// WIDE: R >= 8. Below that B's rows are shorter than a load and are read one by
+// one. Columns past N repeat the last ones, so no branch stands before a load.
+template <int RT, int TT, int BASE, bool WIDE>
+__device__ __forceinline__ void load_columns(const LoraParams &p, const int (&rows)[4],
+                                             const uint16_t *b, int n0, Columns<RT, TT, BASE> &u) {
+  const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt)
-      v[rt] = *(gu32x4p)(uintptr_t)(at + min(rt * 16 + rg, p.R - 8));
-  } else {
+  for (int j = 0; j < TT; ++j)
+    load8<BASE>(p.base, (int64_t)rows[j] * p.ldbase + min(n0 + 8 * g, p.N - 8), u.base[j]);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int n = min(n0 + 8 * (c >> 2) + 4 * i + (c & 3), p.N - 1);
+    const uint16_t *at = b + (int64_t)n * p.R;
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-      v[rt] = (u32x4){0, 0, 0, 0};
+      if constexpr (WIDE) {
+        u.b[i][rt] = *(gu32x4p_a2)(uintptr_t)(at + chunk_start(p.R, 2 * rt + (g & 1)));
+      } else {
+        uint32_t w[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int r = rt * 16 + rg + j;
-        if (r < ra) v[rt][j >> 1] |= (uint32_t)at[r] << (16 * (j & 1));
+        for (int j = 0; j < 8; ++j) w[j] = at[min(j, p.R - 1)];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) u.b[i][rt][j] = w[2 * j] | (w[2 * j + 1] << 16);
       }
     }
   }
-}
-template <int RT>
-__device__ __forceinline__ void mask_b(int rg, int ra, u32x4 (&v)[RT]) {
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (rt * 16 + rg + j >= ra) v[rt][j >> 1] &= j & 1 ? 0x0000ffffu : 0xffff0000u;
 }
 
-// One wave: 64 columns from n0 of TT * 16 rows. Columns are the MFMA rows:
-// row m of MFMA i is column n0 + 32 (i / 2) + 8 (m / 4) + 4 (i % 2) + m % 4,
-// so that a lane's results of MFMAs 2 h and 2 h + 1 are 8 consecutive columns
-// of one row, and the four lanes of a row 32: one run of 64 bytes (16-bit) or
-// 128 (fp32) to each load and store. The base is asked for first and B next;
-// both are on their way together.
-template <int RT, int TT, int TERMS, bool BF16>
-__device__ __forceinline__ void lora_b_block(const LoraParams &p, const int (&rows)[4], int nrows,
-                                             const uint16_t *b, int ra, int n0,
-                                             const SLds<RT, TERMS> &S) {
+// The rest of the work on those columns. mask: some ranks of a chunk are not
+// used or not its own; their B counts as zero whatever it holds (0 * NaN).
+template <int RT, int TT, bool BF16, int BASE>
+__device__ __forceinline__ void use_columns(const LoraParams &p, const int (&rows)[4], int nrows,
+                                            int ra, bool mask, bool three, int n0,
+                                            Columns<RT, TT, BASE> &u, const SLds<RT> &S) {
   const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
-  const int rg = 8 * (g & 1);
-  const int nl = n0 + 8 * g;  // this lane's first column
-  Raw8 base[TT][2];
-  if (p.base) {
+  if (mask) {
 #pragma unroll
-    for (int j = 0; j < TT; ++j)
+    for (int rt = 0; rt < RT; ++rt) {
+      const int lo = 8 * (2 * rt + (g & 1)), r = chunk_start(p.R, 2 * rt + (g & 1));
 #pragma unroll
-      for (int h = 0; h < 2; ++h)  // columns past N repeat the last ones
-        load8(p.base, p.base_dtype, (int64_t)rows[j] * p.ldbase + min(nl + 32 * h, p.N - 8),
-              base[j][h]);
-  }
-  f32x4 acc[4][TT];
+      for (int j = 0; j < 8; ++j) {
+        const bool off = r + j < lo || r + j >= ra;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    u32x4 bv[RT];
-    load_b<RT>(p, b, n0 + 32 * (i >> 1) + 8 * (c >> 2) + 4 * (i & 1) + (c & 3), rg, ra, bv);
-    if (ra != RT * 16) mask_b<RT>(rg, ra, bv);
-#pragma unroll
-    for (int j = 0; j < TT; ++j) {
-      acc[i][j] = (f32x4){0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        const u32x4 s = *(const u32x4 *)&S.s[g >> 1][j * 16 + c][rt * 16 + rg];
-        acc[i][j] = mfma16<BF16>(bv[rt], s, acc[i][j]);
-        if constexpr (TERMS == 3) {
-          u32x4 s3 = *(const u32x4 *)&S.s[2][j * 16 + c][rt * 16 + rg];
-          if (g >> 1) s3 = (u32x4){0, 0, 0, 0};
-          acc[i][j] = mfma16<BF16>(bv[rt], s3, acc[i][j]);
-        }
+        for (int i = 0; i < 2; ++i)
+          if (off) u.b[i][rt][j >> 1] &= j & 1 ? 0x0000ffffu : 0xffff0000u;
       }
     }
   }
+  f32x4 acc[2][TT];
+#pragma unroll
+  for (int j = 0; j < TT; ++j) {
+    acc[0][j] = acc[1][j] = (f32x4){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      const int at = rt * 16 + 8 * (g & 1);
+      const u32x4 s = *(const u32x4 *)&S.s[g >> 1][j * 16 + c][at];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) acc[i][j] = mfma16<BF16>(u.b[i][rt], s, acc[i][j]);
+      if (BF16 && three) {
+        u32x4 s3 = *(const u32x4 *)&S.s[2][j * 16 + c][at];
+        if (g >> 1) s3 = (u32x4){0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) acc[i][j] = mfma16<BF16>(u.b[i][rt], s3, acc[i][j]);
+      }
+    }
+  }
+  const int n = n0 + 8 * g;
 #pragma unroll
   for (int j = 0; j < TT; ++j) {
     const int t = j * 16 + c;
-    if (t >= nrows) continue;
+    float v[8];
+    widen8<BASE>(u.base[j], p.base_dtype, v);
+    if (t >= nrows || n >= p.N) continue;
     const int e = S.e[t];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (p.base) widen8(base[j][h], p.base_dtype, v);
-#pragma unroll
-      for (int u = 0; u < 8; ++u) v[u] += ldexpf(acc[2 * h + (u >> 2)][j][u & 3], e);
-      const int n = nl + 32 * h;
-      if (n < p.N) store8(p.out, p.out_dtype, (int64_t)rows[j] * p.ldout + n, v);
-    }
+    for (int w = 0; w < 8; ++w) v[w] += ldexpf(acc[w >> 2][j][w & 3], e);
+    store8(p.out, p.out_dtype, (int64_t)rows[j] * p.ldout + n, v);
   }
 }
 
-// Rows without an adapter: out = base (or zeros).
+// A wave's columns n0 .. n1 - 1 of TT * 16 rows, 32 at a time: the next 32 are
+// on their way while the present ones are multiplied and stored, and the first
+// are asked for before s is.
+template <int RT, int TT, bool BF16, int BASE, bool WIDE>
+__device__ __forceinline__ void lora_b_tile(const LoraParams &p, const LoraTile *tile, int nrows,
+                                            int ad, int ra, int groups, int n0, int n1,
+                                            SLds<RT> &S) {
+  int rows[4];  // tile row j * 16 + lane % 16; past the end the last row again
+#pragma unroll
+  for (int j = 0; j < TT; ++j) rows[j] = tile->rows[j * 16 + (threadIdx.x & 15)];
+  const uint16_t *b = p.b + (int64_t)ad * p.N * p.R;
+  const bool mask = ra != RT * 16, three = p.out_dtype == 3;
+  Columns<RT, TT, BASE> u[2];
+  load_columns<RT, TT, BASE, WIDE>(p, rows, b, n0, u[0]);
+  load_s<RT, BF16>(p, tile, nrows, ad, ra, groups, S);
+  __syncthreads();
+  for (int n = n0; n < n1; n += 64) {
+    load_columns<RT, TT, BASE, WIDE>(p, rows, b, n + 32, u[1]);
+    __builtin_amdgcn_sched_barrier(0);
+    use_columns<RT, TT, BF16, BASE>(p, rows, nrows, ra, mask, three, n, u[0], S);
+    if (n + 32 >= n1) break;
+    load_columns<RT, TT, BASE, WIDE>(p, rows, b, n + 64, u[0]);
+    __builtin_amdgcn_sched_barrier(0);
+    use_columns<RT, TT, BF16, BASE>(p, rows, nrows, ra, mask, three, n + 32, u[1], S);
+  }
+}
+
+// Rows without an adapter: out = base (or zeros), 16 loads of a thread together.
+template <int BASE>
 __device__ __forceinline__ void copy_rows(const LoraParams &p, const LoraTile *tile, int nrows,
                                           int n0, int n1) {
-  if (p.base == p.out) return;
-  const int per_row = (n1 - n0) / 8;
-  for (int i = threadIdx.x; i < nrows * per_row; i += 256) {
-    const int t = i / per_row, n = n0 + (i - t * per_row) * 8;
-    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (p.base) {
-      Raw8 r;
-      load8(p.base, p.base_dtype, (int64_t)tile->rows[t] * p.ldbase + n, r);
-      widen8(r, p.base_dtype, v);
+  if (p.base == p.out || n0 >= n1) return;
+  const int per_row = (n1 - n0) / 8, total = nrows * per_row;
+  for (int i0 = threadIdx.x; i0 < total; i0 += 256 * 8) {
+    Raw8<BASE> r[8];
+    int64_t row[8];
+    int n[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int i = min(i0 + 256 * u, total - 1), t = i / per_row;
+      row[u] = tile->rows[t];
+      n[u] = n0 + (i - t * per_row) * 8;
     }
-    store8(p.out, p.out_dtype, (int64_t)tile->rows[t] * p.ldout + n, v);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) load8<BASE>(p.base, row[u] * p.ldbase + n[u], r[u]);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      float v[8];
+      widen8<BASE>(r[u], p.base_dtype, v);
+      if (i0 + 256 * u < total) store8(p.out, p.out_dtype, row[u] * p.ldout + n[u], v);
+    }
   }
 }
 
-// Workgroup (tile, `cols` columns, window).
-template <int RT, int TERMS, bool BF16>
-__global__ void __launch_bounds__(256) lora_b_kernel(LoraParams p, int cols, int groups) {
-  __shared__ __align__(16) SLds<RT, TERMS> S;
+// Workgroup (tile, 4 * per_wave columns, window).
+template <int RT, bool BF16, int BASE, bool WIDE>
+__global__ void __launch_bounds__(256) lora_b_kernel(LoraParams p, int per_wave, int groups) {
+  __shared__ __align__(16) SLds<RT> S;
   const LoraTile *tile = p.tiles + (int64_t)blockIdx.z * gridDim.x + blockIdx.x;
   const int ad = uload_i32(&tile->adapter), nrows = uload_i32(&tile->nrows);
   if (ad < 0) return;
-  const int c0 = blockIdx.y * cols, c1 = min(c0 + cols, p.N);
+  const int c0 = blockIdx.y * 4 * per_wave;
   const int ra = ad < p.adapters ? used_rank(p, ad) : 0;
   if (ra == 0) {
-    copy_rows(p, tile, nrows, c0, c1);
+    copy_rows<BASE>(p, tile, nrows, c0, min(c0 + 4 * per_wave, p.N));
     return;
   }
-  int rows[4];  // tile row j * 16 + lane % 16; past the end the last row again
-#pragma unroll
-  for (int j = 0; j < 4; ++j) rows[j] = tile->rows[j * 16 + (threadIdx.x & 15)];
-  load_s<RT, TERMS, BF16>(p, tile, nrows, ad, ra, groups, S);
-  __syncthreads();
-  const uint16_t *b = p.b + (int64_t)ad * p.N * p.R;
-  for (int n0 = c0 + 64 * wave_id(); n0 < c1; n0 += 256) {
-    if (nrows <= 16) lora_b_block<RT, 1, TERMS, BF16>(p, rows, nrows, b, ra, n0, S);
-    else if (nrows <= 32) lora_b_block<RT, 2, TERMS, BF16>(p, rows, nrows, b, ra, n0, S);
-    else lora_b_block<RT, 4, TERMS, BF16>(p, rows, nrows, b, ra, n0, S);
-  }
+  const int n0 = c0 + per_wave * wave_id(), n1 = min(n0 + per_wave, p.N);
+  if (nrows <= 16)
+    lora_b_tile<RT, 1, BF16, BASE, WIDE>(p, tile, nrows, ad, ra, groups, n0, n1, S);
+  else if (nrows <= 32)
+    lora_b_tile<RT, 2, BF16, BASE, WIDE>(p, tile, nrows, ad, ra, groups, n0, n1, S);
+  else
+    lora_b_tile<RT, 4, BF16, BASE, WIDE>(p, tile, nrows, ad, ra, groups, n0, n1, S);
 }
 
 int windows(int rows) { return (rows + kWindow - 1) / kWindow; }
@@ -566,23 +625,40 @@ template <int RT>
 void run_a(const LoraParams &p, hipStream_t s) {
   const int chunks = (p.R + RT * 16 - 1) / (RT * 16);
   const dim3 grid(tile_slots(p.rows, p.adapters), lora_groups(p.K) * chunks, windows(p.rows));
-  if (p.bf16) hipLaunchKernelGGL((lora_a_kernel<RT, true>), grid, dim3(256), 0, s, p, chunks);
-  else hipLaunchKernelGGL((lora_a_kernel<RT, false>), grid, dim3(256), 0, s, p, chunks);
+  if (p.bf16) hipLaunchKernelGGL((lora_a_kernel<RT, true>), grid, dim3(kThreadsA), 0, s, p, chunks);
+  else hipLaunchKernelGGL((lora_a_kernel<RT, false>), grid, dim3(kThreadsA), 0, s, p, chunks);
 }
 
-template <int RT, int TERMS, bool BF16>
+template <int RT, bool BF16, int BASE, bool WIDE>
 void run_b(const LoraParams &p, hipStream_t s) {
-  const int cols = 256;
-  const dim3 grid(tile_slots(p.rows, p.adapters), (p.N + cols - 1) / cols, windows(p.rows));
-  hipLaunchKernelGGL((lora_b_kernel<RT, TERMS, BF16>), grid, dim3(256), 0, s, p, cols,
+  // Columns of a wave, in units of 32. Every workgroup reads its rows' sums, 4
+  // groups R bytes a row; `need` units make that at most half of the base and
+  // output it moves, and are taken as far as 256 workgroups are left. Beyond
+  // that, enough that no more than about 1024 are launched.
+  const int64_t units = (p.N + 127) / 128 * ((p.rows + kTileRows - 1) / kTileRows);
+  const int64_t row_bytes = BASE + (p.out_dtype == 3 ? 4 : 2);
+  const int64_t need = 8 * lora_groups(p.K) * lora_padded_rank(p.R) / (row_bytes * 128) + 1;
+  int64_t u = need < units / 256 ? need : units / 256;
+  if (u < units / 1024) u = units / 1024;
+  const int per_wave = 32 * (int)(u < 1 ? 1 : u > 8 ? 8 : u);
+  const dim3 grid(tile_slots(p.rows, p.adapters), (p.N + 4 * per_wave - 1) / (4 * per_wave),
+                  windows(p.rows));
+  hipLaunchKernelGGL((lora_b_kernel<RT, BF16, BASE, WIDE>), grid, dim3(256), 0, s, p, per_wave,
                      lora_groups(p.K));
 }
 
-template <int RT>
+template <int RT, bool WIDE>
 void run_b(const LoraParams &p, hipStream_t s) {
-  if (!p.bf16) run_b<RT, 2, false>(p, s);
-  else if (p.out_dtype == 3) run_b<RT, 3, true>(p, s);
-  else run_b<RT, 2, true>(p, s);
+  const int base = !p.base ? 0 : p.base_dtype == 3 ? 4 : 2;
+  if (p.bf16) {
+    if (base == 0) run_b<RT, true, 0, WIDE>(p, s);
+    else if (base == 2) run_b<RT, true, 2, WIDE>(p, s);
+    else run_b<RT, true, 4, WIDE>(p, s);
+  } else {
+    if (base == 0) run_b<RT, false, 0, WIDE>(p, s);
+    else if (base == 2) run_b<RT, false, 2, WIDE>(p, s);
+    else run_b<RT, false, 4, WIDE>(p, s);
+  }
 }
 
 }  // namespace
@@ -601,10 +677,11 @@ hipError_t launch_lora_a(const LoraParams &p, hipStream_t s) {
 }
 
 hipError_t launch_lora_b(const LoraParams &p, hipStream_t s) {
-  if (p.R <= 16) run_b<1>(p, s);
-  else if (p.R <= 32) run_b<2>(p, s);
-  else if (p.R <= 64) run_b<4>(p, s);
-  else run_b<8>(p, s);
+  if (p.R < 8) run_b<1, false>(p, s);
+  else if (p.R <= 16) run_b<1, true>(p, s);
+  else if (p.R <= 32) run_b<2, true>(p, s);
+  else if (p.R <= 64) run_b<4, true>(p, s);
+  else run_b<8, true>(p, s);
   return hipGetLastError();
 }
 
