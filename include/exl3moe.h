@@ -82,6 +82,7 @@ enum exl3_status {
 #define EXL3_MAX_ADAPTERS 1024
 #define EXL3_MAX_RANK 128
 #define EXL3_LORA_MAX_ROWS (1 << 26)
+#define EXL3_LORA_MAX_LD (1 << 19)
 
 int32_t exl3_abi_version(void);
 /* Static string for a status code (host; never NULL). */
@@ -426,7 +427,8 @@ typedef struct exl3_lora_adapters {
  * rows: at most EXL3_LORA_MAX_ROWS. x: [rows][K], rows ld_x elements apart. ids: [rows] EXL3_I32 or EXL3_I64.
  * base: [rows][N] fp16, bf16 or fp32, ld_base apart, or NULL (zeros); out:
  * [rows][N] fp16, bf16 or fp32, ld_out apart. x, base, out: 16-byte aligned,
- * their row distances at least a row and a multiple of 16 bytes. out may be
+ * their row distances at least a row, at most EXL3_LORA_MAX_LD elements and a
+ * multiple of 16 bytes. out may be
  * base itself (same dtype and row distance), otherwise it overlaps no input.
  * ws: exl3_lora_workspace_size(rows, in_features, rank, num_adapters) bytes,
  * 16-byte aligned (the inner products and the row tiles); calls that share it

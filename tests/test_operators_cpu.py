@@ -185,7 +185,8 @@ def _lora(ad="default", x=P, dt=exl3.F16, ldx=256, rows=4, ids=P, ids_dt=exl3.I3
     (dict(dt=exl3.F32), -2), (dict(ids_dt=exl3.F16), -2), (dict(out_dt=exl3.I32), -2),
     (dict(base_dt=0), -2), (dict(in_features=252), -3), (dict(out_features=0), -3),
     (dict(out_features=1 << 17, ldo=1 << 17, ldb=1 << 17), -3), (dict(ldx=248), -3),
-    (dict(ldo=120), -3), (dict(ldb=127), -3), (dict(ldx=(1 << 32) + 8), -3),
+    (dict(ldo=120), -3), (dict(ldb=127), -3), (dict(ldx=(1 << 19) + 8), -3),
+    (dict(ldo=(1 << 19) + 8), -3), (dict(ldb=(1 << 19) + 8), -3),
     (dict(x=P + 8), -4), (dict(a=P + 8), -4), (dict(b=P + 4), -4), (dict(base=P + 8), -4),
     (dict(out=2 * P + 2), -4), (dict(ws=P + 8), -4), (dict(ldx=260), -4), (dict(ldo=132), -4),
     (dict(ldb=130), -4), (dict(ids=P + 2), -4), (dict(ids=P + 4, ids_dt=exl3.I64), -4),

@@ -1098,7 +1098,9 @@ int32_t exl3_lora(const exl3_lora_adapters *ad, const uint16_t *x, int32_t x_dty
   for (int64_t f : {K, N})
     if (f < 8 || f > EXL3_MAX_FEATURES || f % 8) return EXL3_E_SHAPE;
   if (ld_x < K || ld_out < N || (base && ld_base < N)) return EXL3_E_SHAPE;
-  if (ld_x > kMaxLd || ld_out > kMaxLd || (base && ld_base > kMaxLd)) return EXL3_E_SHAPE;
+  if (ld_x > EXL3_LORA_MAX_LD || ld_out > EXL3_LORA_MAX_LD ||
+      (base && ld_base > EXL3_LORA_MAX_LD))
+    return EXL3_E_SHAPE;
   if (base == out && (base_dtype != out_dtype || ld_base != ld_out)) return EXL3_E_ARG;
   for (const void *q : {(const void *)ad->a, (const void *)ad->b, (const void *)x, base,
                         (const void *)out, (const void *)ws})

@@ -12,8 +12,8 @@
 // tiles lora_b copies.
 //
 // A row's bytes depend on that row alone: the K axis is cut the same way in
-// every call (256 inputs to a wave, eight waves to a group, groups in
-// ascending order), a row is one column of the MFMA tiles whichever row it
+// every call (slices of 256 inputs, eight to a group, groups in ascending
+// order, whichever waves take them), a row is one column of the MFMA tiles whichever row it
 // shares them with, and the second product's scaling is per row.
 #include <type_traits>
 
@@ -28,16 +28,14 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kWindow = 2048;       // rows planned together
 constexpr int kTileRows = 64;       // rows of a tile
-constexpr int kWavesA = 8;          // waves of a workgroup of lora_a
-constexpr int kThreadsA = 64 * kWavesA;
-constexpr int kSlice = 256;         // inputs a wave of lora_a sums
-constexpr int kGroup = kWavesA * kSlice;  // inputs a workgroup of lora_a sums
+constexpr int kSlice = 256;         // inputs summed in one run
+constexpr int kSlices = 8;          // slices of a workgroup of lora_a
+constexpr int kGroup = kSlices * kSlice;
 constexpr int kMaxBuckets = 1025;  // EXL3_MAX_ADAPTERS and "none"
-constexpr int kChunks = kWindow / kThreadsA;  // IDs of a thread
 
 struct PlanLds {
   int count[kMaxBuckets];
-  int hits[kChunks * kWavesA];  // rows of the bucket, by chunk and wave
+  int hits[kWindow / 64];  // rows of the bucket, by 64 rows
   int rows[kTileRows];
 };
 
@@ -54,10 +52,13 @@ __device__ __forceinline__ int wave_scan(int v) {
 }
 
 // Tile `tile` of window `win`: its adapter (p.adapters: rows without one; -1:
-// the window has fewer tiles) and its rows in L.rows[0 .. nrows). Called by
-// all kThreadsA threads.
+// the window has fewer tiles) and its rows, counted from the window's first,
+// in L.rows[0 .. nrows). Called by
+// all threads of a workgroup of W waves.
+template <int W>
 __device__ __forceinline__ int plan_tile(const LoraParams &p, int win, int tile, PlanLds &L,
                                          int &nrows) {
+  constexpr int kThreads = 64 * W, kChunks = kWindow / kThreads;
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_id();
   const int row0 = win * kWindow;
   const int n = min(p.rows - row0, kWindow);
@@ -68,21 +69,21 @@ __device__ __forceinline__ int plan_tile(const LoraParams &p, int win, int tile,
     int64_t id[kChunks];
 #pragma unroll
     for (int i = 0; i < kChunks; ++i)
-      id[i] = ((const int64_t *)p.ids)[row0 + min(i * kThreadsA + tid, n - 1)];
+      id[i] = ((const int64_t *)p.ids)[row0 + min(i * kThreads + tid, n - 1)];
 #pragma unroll
     for (int i = 0; i < kChunks; ++i)
       a[i] = id[i] >= 0 && id[i] < p.adapters ? (int)id[i] : p.adapters;
   } else {
 #pragma unroll
     for (int i = 0; i < kChunks; ++i)
-      a[i] = ((const int32_t *)p.ids)[row0 + min(i * kThreadsA + tid, n - 1)];
+      a[i] = ((const int32_t *)p.ids)[row0 + min(i * kThreads + tid, n - 1)];
 #pragma unroll
     for (int i = 0; i < kChunks; ++i)
       a[i] = (uint32_t)a[i] < (uint32_t)p.adapters ? a[i] : p.adapters;
   }
 #pragma unroll
-  for (int i = 0; i < kChunks; ++i) a[i] = i * kThreadsA + tid < n ? a[i] : -1;
-  for (int b = tid; b <= p.adapters; b += kThreadsA) L.count[b] = 0;
+  for (int i = 0; i < kChunks; ++i) a[i] = i * kThreads + tid < n ? a[i] : -1;
+  for (int b = tid; b <= p.adapters; b += kThreads) L.count[b] = 0;
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < kChunks; ++i) {
@@ -121,19 +122,18 @@ __device__ __forceinline__ int plan_tile(const LoraParams &p, int win, int tile,
 #pragma unroll
   for (int i = 0; i < kChunks; ++i) {
     hit[i] = __ballot(a[i] == ad);
-    if (lane == 0) L.hits[i * kWavesA + wave] = __popcll(hit[i]);
+    if (lane == 0) L.hits[i * W + wave] = __popcll(hit[i]);
   }
   __syncthreads();
-  // rows before this wave's of each chunk: lane i of the first kChunks *
-  // kWavesA lanes sums up to entry i
-  static_assert(kChunks * kWavesA <= 64, "one entry to a lane");
-  const int own = lane < kChunks * kWavesA ? L.hits[lane] : 0;
+  // rows before this wave's of each chunk: lane i sums up to entry i
+  static_assert(kWindow / 64 <= 64, "one entry to a lane");
+  const int own = lane < kWindow / 64 ? L.hits[lane] : 0;
   const int before = wave_scan(own) - own;
 #pragma unroll
   for (int i = 0; i < kChunks; ++i) {
-    const int at = __builtin_amdgcn_readlane(before, i * kWavesA + wave) +
+    const int at = __builtin_amdgcn_readlane(before, i * W + wave) +
                    __popcll(hit[i] & ((1ull << lane) - 1)) - skip;
-    if (a[i] == ad && at >= 0 && at < kTileRows) L.rows[at] = row0 + i * kThreadsA + tid;
+    if (a[i] == ad && at >= 0 && at < kTileRows) L.rows[at] = i * kThreads + tid;
   }
   __syncthreads();
   return ad;
@@ -142,6 +142,15 @@ __device__ __forceinline__ int plan_tile(const LoraParams &p, int win, int tile,
 // Ranks the adapter uses.
 __device__ __forceinline__ int used_rank(const LoraParams &p, int ad) {
   return p.ranks ? max(0, min(p.R, uload_i32(p.ranks + ad))) : p.R;
+}
+
+// A load from a uniform address and a lane's byte offset: a window's rows lie
+// within 2^32 bytes (row distances are at most EXL3_LORA_MAX_LD), so a row's
+// address takes one register instead of two.
+template <typename T>
+__device__ __forceinline__ T load_at(const void *base, uint32_t off) {
+  typedef const T __attribute__((address_space(1))) *gp;
+  return *(gp)((uintptr_t)base + off);
 }
 
 template <bool BF16>
@@ -155,143 +164,165 @@ __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
 }
 
 // ------------------------------------------------------------------ x A^T
-// One wave: s[r][t] of RT * 16 ranks and TT * 16 rows over one slice. Ranks
-// are the MFMA rows, tile rows its columns; both operands are contiguous along
-// K, so each lane's 16-byte loads are MFMA operands as they come and nothing
-// goes through LDS on the way in.
-template <int RT, int TT, bool BF16>
-__device__ __forceinline__ void lora_a_tile(const LoraParams &p, const PlanLds &L, int nrows,
-                                            int ad, int r0, int ra, int k0, float *red) {
-  constexpr int kLd = RT * 16 + 4;
-  const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
-  const int k1 = min(k0 + kSlice, p.K);
+// One wave of W: s[r][t] of RT * 16 ranks and TT * 16 rows over slices w and,
+// with four waves, w + 4 of its group. Ranks are the MFMA rows, tile rows its
+// columns. A lane's operand is 16 bytes of row (lane % 16), so loading operands
+// as they are used puts 64 lanes on 64 cache lines, and the cache looks up one
+// line a cycle: that took 58 us on 16384 x 4096 where the bytes need 27.
+// Instead eight lanes take 128 bytes of a row, 64 inputs of 8 rows to a load,
+// and the wave turns them round in LDS that it shares with no other: chunk k of
+// row r lies at place k ^ (r % 8) of the row, so that the writes of eight lanes
+// (one row) and the reads of eight (one chunk of eight rows) fall into
+// different banks. red[i], i < 4, gets the sum of slices i and i + 4.
+template <int RT, int TT>
+struct LdsA {
+  static constexpr int kLd = RT * 16 + 4;
+  static constexpr int kStage = (TT + RT) * 2048;  // bytes of a wave
+};
+
+template <int RT, int TT, int W, bool BF16>
+__device__ __forceinline__ void lora_a_tile(const LoraParams &p, const int *tile_rows, int nrows,
+                                            int ad, int r0, int ra, int kg, char *lds) {
+  constexpr int kLd = LdsA<RT, TT>::kLd;
+  constexpr int kPairs = kSlice / 64 * (kSlices / W);  // loads of 64 inputs
+  constexpr int kAhead = TT + RT <= 3 ? 3 : TT + RT <= 4 ? 2 : 1;  // of them on their way
+  const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15, wave = wave_id();
   f32x4 acc[RT][TT];
+  auto clear = [&] {
 #pragma unroll
-  for (int i = 0; i < RT; ++i)
+    for (int i = 0; i < RT; ++i)
 #pragma unroll
-    for (int j = 0; j < TT; ++j) acc[i][j] = (f32x4){0.f, 0.f, 0.f, 0.f};
-  if (k0 < k1) {
-    const uint16_t *px[TT], *pa[RT];
-    // lanes past the last row or rank repeat it; their sums are not used
+      for (int j = 0; j < TT; ++j) acc[i][j] = (f32x4){0.f, 0.f, 0.f, 0.f};
+  };
+  // load h of a 16-row operand: row 8 h + lane / 8, inputs 8 (lane % 8) ..;
+  // rows past the last row or rank repeat it, their sums are not used
+  const uint16_t *x0 = p.x + (int64_t)blockIdx.z * kWindow * p.ldx;
+  const uint16_t *a0 = p.a + (int64_t)ad * p.R * p.K;
+  uint32_t src[TT + RT][2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int r = 8 * h + (lane >> 3);
 #pragma unroll
     for (int j = 0; j < TT; ++j)
-      px[j] = p.x + (int64_t)L.rows[min(j * 16 + c, nrows - 1)] * p.ldx + 8 * g;
+      src[j][h] = (uint32_t)tile_rows[min(j * 16 + r, nrows - 1)] * (uint32_t)p.ldx * 2;
 #pragma unroll
-    for (int i = 0; i < RT; ++i)
-      pa[i] = p.a + ((int64_t)ad * p.R + min(r0 + i * 16 + c, ra - 1)) * p.K + 8 * g;
-    // the loads of kBuf - 1 K steps of 32 inputs are on their way while one goes
-    // through the matrix units: about 120 registers, two waves to a SIMD
-    constexpr int kSteps = kSlice / 32;
-    constexpr int kWant = 30 / (TT + RT);
-    constexpr int kBuf = kWant < 3 ? 3 : kWant < kSteps ? kWant : kSteps;
-    u32x4 x[kBuf][TT], a[kBuf][RT];
-    auto fetch = [&](int n) {
-#pragma unroll
-      for (int j = 0; j < TT; ++j)
-        x[n % kBuf][j] = *(gu32x4p)(uintptr_t)(px[j] + k0 + 32 * n);
-#pragma unroll
-      for (int i = 0; i < RT; ++i)
-        a[n % kBuf][i] = *(gu32x4p)(uintptr_t)(pa[i] + k0 + 32 * n);
-    };
-    int k = k0;
-    if (k1 - k0 == kSlice) {
-#pragma unroll
-      for (int n = 0; n < kBuf - 1; ++n) fetch(n);
-#pragma unroll
-      for (int n = 0; n < kSteps; ++n) {
-        if (n + kBuf - 1 < kSteps) fetch(n + kBuf - 1);
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int i = 0; i < RT; ++i)
-#pragma unroll
-          for (int j = 0; j < TT; ++j)
-            acc[i][j] = mfma16<BF16>(a[n % kBuf][i], x[n % kBuf][j], acc[i][j]);
-      }
-      k = k1;
-    }
-    for (; k + 32 <= k1; k += 32) {  // the last slice of a K that is no multiple of kSlice
-      u32x4 xs[TT], as[RT];
-#pragma unroll
-      for (int j = 0; j < TT; ++j) xs[j] = *(gu32x4p)(uintptr_t)(px[j] + k);
-#pragma unroll
-      for (int i = 0; i < RT; ++i) as[i] = *(gu32x4p)(uintptr_t)(pa[i] + k);
-#pragma unroll
-      for (int i = 0; i < RT; ++i)
-#pragma unroll
-        for (int j = 0; j < TT; ++j) acc[i][j] = mfma16<BF16>(as[i], xs[j], acc[i][j]);
-    }
-    if (k < k1) {  // K is a multiple of 8: a lane's eight inputs are all there or none is
-      const bool ok = k + 8 * g < k1;
-      const u32x4 zero = {0, 0, 0, 0};
-      u32x4 xs[TT], as[RT];
-#pragma unroll
-      for (int j = 0; j < TT; ++j) xs[j] = ok ? *(gu32x4p)(uintptr_t)(px[j] + k) : zero;
-#pragma unroll
-      for (int i = 0; i < RT; ++i) as[i] = ok ? *(gu32x4p)(uintptr_t)(pa[i] + k) : zero;
-#pragma unroll
-      for (int i = 0; i < RT; ++i)
-#pragma unroll
-        for (int j = 0; j < TT; ++j) acc[i][j] = mfma16<BF16>(as[i], xs[j], acc[i][j]);
-    }
+    for (int i = 0; i < RT; ++i) src[TT + i][h] = min(r0 + i * 16 + r, ra - 1) * p.K * 2;
   }
-  // lane: ranks 4 g .. 4 g + 3 of row c. Waves 4 .. 7 leave theirs in LDS, waves
-  // 0 .. 3 add their own; the kernel adds those four.
-  const int wave = wave_id();
-  float *at = red + (wave & 3) * kTileRows * kLd;
-  if (wave >= 4) {
+  char *stage = lds + wave * LdsA<RT, TT>::kStage;
+  char *put = stage + (lane >> 3) * 128 + (((lane & 7) ^ (lane >> 3)) << 4);
+  const char *get[2] = {stage + c * 128 + ((g ^ (c & 7)) << 4),
+                        stage + c * 128 + (((4 + g) ^ (c & 7)) << 4)};
+  const int k0 = kg + wave * kSlice + 8 * (lane & 7);
+  u32x4 v[kAhead][TT + RT][2];
+  // K is a multiple of 8: a lane's eight inputs are all there or none is. Those
+  // that are not read the row's last eight and count as zero.
+  auto input = [&](int n) { return k0 + n / (kSlice / 64) * 4 * kSlice + n % (kSlice / 64) * 64; };
+  auto fetch = [&](int n) {
+    const int k = min(input(n), p.K - 8);
 #pragma unroll
-    for (int i = 0; i < RT; ++i)
+    for (int i = 0; i < TT + RT; ++i)
 #pragma unroll
-      for (int j = 0; j < TT; ++j)
-        *(f32x4 *)(at + (j * 16 + c) * kLd + i * 16 + 4 * g) = acc[i][j];
-  }
-  __syncthreads();
-  if (wave < 4) {
+      for (int h = 0; h < 2; ++h)
+        v[n % kAhead][i][h] = load_at<u32x4>(i < TT ? x0 : a0, src[i][h] + 2 * k);
+  };
+  float *red = (float *)lds + ((wave & 3) * TT * 16 + c) * kLd + 4 * g;
+  auto leave = [&](bool add) {
 #pragma unroll
     for (int i = 0; i < RT; ++i)
 #pragma unroll
       for (int j = 0; j < TT; ++j) {
-        f32x4 *to = (f32x4 *)(at + (j * 16 + c) * kLd + i * 16 + 4 * g);
-        *to = acc[i][j] + *to;
+        f32x4 *q = (f32x4 *)(red + j * 16 * kLd + i * 16);
+        *q = add ? acc[i][j] + *q : acc[i][j];
       }
+  };
+  f32x4 first[RT][TT];  // four waves: the sums of slice w
+  clear();
+#pragma unroll
+  for (int n = 0; n < kAhead; ++n) fetch(n);
+#pragma unroll
+  for (int n = 0; n < kPairs; ++n) {
+    if (n == kSlice / 64) {
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int j = 0; j < TT; ++j) first[i][j] = acc[i][j];
+      clear();
+    }
+    const bool there = input(n) < p.K;
+#pragma unroll
+    for (int i = 0; i < TT + RT; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const u32x4 zero = {0, 0, 0, 0};
+        *(u32x4 *)(put + i * 2048 + h * 1024) = there ? v[n % kAhead][i][h] : zero;
+      }
+    if (n + kAhead < kPairs) fetch(n + kAhead);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      u32x4 x[TT], a[RT];
+#pragma unroll
+      for (int j = 0; j < TT; ++j) x[j] = *(const u32x4 *)(get[s] + j * 2048);
+#pragma unroll
+      for (int i = 0; i < RT; ++i) a[i] = *(const u32x4 *)(get[s] + (TT + i) * 2048);
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int j = 0; j < TT; ++j) acc[i][j] = mfma16<BF16>(a[i], x[j], acc[i][j]);
+    }
+  }
+  __syncthreads();  // the sums take the place of the staged operands
+  // lane: ranks 4 g .. 4 g + 3 of row c
+  if constexpr (W == 4) {
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int j = 0; j < TT; ++j) acc[i][j] = first[i][j] + acc[i][j];
+    leave(false);
+  } else {
+    if (wave >= 4) leave(false);
+    __syncthreads();
+    if (wave < 4) leave(true);
   }
   __syncthreads();
 }
 
-// Workgroup (tile, group and rank chunk, window).
-template <int RT, bool BF16>
-__global__ void __launch_bounds__(kThreadsA) lora_a_kernel(LoraParams p, int chunks) {
-  constexpr int kLd = RT * 16 + 4;
+// Workgroup (tile, half of its rows, group and rank chunk, window).
+template <int RT, int W, bool BF16>
+__global__ void __launch_bounds__(64 * W) lora_a_kernel(LoraParams p, int chunks) {
+  constexpr int kStages = W * LdsA<RT, 2>::kStage, kSums = 4 * 32 * LdsA<RT, 2>::kLd * 4;
   __shared__ PlanLds L;
-  __shared__ __align__(16) float red[4 * kTileRows * kLd];
+  __shared__ __align__(16) char lds[kStages > kSums ? kStages : kSums];
   int nrows = 0;
-  const int ad = plan_tile(p, blockIdx.z, blockIdx.x, L, nrows);
+  const int ad = plan_tile<W>(p, blockIdx.z, blockIdx.x, L, nrows);
   if (blockIdx.y == 0) {
     LoraTile *tile = p.tiles + (int64_t)blockIdx.z * gridDim.x + blockIdx.x;
     if (threadIdx.x == 0) {
       tile->adapter = ad;
       tile->nrows = nrows;
     }
-    if (threadIdx.x < kTileRows) tile->rows[threadIdx.x] = L.rows[min((int)threadIdx.x, max(nrows - 1, 0))];
+    if (threadIdx.x < kTileRows)
+      tile->rows[threadIdx.x] = L.rows[min((int)threadIdx.x, max(nrows - 1, 0))];
   }
   if (ad < 0 || ad == p.adapters) return;
-  const int group = blockIdx.y / chunks;
-  const int r0 = (blockIdx.y - group * chunks) * RT * 16;
+  const int half = blockIdx.y & 1, gc = blockIdx.y >> 1;
+  const int group = gc / chunks, r0 = (gc - group * chunks) * RT * 16;
   const int ra = used_rank(p, ad);
-  if (r0 >= ra) return;
-  const int k0 = group * kGroup + wave_id() * kSlice;
-  if (nrows <= 16) lora_a_tile<RT, 1, BF16>(p, L, nrows, ad, r0, ra, k0, red);
-  else if (nrows <= 32) lora_a_tile<RT, 2, BF16>(p, L, nrows, ad, r0, ra, k0, red);
-  else lora_a_tile<RT, 4, BF16>(p, L, nrows, ad, r0, ra, k0, red);
-  const int rp = (p.R + 15) & ~15;
-  for (int i = threadIdx.x; i < nrows * RT * 4; i += kThreadsA) {
+  const int *tile_rows = L.rows + 32 * half;
+  nrows = min(nrows - 32 * half, 32);
+  if (r0 >= ra || nrows <= 0) return;
+  const int kg = group * kGroup;
+  if (nrows <= 16) lora_a_tile<RT, 1, W, BF16>(p, tile_rows, nrows, ad, r0, ra, kg, lds);
+  else lora_a_tile<RT, 2, W, BF16>(p, tile_rows, nrows, ad, r0, ra, kg, lds);
+  const int rp = (p.R + 15) & ~15, row0 = blockIdx.z * kWindow;
+  const int w = (nrows <= 16 ? 16 : 32) * LdsA<RT, 2>::kLd;
+  for (int i = threadIdx.x; i < nrows * RT * 4; i += 64 * W) {
     const int t = i / (RT * 4), r = (i - t * RT * 4) * 4;
-    const float *from = red + t * kLd + r;
-    constexpr int w = kTileRows * kLd;
+    const float *from = (const float *)lds + t * LdsA<RT, 2>::kLd + r;
     const f32x4 s = (*(const f32x4 *)from + *(const f32x4 *)(from + w)) +
                     (*(const f32x4 *)(from + 2 * w) + *(const f32x4 *)(from + 3 * w));
     if (r0 + r < rp)
-      *(f32x4 *)(p.part + ((int64_t)group * p.rows + L.rows[t]) * rp + r0 + r) = s;
+      *(f32x4 *)(p.part + ((int64_t)group * p.rows + row0 + tile_rows[t]) * rp + r0 + r) = s;
   }
 }
 
@@ -303,59 +334,56 @@ __device__ __forceinline__ float from16(uint16_t b, bool bf16) {
   return bf16 ? bf16_bits_to_f32(b) : f16_bits_to_f32(b);
 }
 
-// Eight consecutive columns of a row: base as loaded (BASE: 0 none, 2 a 16-bit
-// type, 4 fp32; the size is a template argument so that no branch stands
-// between the loads), as fp32, and stored.
+// Four consecutive columns of a row: base as loaded (BASE: bytes of a value, 0
+// for no base; a template argument so that no branch stands between the loads),
+// as fp32, and stored.
 template <int BASE>
-struct Raw8 {
-  u32x4 v[BASE == 4 ? 2 : 1];
+struct Raw4 {
+  typedef uint32_t type __attribute__((ext_vector_type(2)));
 };
+template <>
+struct Raw4<4> {
+  typedef u32x4 type;
+};
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 template <int BASE>
-__device__ __forceinline__ void load8(const void *p, int64_t i, Raw8<BASE> &r) {
-  if constexpr (BASE == 4) {
-    r.v[0] = *(gu32x4p)(uintptr_t)((const float *)p + i);
-    r.v[1] = *(gu32x4p)(uintptr_t)((const float *)p + i + 4);
-  } else if constexpr (BASE == 2) {
-    r.v[0] = *(gu32x4p)(uintptr_t)((const uint16_t *)p + i);
-  }
+__device__ __forceinline__ typename Raw4<BASE>::type load4(const void *p, uint32_t i) {
+  if constexpr (BASE == 0) return (u32x2){0, 0};
+  else return load_at<typename Raw4<BASE>::type>(p, i * BASE);
 }
 template <int BASE>
-__device__ __forceinline__ void widen8(const Raw8<BASE> &r, int dtype, float (&v)[8]) {
+__device__ __forceinline__ void widen4(const typename Raw4<BASE>::type &r, int dtype,
+                                       float (&v)[4]) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
+  for (int j = 0; j < 4; ++j) {
     if constexpr (BASE == 4) {
-      const uint32_t w = r.v[j >> 2][j & 3];
+      const uint32_t w = r[j];
       v[j] = __builtin_bit_cast(float, w);
     } else if constexpr (BASE == 2) {
-      const uint32_t w = r.v[0][j >> 1];
+      const uint32_t w = r[j >> 1];
       v[j] = from16((uint16_t)(w >> (16 * (j & 1))), dtype == 2);
     } else {
       v[j] = 0.0f;
     }
   }
 }
-__device__ __forceinline__ void store8(void *p, int dtype, int64_t i, const float (&v)[8]) {
+__device__ __forceinline__ void store4(void *p, int dtype, uint32_t i, const float (&v)[4]) {
   if (dtype == 3) {
-    *(f32x4 *)((float *)p + i) = (f32x4){v[0], v[1], v[2], v[3]};
-    *(f32x4 *)((float *)p + i + 4) = (f32x4){v[4], v[5], v[6], v[7]};
+    typedef f32x4 __attribute__((address_space(1))) *gp;
+    *(gp)((uintptr_t)p + i * 4) = (f32x4){v[0], v[1], v[2], v[3]};
   } else {
-    u32x4 q;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) q[j] = f32x2_to_out16(v[2 * j], v[2 * j + 1], dtype == 2);
-    *(u32x4 *)((uint16_t *)p + i) = q;
+    typedef u32x2 __attribute__((address_space(1))) *gp;
+    *(gp)((uintptr_t)p + i * 2) = (u32x2){f32x2_to_out16(v[0], v[1], dtype == 2),
+                                          f32x2_to_out16(v[2], v[3], dtype == 2)};
   }
 }
-
-// Ranks go through the second product in chunks of eight. Chunk c holds ranks
-// 8 c .. 8 c + 7; where R is no multiple of 8 (and at least 8), the last one
-// starts at R - 8 instead, so that its load stays inside B's row, and leaves
-// out the ranks that the chunk before it has. Loads of 16 bytes need no
-// alignment here. First rank of a chunk:
-__device__ __forceinline__ int chunk_start(int R, int c) {
-  return R >= 8 ? min(8 * c, R - 8) : 8 * c;
+// The window's first row of base and out.
+__device__ __forceinline__ const void *window_base(const LoraParams &p, int bytes) {
+  return (const char *)p.base + (int64_t)blockIdx.z * kWindow * p.ldbase * bytes;
 }
-typedef f32x4 f32x4_a4 __attribute__((aligned(4)));
-typedef const u32x4 __attribute__((address_space(1), aligned(2))) *gu32x4p_a2;
+__device__ __forceinline__ void *window_out(const LoraParams &p) {
+  return (char *)p.out + (int64_t)blockIdx.z * kWindow * p.ldout * (p.out_dtype == 3 ? 4 : 2);
+}
 
 // s as MFMA operands. The matrix cores take 16-bit inputs, so s is written as
 // a sum of 16-bit terms, each the rounded rest of the ones before: two fp16
@@ -369,30 +397,25 @@ typedef const u32x4 __attribute__((address_space(1), aligned(2))) *gu32x4p_a2;
 // term of the same 16, against B given twice. The third term, if any, is a
 // second MFMA with zeros in the other half.
 template <int RT>
-struct SLds {
-  static constexpr int kLd = RT * 16 + 8;  // 16-byte rows, spread over the banks
+struct LdsB {
+  static constexpr int kLd = RT * 16 + 8;       // entries of a row: spread over the banks
+  static constexpr int kRow = RT * 32 + 16;     // bytes of a column's B
   uint16_t s[3][kTileRows][kLd];
   int e[kTileRows];
+  __align__(16) char b[4][64 * kRow];           // a wave's 64 columns
 };
 
+// The rows' sums from the workspace, four lanes to a row. kParts groups at a
+// time are asked for together; groups and ranks that are not there repeat one
+// that is, and are not added.
 template <int RT, bool BF16>
 __device__ __forceinline__ void load_s(const LoraParams &p, const LoraTile *tile, int nrows,
-                                       int ad, int ra, int groups, SLds<RT> &S) {
+                                       int ad, int ra, int groups, LdsB<RT> &S) {
   const int t = threadIdx.x >> 2, q = threadIdx.x & 3;
-  if (t >= nrows) return;  // columns of the tile past its rows are not used
+  if (t >= nrows) return;  // rows of the tile past its end are not used
   const int rp = (p.R + 15) & ~15;
   const float scale = p.scale ? p.scale[ad] : 1.0f;
-  const float *from = p.part + (int64_t)tile->rows[t] * rp;
-  // slots 4 (q + 4 j) .. + 3 hold ranks r0[j] .. + 3, those from lo[j] on
-  int r0[RT], lo[RT];
-#pragma unroll
-  for (int j = 0; j < RT; ++j) {
-    const int slot = 4 * (q + 4 * j);
-    lo[j] = slot & ~7;
-    r0[j] = chunk_start(p.R, slot >> 3) + (slot & 4);
-  }
-  // kParts groups' sums at a time are asked for together; groups and ranks that
-  // are not there repeat one that is, and are not added
+  const float *from = p.part + (int64_t)(blockIdx.z * kWindow + tile->rows[t]) * rp;
   constexpr int kParts = RT <= 2 ? 4 : RT == 4 ? 2 : 1;
   f32x4 sum[RT];
 #pragma unroll
@@ -402,9 +425,11 @@ __device__ __forceinline__ void load_s(const LoraParams &p, const LoraTile *tile
 #pragma unroll
     for (int i = 0; i < kParts; ++i)
 #pragma unroll
-      for (int j = 0; j < RT; ++j)
-        part[i][j] = *(const f32x4_a4 *)(from + (int64_t)min(i0 + i, groups - 1) * p.rows * rp +
-                                         (lo[j] < ra ? r0[j] : 0));
+      for (int j = 0; j < RT; ++j) {
+        const int r = 4 * (q + 4 * j);
+        part[i][j] = *(const f32x4 *)(from + (int64_t)min(i0 + i, groups - 1) * p.rows * rp +
+                                      (r < ra ? r : 0));
+      }
 #pragma unroll
     for (int i = 0; i < kParts; ++i)
 #pragma unroll
@@ -417,8 +442,7 @@ __device__ __forceinline__ void load_s(const LoraParams &p, const LoraTile *tile
   for (int j = 0; j < RT; ++j)
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const int r = r0[j] + u;
-      v[j][u] = r >= lo[j] && r < ra ? sum[j][u] * scale : 0.0f;
+      v[j][u] = 4 * (q + 4 * j) + u < ra ? sum[j][u] * scale : 0.0f;
       big = fmaxf(big, fabsf(v[j][u]));
     }
   big = fmaxf(big, __shfl_xor(big, 1, 64));
@@ -447,170 +471,195 @@ __device__ __forceinline__ void load_s(const LoraParams &p, const LoraTile *tile
   if (q == 0) S.e[t] = e;
 }
 
-// What a wave loads for 32 columns of TT * 16 rows: the base and B. Columns
-// are the MFMA rows: row m of MFMA i is column n0 + 8 (m / 4) + 4 i + m % 4, so
-// that a lane's results of both MFMAs are 8 consecutive columns of one row, and
-// the four lanes of a row 32: one run of 64 bytes (16-bit) or 128 (fp32).
-template <int RT, int TT, int BASE>
-struct Columns {
-  Raw8<BASE> base[TT];
-  u32x4 b[2][RT];
-};
-
-// WIDE: R >= 8. Below that B's rows are shorter than a load and are read one by
-// one. Columns past N repeat the last ones, so no branch stands before a load.
-template <int RT, int TT, int BASE, bool WIDE>
-__device__ __forceinline__ void load_columns(const LoraParams &p, const int (&rows)[4],
-                                             const uint16_t *b, int n0, Columns<RT, TT, BASE> &u) {
-  const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
+// One wave: columns n0 .. n1 - 1, 64 at a time, of TT * 16 tile rows from t0.
+// Tile rows are the MFMA rows and column n + 4 (lane % 16) + i is column
+// (lane % 16) of MFMA i, so that a lane's results of four MFMAs are four
+// consecutive columns of a row and 16 lanes have 64: base and output move in
+// runs of 128 bytes (16-bit) or 256 (fp32) with neighbouring lanes side by side.
+// (With tile rows as the MFMA columns, neighbouring lanes held different rows
+// and every load and store touched 64 cache lines: 128 us instead of 90 on
+// 16384 x 4096.) B's rows of 64 columns are one run of memory: they are loaded
+// as such and turned round in LDS. The loads of the next 64 columns are under
+// way while these are worked on.
+template <int RT, int TT, bool BF16, int BASE>
+__device__ __forceinline__ void lora_b_columns(const LoraParams &p, const LoraTile *tile, int nrows,
+                                               int t0, int ad, int ra, int groups, int n0, int n1,
+                                               LdsB<RT> &S) {
+  typedef typename Raw4<BASE>::type raw_t;
+  const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15, wave = wave_id();
+  constexpr int kRow = LdsB<RT>::kRow;
+  // the lane's rows t0 + 16 j + 4 g + r, as element offsets of base and out;
+  // past the end the last row again
+  uint32_t bo[TT][4], oo[TT][4];
 #pragma unroll
   for (int j = 0; j < TT; ++j)
-    load8<BASE>(p.base, (int64_t)rows[j] * p.ldbase + min(n0 + 8 * g, p.N - 8), u.base[j]);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int n = min(n0 + 8 * (c >> 2) + 4 * i + (c & 3), p.N - 1);
-    const uint16_t *at = b + (int64_t)n * p.R;
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      if constexpr (WIDE) {
-        u.b[i][rt] = *(gu32x4p_a2)(uintptr_t)(at + chunk_start(p.R, 2 * rt + (g & 1)));
-      } else {
-        uint32_t w[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = at[min(j, p.R - 1)];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) u.b[i][rt][j] = w[2 * j] | (w[2 * j + 1] << 16);
-      }
+    for (int r = 0; r < 4; ++r) {
+      const uint32_t row = tile->rows[t0 + 16 * j + 4 * g + r];
+      bo[j][r] = row * (uint32_t)p.ldbase;
+      oo[j][r] = row * (uint32_t)p.ldout;
     }
-  }
-}
-
-// The rest of the work on those columns. mask: some ranks of a chunk are not
-// used or not its own; their B counts as zero whatever it holds (0 * NaN).
-template <int RT, int TT, bool BF16, int BASE>
-__device__ __forceinline__ void use_columns(const LoraParams &p, const int (&rows)[4], int nrows,
-                                            int ra, bool mask, bool three, int n0,
-                                            Columns<RT, TT, BASE> &u, const SLds<RT> &S) {
-  const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
-  if (mask) {
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      const int lo = 8 * (2 * rt + (g & 1)), r = chunk_start(p.R, 2 * rt + (g & 1));
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const bool off = r + j < lo || r + j >= ra;
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          if (off) u.b[i][rt][j >> 1] &= j & 1 ? 0x0000ffffu : 0xffff0000u;
-      }
-    }
-  }
-  f32x4 acc[2][TT];
-#pragma unroll
-  for (int j = 0; j < TT; ++j) {
-    acc[0][j] = acc[1][j] = (f32x4){0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      const int at = rt * 16 + 8 * (g & 1);
-      const u32x4 s = *(const u32x4 *)&S.s[g >> 1][j * 16 + c][at];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) acc[i][j] = mfma16<BF16>(u.b[i][rt], s, acc[i][j]);
-      if (BF16 && three) {
-        u32x4 s3 = *(const u32x4 *)&S.s[2][j * 16 + c][at];
-        if (g >> 1) s3 = (u32x4){0, 0, 0, 0};
-#pragma unroll
-        for (int i = 0; i < 2; ++i) acc[i][j] = mfma16<BF16>(u.b[i][rt], s3, acc[i][j]);
-      }
-    }
-  }
-  const int n = n0 + 8 * g;
-#pragma unroll
-  for (int j = 0; j < TT; ++j) {
-    const int t = j * 16 + c;
-    float v[8];
-    widen8<BASE>(u.base[j], p.base_dtype, v);
-    if (t >= nrows || n >= p.N) continue;
-    const int e = S.e[t];
-#pragma unroll
-    for (int w = 0; w < 8; ++w) v[w] += ldexpf(acc[w >> 2][j][w & 3], e);
-    store8(p.out, p.out_dtype, (int64_t)rows[j] * p.ldout + n, v);
-  }
-}
-
-// A wave's columns n0 .. n1 - 1 of TT * 16 rows, 32 at a time: the next 32 are
-// on their way while the present ones are multiplied and stored, and the first
-// are asked for before s is.
-template <int RT, int TT, bool BF16, int BASE, bool WIDE>
-__device__ __forceinline__ void lora_b_tile(const LoraParams &p, const LoraTile *tile, int nrows,
-                                            int ad, int ra, int groups, int n0, int n1,
-                                            SLds<RT> &S) {
-  int rows[4];  // tile row j * 16 + lane % 16; past the end the last row again
-#pragma unroll
-  for (int j = 0; j < TT; ++j) rows[j] = tile->rows[j * 16 + (threadIdx.x & 15)];
+  const void *base0 = window_base(p, BASE);
+  void *out0 = window_out(p);
   const uint16_t *b = p.b + (int64_t)ad * p.N * p.R;
-  const bool mask = ra != RT * 16, three = p.out_dtype == 3;
-  Columns<RT, TT, BASE> u[2];
-  load_columns<RT, TT, BASE, WIDE>(p, rows, b, n0, u[0]);
+  char *stage = S.b[wave];
+  u32x4 bn[2 * RT];
+  raw_t base[TT][4];
+  // 16-byte chunk m * 64 + lane of the columns' run of B; N - n is a multiple
+  // of 8, so the run is one of whole chunks. Chunks past its end repeat the last.
+  auto fetch_b = [&](int n) {
+    n = min(n, p.N - 8);
+    const int last = min(64, p.N - n) * p.R / 8 - 1;
+#pragma unroll
+    for (int m = 0; m < 2 * RT; ++m)
+      bn[m] = load_at<u32x4>(b, (uint32_t)(n * p.R * 2 + min(m * 64 + lane, last) * 16));
+  };
+  auto fetch_base = [&](int j, int r, int n) {
+    base[j][r] = load4<BASE>(base0, bo[j][r] + min(n + 4 * c, p.N - 4));
+  };
+  // into LDS, a column's ranks kRow apart
+  const int row_chunks = p.R / 8, inverse = 65536 / max(row_chunks, 1) + 1;
+  auto put_b = [&] {
+    if (p.R % 8 == 0) {
+#pragma unroll
+      for (int m = 0; m < 2 * RT; ++m) {
+        const int q = m * 64 + lane, row = (q * inverse) >> 16;  // q / row_chunks: q < 1024
+        if (q < 8 * p.R) *(u32x4 *)(stage + row * kRow + (q - row * row_chunks) * 16) = bn[m];
+      }
+    } else {  // chunks that span columns: value by value
+      int l = lane;
+      asm volatile("" : "+v"(l));  // the places are computed here, not kept in registers
+#pragma unroll
+      for (int m = 0; m < 2 * RT; ++m) {
+        int row = (m * 64 + l) * 8 / p.R, r = (m * 64 + l) * 8 - row * p.R;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {
+          if (row < 64) *(uint16_t *)(stage + row * kRow + r * 2) = (uint16_t)(bn[m][w >> 1] >> (16 * (w & 1)));
+          r = r + 1 == p.R ? 0 : r + 1;
+          row += r == 0 ? 1 : 0;
+        }
+      }
+    }
+  };
+  constexpr bool kNextB = RT <= 4;  // 128 ranks: no registers for the next B
+  if (kNextB) fetch_b(n0);
+#pragma unroll
+  for (int j = 0; j < TT; ++j)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) fetch_base(j, r, n0);
   load_s<RT, BF16>(p, tile, nrows, ad, ra, groups, S);
   __syncthreads();
+  const bool three = BF16 && p.out_dtype == 3;
+
   for (int n = n0; n < n1; n += 64) {
-    load_columns<RT, TT, BASE, WIDE>(p, rows, b, n + 32, u[1]);
+    if (!kNextB) fetch_b(n);
+    put_b();
+    if (kNextB) fetch_b(n + 64);
     __builtin_amdgcn_sched_barrier(0);
-    use_columns<RT, TT, BF16, BASE>(p, rows, nrows, ra, mask, three, n, u[0], S);
-    if (n + 32 >= n1) break;
-    load_columns<RT, TT, BASE, WIDE>(p, rows, b, n + 64, u[0]);
-    __builtin_amdgcn_sched_barrier(0);
-    use_columns<RT, TT, BF16, BASE>(p, rows, nrows, ra, mask, three, n + 32, u[1], S);
+    f32x4 acc[4][TT];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < TT; ++j) acc[i][j] = (f32x4){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      const int r = rt * 16 + 8 * (g & 1);
+      if (RT >= 4) __builtin_amdgcn_sched_barrier(0);
+      u32x4 bv[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) bv[i] = *(const u32x4 *)(stage + (4 * c + i) * kRow + r * 2);
+      // ranks from ra on give zero whatever B, or LDS behind it, holds there
+      if (rt * 16 + 16 > ra) {
+#pragma unroll
+        for (int w = 0; w < 8; ++w)
+          if (r + w >= ra) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) bv[i][w >> 1] &= w & 1 ? 0x0000ffffu : 0xffff0000u;
+          }
+      }
+#pragma unroll
+      for (int j = 0; j < TT; ++j) {
+        const u32x4 s = *(const u32x4 *)&S.s[g >> 1][t0 + j * 16 + c][r];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i][j] = mfma16<BF16>(s, bv[i], acc[i][j]);
+        if (three) {
+          u32x4 s3 = *(const u32x4 *)&S.s[2][t0 + j * 16 + c][r];
+          if (g >> 1) s3 = (u32x4){0, 0, 0, 0};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[i][j] = mfma16<BF16>(s3, bv[i], acc[i][j]);
+        }
+      }
+    }
+    const int col = n + 4 * c;
+#pragma unroll
+    for (int j = 0; j < TT; ++j)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int t = t0 + 16 * j + 4 * g + r;
+        const int e = S.e[t];
+        float v[4];
+        widen4<BASE>(base[j][r], p.base_dtype, v);
+        fetch_base(j, r, n + 64);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] += ldexpf(acc[i][j][r], e);
+        if (t < nrows && col < p.N) store4(out0, p.out_dtype, oo[j][r] + col, v);
+      }
   }
 }
 
-// Rows without an adapter: out = base (or zeros), 16 loads of a thread together.
+// Rows without an adapter: out = base (or zeros), 8 loads of a thread together.
 template <int BASE>
 __device__ __forceinline__ void copy_rows(const LoraParams &p, const LoraTile *tile, int nrows,
                                           int n0, int n1) {
   if (p.base == p.out || n0 >= n1) return;
-  const int per_row = (n1 - n0) / 8, total = nrows * per_row;
+  const int per_row = (n1 - n0) / 4, total = nrows * per_row;
   for (int i0 = threadIdx.x; i0 < total; i0 += 256 * 8) {
-    Raw8<BASE> r[8];
-    int64_t row[8];
-    int n[8];
+    typename Raw4<BASE>::type raw[8];
+    uint32_t row[8], n[8];
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
       const int i = min(i0 + 256 * u, total - 1), t = i / per_row;
       row[u] = tile->rows[t];
-      n[u] = n0 + (i - t * per_row) * 8;
+      n[u] = n0 + (i - t * per_row) * 4;
     }
 #pragma unroll
-    for (int u = 0; u < 8; ++u) load8<BASE>(p.base, row[u] * p.ldbase + n[u], r[u]);
+    for (int u = 0; u < 8; ++u)
+      raw[u] = load4<BASE>(window_base(p, BASE), row[u] * (uint32_t)p.ldbase + n[u]);
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
-      float v[8];
-      widen8<BASE>(r[u], p.base_dtype, v);
-      if (i0 + 256 * u < total) store8(p.out, p.out_dtype, row[u] * p.ldout + n[u], v);
+      float v[4];
+      widen4<BASE>(raw[u], p.base_dtype, v);
+      if (i0 + 256 * u < total)
+        store4(window_out(p), p.out_dtype, row[u] * (uint32_t)p.ldout + n[u], v);
     }
   }
 }
 
-// Workgroup (tile, 4 * per_wave columns, window).
-template <int RT, bool BF16, int BASE, bool WIDE>
-__global__ void __launch_bounds__(256) lora_b_kernel(LoraParams p, int per_wave, int groups) {
-  __shared__ __align__(16) SLds<RT> S;
+// Workgroup (tile, `cols` columns, window). Up to 32 rows: each wave takes a
+// quarter of the columns; more: two waves take each half of the rows.
+template <int RT, bool BF16, int BASE>
+__global__ void __launch_bounds__(256) lora_b_kernel(LoraParams p, int cols, int groups) {
+  __shared__ LdsB<RT> S;
   const LoraTile *tile = p.tiles + (int64_t)blockIdx.z * gridDim.x + blockIdx.x;
   const int ad = uload_i32(&tile->adapter), nrows = uload_i32(&tile->nrows);
   if (ad < 0) return;
-  const int c0 = blockIdx.y * 4 * per_wave;
+  const int c0 = blockIdx.y * cols, c1 = min(c0 + cols, p.N);
   const int ra = ad < p.adapters ? used_rank(p, ad) : 0;
   if (ra == 0) {
-    copy_rows<BASE>(p, tile, nrows, c0, min(c0 + 4 * per_wave, p.N));
+    copy_rows<BASE>(p, tile, nrows, c0, c1);
     return;
   }
-  const int n0 = c0 + per_wave * wave_id(), n1 = min(n0 + per_wave, p.N);
-  if (nrows <= 16)
-    lora_b_tile<RT, 1, BF16, BASE, WIDE>(p, tile, nrows, ad, ra, groups, n0, n1, S);
-  else if (nrows <= 32)
-    lora_b_tile<RT, 2, BF16, BASE, WIDE>(p, tile, nrows, ad, ra, groups, n0, n1, S);
-  else
-    lora_b_tile<RT, 4, BF16, BASE, WIDE>(p, tile, nrows, ad, ra, groups, n0, n1, S);
+  const int wave = wave_id();
+  if (nrows > 32) {
+    const int n0 = c0 + cols / 2 * (wave >> 1), n1 = min(n0 + cols / 2, p.N);
+    lora_b_columns<RT, 2, BF16, BASE>(p, tile, nrows, 32 * (wave & 1), ad, ra, groups, n0, n1, S);
+  } else {
+    const int n0 = c0 + cols / 4 * wave, n1 = min(n0 + cols / 4, p.N);
+    if (nrows <= 16)
+      lora_b_columns<RT, 1, BF16, BASE>(p, tile, nrows, 0, ad, ra, groups, n0, n1, S);
+    else
+      lora_b_columns<RT, 2, BF16, BASE>(p, tile, nrows, 0, ad, ra, groups, n0, n1, S);
+  }
 }
 
 int windows(int rows) { return (rows + kWindow - 1) / kWindow; }
@@ -623,41 +672,47 @@ int tile_slots(int rows, int adapters) {
 
 template <int RT>
 void run_a(const LoraParams &p, hipStream_t s) {
+  // 64 ranks: four waves with two slices each, so that two workgroups fit on a
+  // CU (6144 -> 64 ranks, 4001 rows: 18.5 us; eight waves 21.7). Fewer ranks:
+  // eight waves, which finish a few rows sooner (16 ranks, one row: 5.6 us, four
+  // waves 6.1; 16384 rows: no difference).
+  constexpr int W = RT == 4 ? 4 : 8;
   const int chunks = (p.R + RT * 16 - 1) / (RT * 16);
-  const dim3 grid(tile_slots(p.rows, p.adapters), lora_groups(p.K) * chunks, windows(p.rows));
-  if (p.bf16) hipLaunchKernelGGL((lora_a_kernel<RT, true>), grid, dim3(kThreadsA), 0, s, p, chunks);
-  else hipLaunchKernelGGL((lora_a_kernel<RT, false>), grid, dim3(kThreadsA), 0, s, p, chunks);
+  const dim3 grid(tile_slots(p.rows, p.adapters), lora_groups(p.K) * chunks * 2, windows(p.rows));
+  if (p.bf16)
+    hipLaunchKernelGGL((lora_a_kernel<RT, W, true>), grid, dim3(64 * W), 0, s, p, chunks);
+  else
+    hipLaunchKernelGGL((lora_a_kernel<RT, W, false>), grid, dim3(64 * W), 0, s, p, chunks);
 }
 
-template <int RT, bool BF16, int BASE, bool WIDE>
+template <int RT, bool BF16, int BASE>
 void run_b(const LoraParams &p, hipStream_t s) {
-  // Columns of a wave, in units of 32. Every workgroup reads its rows' sums, 4
-  // groups R bytes a row; `need` units make that at most half of the base and
-  // output it moves, and are taken as far as 256 workgroups are left. Beyond
-  // that, enough that no more than about 1024 are launched.
-  const int64_t units = (p.N + 127) / 128 * ((p.rows + kTileRows - 1) / kTileRows);
+  // Columns of a workgroup, in units of 256. Every workgroup reads its rows'
+  // sums, 4 groups R bytes a row; `need` units make that at most half of the
+  // base and output it moves, and are taken as far as 128 workgroups are left.
+  // Beyond that, enough that no more than about 1024 are launched.
+  const int64_t units = (p.N + 255) / 256 * (int64_t)((p.rows + kTileRows - 1) / kTileRows);
   const int64_t row_bytes = BASE + (p.out_dtype == 3 ? 4 : 2);
-  const int64_t need = 8 * lora_groups(p.K) * lora_padded_rank(p.R) / (row_bytes * 128) + 1;
-  int64_t u = need < units / 256 ? need : units / 256;
+  const int64_t need = 8 * lora_groups(p.K) * lora_padded_rank(p.R) / (row_bytes * 256) + 1;
+  int64_t u = need < units / 128 ? need : units / 128;
   if (u < units / 1024) u = units / 1024;
-  const int per_wave = 32 * (int)(u < 1 ? 1 : u > 8 ? 8 : u);
-  const dim3 grid(tile_slots(p.rows, p.adapters), (p.N + 4 * per_wave - 1) / (4 * per_wave),
-                  windows(p.rows));
-  hipLaunchKernelGGL((lora_b_kernel<RT, BF16, BASE, WIDE>), grid, dim3(256), 0, s, p, per_wave,
+  const int cols = 256 * (int)(u < 1 ? 1 : u > 8 ? 8 : u);
+  const dim3 grid(tile_slots(p.rows, p.adapters), (p.N + cols - 1) / cols, windows(p.rows));
+  hipLaunchKernelGGL((lora_b_kernel<RT, BF16, BASE>), grid, dim3(256), 0, s, p, cols,
                      lora_groups(p.K));
 }
 
-template <int RT, bool WIDE>
+template <int RT>
 void run_b(const LoraParams &p, hipStream_t s) {
   const int base = !p.base ? 0 : p.base_dtype == 3 ? 4 : 2;
   if (p.bf16) {
-    if (base == 0) run_b<RT, true, 0, WIDE>(p, s);
-    else if (base == 2) run_b<RT, true, 2, WIDE>(p, s);
-    else run_b<RT, true, 4, WIDE>(p, s);
+    if (base == 0) run_b<RT, true, 0>(p, s);
+    else if (base == 2) run_b<RT, true, 2>(p, s);
+    else run_b<RT, true, 4>(p, s);
   } else {
-    if (base == 0) run_b<RT, false, 0, WIDE>(p, s);
-    else if (base == 2) run_b<RT, false, 2, WIDE>(p, s);
-    else run_b<RT, false, 4, WIDE>(p, s);
+    if (base == 0) run_b<RT, false, 0>(p, s);
+    else if (base == 2) run_b<RT, false, 2>(p, s);
+    else run_b<RT, false, 4>(p, s);
   }
 }
 
@@ -677,11 +732,10 @@ hipError_t launch_lora_a(const LoraParams &p, hipStream_t s) {
 }
 
 hipError_t launch_lora_b(const LoraParams &p, hipStream_t s) {
-  if (p.R < 8) run_b<1, false>(p, s);
-  else if (p.R <= 16) run_b<1, true>(p, s);
-  else if (p.R <= 32) run_b<2, true>(p, s);
-  else if (p.R <= 64) run_b<4, true>(p, s);
-  else run_b<8, true>(p, s);
+  if (p.R <= 16) run_b<1>(p, s);
+  else if (p.R <= 32) run_b<2>(p, s);
+  else if (p.R <= 64) run_b<4>(p, s);
+  else run_b<8>(p, s);
   return hipGetLastError();
 }
 
