@@ -17,6 +17,9 @@ namespace exl3 {
 namespace {
 
 constexpr int kRowsPerWg = 16;  // 256 threads
+// balance_kernel: 32 rows at a time, 16 above 512 experts (its sums are
+// registers, and eight waves would not have enough)
+constexpr int balance_threads(int I) { return I <= 8 ? 512 : 256; }
 constexpr float kFltMax = 3.40282346638528859812e+38f;
 constexpr float kNegInf = -__builtin_inff();
 
@@ -260,15 +263,25 @@ __global__ void __launch_bounds__(256) route_topk_kernel(RouterParams p) {
   // Lane j keeps picks j and j + 16.
   int pick[2] = {-1, -1};
   for (int k = 0; k < p.topk; ++k) {
-    key_t best = s[0];
+    // four chains side by side: one chain of 4 I dependent steps is most of a
+    // small call's time
+    key_t top[4];
 #pragma unroll
-    for (int j = 1; j < 4 * I; ++j) best = kmax(best, s[j]);
-    best = row_max(best);
-    int e = 0x7fffffff;
+    for (int v = 0; v < 4; ++v) {
+      top[v] = s[v];
 #pragma unroll
-    for (int j = 4 * I - 1; j >= 0; --j)
-      e = s[j] == best ? 64 * (j >> 2) + 4 * lane + (j & 3) : e;
-    e = row_min(e);
+      for (int j = 1; j < I; ++j) top[v] = kmax(top[v], s[4 * j + v]);
+    }
+    const key_t best = row_max(kmax(kmax(top[0], top[1]), kmax(top[2], top[3])));
+    int first[4];
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      first[v] = 0x7fffffff;
+#pragma unroll
+      for (int j = I - 1; j >= 0; --j)
+        first[v] = s[4 * j + v] == best ? 64 * j + 4 * lane + v : first[v];
+    }
+    const int e = row_min(min(min(first[0], first[1]), min(first[2], first[3])));
     const bool some = best > (key_t)kNegInf;
 #pragma unroll
     for (int j = 0; j < 4 * I; ++j)
@@ -319,19 +332,20 @@ __device__ __forceinline__ void take_ids(const RouterParams &p, bool in, int lan
 }
 
 // ----------------------------------------------------------------- balance
-// Workgroup b sums rows 16 b + 16 gridDim n + its 16 row groups: probabilities
+// Workgroup b sums every gridDim-th 32 rows from the 32 b-th on: probabilities
 // in registers, counts by LDS integer atomics (exact in any order). Its sums
 // go to part_prob[b][E], part_count[b][E] and part_tokens[b]; they are added
 // in the order of b by balance_sum_kernel, so the same call gives the same
 // bytes.
 // The next rows' loads are under way while a row is summed up.
 template <int I, int DT>
-__global__ void __launch_bounds__(256) balance_kernel(RouterParams p) {
+__global__ void __launch_bounds__(balance_threads(I)) balance_kernel(RouterParams p) {
+  constexpr int kThreads = balance_threads(I), kWaves = kThreads / 64, kRows = kThreads / 16;
   __shared__ int s_count[64 * I];
-  __shared__ float s_prob[4][64 * I];
+  __shared__ float s_prob[kWaves][64 * I];
   __shared__ int s_tokens;
   const int lane = threadIdx.x & 15, wave = threadIdx.x >> 6;
-  for (int e = threadIdx.x; e < 64 * I; e += 256) s_count[e] = 0;
+  for (int e = threadIdx.x; e < 64 * I; e += kThreads) s_count[e] = 0;
   if (threadIdx.x == 0) s_tokens = 0;
   __syncthreads();
   float acc[4 * I];
@@ -339,8 +353,8 @@ __global__ void __launch_bounds__(256) balance_kernel(RouterParams p) {
   for (int j = 0; j < 4 * I; ++j) acc[j] = 0.0f;
   const bool sig = p.sigmoid;
   int tokens = 0;
-  int64_t row = (int64_t)blockIdx.x * kRowsPerWg + (threadIdx.x >> 4);
-  const int64_t step = (int64_t)gridDim.x * kRowsPerWg;
+  int64_t row = (int64_t)blockIdx.x * kRows + (threadIdx.x >> 4);
+  const int64_t step = (int64_t)gridDim.x * kRows;
   const int64_t last = p.rows - 1;
   int64_t next_id[2];
   RawRow<I, DT> next;
@@ -348,7 +362,7 @@ __global__ void __launch_bounds__(256) balance_kernel(RouterParams p) {
     load_ids(p, min(row, last), lane, next_id);
     load_raw<I, DT>(p, min(row, last) * p.ld_logits, lane, next);
   }
-  for (int64_t r0 = (int64_t)blockIdx.x * kRowsPerWg; r0 <= last; r0 += step, row += step) {
+  for (int64_t r0 = (int64_t)blockIdx.x * kRows; r0 <= last; r0 += step, row += step) {
     int id[2];
     take_ids(p, row <= last, lane, next_id, id);
     float l[4 * I];
@@ -374,7 +388,7 @@ __global__ void __launch_bounds__(256) balance_kernel(RouterParams p) {
     tokens += live ? 1 : 0;
   }
   if (lane == 0 && tokens) atomicAdd(&s_tokens, tokens);
-  // the wave's four rows, then the four waves
+  // the wave's four rows, then the waves
 #pragma unroll
   for (int j = 0; j < 4 * I; ++j) {
     acc[j] += __shfl_xor(acc[j], 16, 64);
@@ -382,9 +396,11 @@ __global__ void __launch_bounds__(256) balance_kernel(RouterParams p) {
     if ((threadIdx.x & 48) == 0) s_prob[wave][64 * (j >> 2) + 4 * lane + (j & 3)] = acc[j];
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < p.E; e += 256) {
-    p.part_prob[(int64_t)blockIdx.x * p.E + e] =
-        (s_prob[0][e] + s_prob[1][e]) + (s_prob[2][e] + s_prob[3][e]);
+  for (int e = threadIdx.x; e < p.E; e += kThreads) {
+    float sum = s_prob[0][e];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) sum += s_prob[w][e];
+    p.part_prob[(int64_t)blockIdx.x * p.E + e] = sum;
     p.part_count[(int64_t)blockIdx.x * p.E + e] = s_count[e];
   }
   if (threadIdx.x == 0) {
@@ -481,20 +497,6 @@ __global__ void __launch_bounds__(256) route_backward_kernel(RouterParams p) {
   __shared__ __align__(16) float s_add[kRowsPerWg][64 * I];
   const int lane = threadIdx.x & 15;
   const bool sig = p.sigmoid;
-  // the balance loss: c f_e
-  float cf[4 * I];
-#pragma unroll
-  for (int j = 0; j < 4 * I; ++j) cf[j] = 0.0f;
-  if (p.count) {
-    const float T = (float)*p.tokens;
-    const float c = T > 0.0f ? (p.dloss ? *p.dloss : 1.0f) * p.coef * (float)p.E / T : 0.0f;
-    const float cn = T > 0.0f ? c / (T * (float)p.topk) : 0.0f;
-#pragma unroll
-    for (int j = 0; j < 4 * I; ++j) {
-      const int e = 64 * (j >> 2) + 4 * lane + (j & 3);
-      cf[j] = e < p.E ? cn * (float)p.count[e] : 0.0f;
-    }
-  }
   const bool need_all = p.count != nullptr || (!sig && !p.renorm);
   const bool two = p.topk > 16;  // else no lane has a second entry
   float *add = s_add[threadIdx.x >> 4];
@@ -517,6 +519,20 @@ __global__ void __launch_bounds__(256) route_backward_kernel(RouterParams p) {
     }
   };
   fetch(min(row, last));
+  // the balance loss: c f_e
+  float cf[4 * I];
+#pragma unroll
+  for (int j = 0; j < 4 * I; ++j) cf[j] = 0.0f;
+  if (p.count) {
+#pragma unroll
+    for (int j = 0; j < 4 * I; ++j)  // past E: the last expert's, times p = 0
+      cf[j] = (float)p.count[min(64 * (j >> 2) + 4 * lane + (j & 3), p.E - 1)];
+    const float T = (float)*p.tokens;
+    const float c = T > 0.0f ? (p.dloss ? *p.dloss : 1.0f) * p.coef * (float)p.E / T : 0.0f;
+    const float cn = T > 0.0f ? c / (T * (float)p.topk) : 0.0f;
+#pragma unroll
+    for (int j = 0; j < 4 * I; ++j) cf[j] *= cn;
+  }
   for (int64_t r0 = (int64_t)blockIdx.x * kRowsPerWg; r0 <= last; r0 += step, row += step) {
     int id[2];
     take_ids(p, row <= last, lane, next_id, id);
@@ -682,12 +698,14 @@ hipError_t launch_route_topk(const RouterParams &p, hipStream_t s) {
   });
 }
 
-int balance_blocks(int rows) { return (int)max(1u, min(row_groups(rows), 512u)); }
+int balance_blocks(int rows) {
+  return (int)max(1u, min((row_groups(rows) + 1) / 2, 512u));  // two workgroups to a CU
+}
 
 hipError_t launch_balance(const RouterParams &p, hipStream_t s) {
   return by_row(p, [&](auto I, auto D) {
     hipLaunchKernelGGL((balance_kernel<decltype(I)::value, decltype(D)::value>), dim3(p.nblk),
-                       dim3(256), 0, s, p);
+                       dim3(balance_threads(decltype(I)::value)), 0, s, p);
   });
 }
 

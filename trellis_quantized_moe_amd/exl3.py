@@ -6,6 +6,7 @@ built, every call raises; there is no fallback path.
 """
 
 import ctypes
+import functools
 import os
 
 import numpy as np
@@ -142,7 +143,7 @@ def _check(status):
 def _stream():
     # the current stream's handle without building a Stream object (0.3 us
     # instead of 2.8: a third of a small call's time on the host)
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _p(t):
@@ -401,6 +402,7 @@ def alloc_balance(num_experts, device="cuda"):
     }
 
 
+@functools.lru_cache(maxsize=1024)
 def balance_workspace_size(rows, num_experts):
     return lib().exl3_balance_workspace_size(rows, num_experts)
 
@@ -460,6 +462,7 @@ def exl3_route_backward(logits, ids, dw=None, scoring="softmax", renorm=True, sc
     return dlogits
 
 
+@functools.lru_cache(maxsize=1024)
 def lora_workspace_size(rows, in_f, rank, num_adapters):
     return lib().exl3_lora_workspace_size(rows, in_f, rank, num_adapters)
 
