@@ -921,7 +921,8 @@ RouterParams router_params(const exl3_router *r, const void *logits, int32_t log
   RouterParams p{};
   p.logits = logits;
   p.logits_dtype = logits_dtype;  // EXL3_F16, BF16, F32 are the kernels' 1, 2, 3
-  p.vec4 = ld_logits % 4 == 0 && aligned_to(logits, 4 * float_size(logits_dtype));
+  p.vec4 = r->num_experts % 4 == 0 && ld_logits % 4 == 0 &&
+           aligned_to(logits, 4 * float_size(logits_dtype));
   p.ld_logits = ld_logits;
   p.rows = rows;
   p.E = r->num_experts;

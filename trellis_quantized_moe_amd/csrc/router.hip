@@ -16,6 +16,8 @@ namespace exl3 {
 
 namespace {
 
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
 constexpr int kRowsPerWg = 16;  // 256 threads
 // balance_kernel: 32 rows at a time, 16 above 512 experts (its sums are
 // registers, and eight waves would not have enough)
@@ -79,14 +81,11 @@ __device__ __forceinline__ float load_as_f32(const void *p, int dtype, int64_t i
 __device__ __forceinline__ float clean(float l) {
   return l == l ? fminf(l, kFltMax) : kNegInf;
 }
-__device__ __forceinline__ int64_t load_id(const void *p, int i64, int64_t i) {
-  return i64 ? ((const int64_t *)p)[i] : (int64_t)((const int32_t *)p)[i];
-}
 
 // The lane's share of a row as loaded: four fp32 or four 16-bit logits a block.
 template <int DT>
 struct Raw {
-  typedef uint2 type;
+  typedef uint32_t type __attribute__((ext_vector_type(2)));
 };
 template <>
 struct Raw<3> {
@@ -96,49 +95,54 @@ template <int I, int DT>
 using RawRow = typename Raw<DT>::type[I];
 
 // Loads of the row whose first element has index `at` (not waited for). vec4:
-// every group of four starts on a multiple of four elements and is one load; a
-// group that runs past E is read element by element, -inf behind the end.
+// E is a multiple of four and every group of four starts on one, so a group is
+// one load. Groups and values past E read the last ones again: no branch stands
+// between the loads, which would make each wait for the one before.
 template <int I, int DT>
 __device__ __forceinline__ void load_raw(const RouterParams &p, int64_t at, int lane,
                                          RawRow<I, DT> &raw) {
   typedef typename Raw<DT>::type raw_t;
-  const raw_t *q = (const raw_t *)((const char *)p.logits + (at + 4 * lane) * (DT == 3 ? 4 : 2));
+  if (p.vec4) {
+    const char *q = (const char *)p.logits + at * (DT == 3 ? 4 : 2);
 #pragma unroll
-  for (int j = 0; j < I; ++j) {
-    const int e0 = 64 * j + 4 * lane;
-    if (p.vec4 && (64 * (j + 1) <= p.E || e0 + 4 <= p.E)) {
-      raw[j] = q[16 * j];
-    } else if constexpr (DT == 3) {
+    for (int j = 0; j < I; ++j)
+      raw[j] = *(const raw_t *)(q + min(64 * j + 4 * lane, p.E - 4) * (DT == 3 ? 4 : 2));
+  } else {
+    asm volatile("" : "+v"(lane));  // 4 I indexes are computed here, not kept in registers
 #pragma unroll
-      for (int v = 0; v < 4; ++v)
-        raw[j][v] = e0 + v < p.E ? ((const uint32_t *)p.logits)[at + e0 + v] : 0xff800000u;
-    } else {
+    for (int j = 0; j < I; ++j) {
       uint32_t w[4];
 #pragma unroll
-      for (int v = 0; v < 4; ++v)
-        w[v] = e0 + v < p.E ? ((const uint16_t *)p.logits)[at + e0 + v]
-                            : DT == 2 ? 0xff80u : 0xfc00u;
-      raw[j] = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+      for (int v = 0; v < 4; ++v) {
+        const int64_t e = at + min(64 * j + 4 * lane + v, p.E - 1);
+        if constexpr (DT == 3) w[v] = ((const uint32_t *)p.logits)[e];
+        else w[v] = ((const uint16_t *)p.logits)[e];
+      }
+      if constexpr (DT == 3) raw[j] = (raw_t){w[0], w[1], w[2], w[3]};
+      else raw[j] = (raw_t){w[0] | (w[1] << 16), w[2] | (w[3] << 16)};
     }
   }
 }
 template <int I, int DT>
-__device__ __forceinline__ void unpack_row(const RawRow<I, DT> &raw, float (&l)[4 * I]) {
+__device__ __forceinline__ void unpack_row(const RouterParams &p, int lane,
+                                           const RawRow<I, DT> &raw, float (&l)[4 * I]) {
 #pragma unroll
   for (int j = 0; j < I; ++j) {
-    if constexpr (DT == 3) {
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
+    for (int v = 0; v < 4; ++v) {
+      if constexpr (DT == 3) {
         const uint32_t b = raw[j][v];
         l[4 * j + v] = clean(__builtin_bit_cast(float, b));
-      }
-    } else {
-      const uint32_t w[2] = {raw[j].x, raw[j].y};
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const uint16_t b = (uint16_t)(w[v >> 1] >> (16 * (v & 1)));
+      } else {
+        const uint32_t w = raw[j][v >> 1];
+        const uint16_t b = (uint16_t)(w >> (16 * (v & 1)));
         l[4 * j + v] = clean(DT == 2 ? bf16_bits_to_f32(b) : f16_bits_to_f32(b));
       }
+    }
+    if (64 * (j + 1) > p.E) {  // the block that E ends in
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+        l[4 * j + v] = 64 * j + 4 * lane + v < p.E ? l[4 * j + v] : kNegInf;
     }
   }
 }
@@ -233,7 +237,7 @@ __global__ void __launch_bounds__(256) route_topk_kernel(RouterParams p) {
   RawRow<I, DT> raw;
   load_raw<I, DT>(p, at, lane, raw);
   float l[4 * I];
-  unpack_row<I, DT>(raw, l);
+  unpack_row<I, DT>(p, lane, raw, l);
   if (!live) {
 #pragma unroll
     for (int j = 0; j < 4 * I; ++j) l[j] = kNegInf;
@@ -312,23 +316,42 @@ __global__ void __launch_bounds__(256) route_topk_kernel(RouterParams p) {
 }
 
 // The row's IDs j = lane and lane + 16, as loaded (a lane without one reads
-// the row's last, so no branch stands around a load and the loads that follow
-// it) and as experts: -1 for none, outside [0, E), or past the row's topk. At
-// most 16 IDs leave the second one out.
+// the row's last) and as experts: -1 for none, outside [0, E), or past the
+// row's topk. At most 16 IDs leave the second one out. Nothing is made of a
+// loaded value here, behind a branch on its type: the wait for it would come
+// before the loads that follow.
 __device__ __forceinline__ void load_ids(const RouterParams &p, int64_t row, int lane,
-                                         int64_t (&raw)[2]) {
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    raw[h] = -1;
-    if (h == 1 && p.topk <= 16) break;
-    raw[h] = load_id(p.ids, p.ids_i64, row * p.topk + min(lane + 16 * h, p.topk - 1));
-  }
+                                         uint32_t (&raw)[4]) {
+  const int64_t at = row * p.topk;
+  auto one = [&](int64_t i, uint32_t &lo, uint32_t &hi) {
+    if (p.ids_i64) {
+      const u32x2 v = ((const u32x2 *)p.ids)[i];
+      lo = v[0];
+      hi = v[1];
+    } else {
+      lo = ((const uint32_t *)p.ids)[i];
+    }
+  };
+  one(at + min(lane, p.topk - 1), raw[0], raw[1]);
+  if (p.topk > 16) one(at + min(lane + 16, p.topk - 1), raw[2], raw[3]);
 }
 __device__ __forceinline__ void take_ids(const RouterParams &p, bool in, int lane,
-                                         const int64_t (&raw)[2], int (&id)[2]) {
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-    id[h] = in && lane + 16 * h < p.topk && (uint64_t)raw[h] < (uint64_t)p.E ? (int)raw[h] : -1;
+                                         const uint32_t (&raw)[4], int (&id)[2]) {
+  auto one = [&](int k, uint32_t lo, uint32_t hi) {
+    const bool ok = lo < (uint32_t)p.E && (!p.ids_i64 || hi == 0);
+    return in && k < p.topk && ok ? (int)lo : -1;
+  };
+  id[0] = one(lane, raw[0], raw[1]);
+  id[1] = one(lane + 16, raw[2], raw[3]);
+}
+// A value of a [rows][topk] array, as loaded and as fp32.
+__device__ __forceinline__ uint32_t load_bits(const void *p, int dtype, int64_t i) {
+  return dtype == 3 ? ((const uint32_t *)p)[i] : ((const uint16_t *)p)[i];
+}
+__device__ __forceinline__ float bits_to_f32(uint32_t b, int dtype) {
+  return dtype == 3   ? __builtin_bit_cast(float, b)
+         : dtype == 2 ? bf16_bits_to_f32((uint16_t)b)
+                      : f16_bits_to_f32((uint16_t)b);
 }
 
 // ----------------------------------------------------------------- balance
@@ -356,7 +379,7 @@ __global__ void __launch_bounds__(balance_threads(I)) balance_kernel(RouterParam
   int64_t row = (int64_t)blockIdx.x * kRows + (threadIdx.x >> 4);
   const int64_t step = (int64_t)gridDim.x * kRows;
   const int64_t last = p.rows - 1;
-  int64_t next_id[2];
+  uint32_t next_id[4] = {0, 0, 0, 0};
   RawRow<I, DT> next;
   if (last >= 0) {
     load_ids(p, min(row, last), lane, next_id);
@@ -366,7 +389,7 @@ __global__ void __launch_bounds__(balance_threads(I)) balance_kernel(RouterParam
     int id[2];
     take_ids(p, row <= last, lane, next_id, id);
     float l[4 * I];
-    unpack_row<I, DT>(next, l);
+    unpack_row<I, DT>(p, lane, next, l);
     if (r0 + step <= last) {
       load_ids(p, min(row + step, last), lane, next_id);
       load_raw<I, DT>(p, min(row + step, last) * p.ld_logits, lane, next);
@@ -505,8 +528,8 @@ __global__ void __launch_bounds__(256) route_backward_kernel(RouterParams p) {
   const int64_t step = (int64_t)gridDim.x * kRowsPerWg;
   const int64_t last = p.rows - 1;
   // the next rows' loads are under way while a row is worked on
-  int64_t next_id[2];
-  float next_g[2] = {0.0f, 0.0f};
+  uint32_t next_id[4] = {0, 0, 0, 0};
+  uint32_t next_g[2] = {0, 0};
   RawRow<I, DT> next;
   auto fetch = [&](int64_t r) {
     load_raw<I, DT>(p, r * p.ld_logits, lane, next);
@@ -514,8 +537,7 @@ __global__ void __launch_bounds__(256) route_backward_kernel(RouterParams p) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       if (!p.dw || (h == 1 && !two)) break;
-      next_g[h] =
-          load_as_f32(p.dw, p.dw_dtype, r * p.topk + min(lane + 16 * h, p.topk - 1));
+      next_g[h] = load_bits(p.dw, p.dw_dtype, r * p.topk + min(lane + 16 * h, p.topk - 1));
     }
   };
   fetch(min(row, last));
@@ -536,9 +558,9 @@ __global__ void __launch_bounds__(256) route_backward_kernel(RouterParams p) {
   for (int64_t r0 = (int64_t)blockIdx.x * kRowsPerWg; r0 <= last; r0 += step, row += step) {
     int id[2];
     take_ids(p, row <= last, lane, next_id, id);
-    float g[2] = {next_g[0], next_g[1]};
+    float g[2] = {bits_to_f32(next_g[0], p.dw_dtype), bits_to_f32(next_g[1], p.dw_dtype)};
     float l[4 * I];
-    unpack_row<I, DT>(next, l);
+    unpack_row<I, DT>(p, lane, next, l);
     if (r0 + step <= last) fetch(min(row + step, last));
     const bool live = row_any(id[0] >= 0 || id[1] >= 0);
     const float m = shift(sig, row_max(max_of(l)));
