@@ -168,7 +168,7 @@ enum exl3_kernel_id {
   EXL3_K_EXPERTS = 8, /* 128-row tiles: gate/up and down of a single pass in one launch, or one
                          launch of the passes pipelined across launches */
   EXL3_K_ROUTE = 9, EXL3_K_BALANCE = 10, EXL3_K_BALANCE_SUM = 11, EXL3_K_ROUTE_BACKWARD = 12,
-  EXL3_K_LORA_A = 13, EXL3_K_LORA_B = 14
+  EXL3_K_LORA_A = 13, EXL3_K_LORA_B = 14, EXL3_K_LORA = 15 /* both in one */
 };
 typedef struct exl3_profile {
   void **events;        /* host: 2 * cap event handles (hipEvent_t) */

@@ -487,6 +487,21 @@ def test_lora_rows_are_independent_of_their_company():
         assert torch.equal(part, full[lo:hi]), (lo, hi)
 
 
+def test_lora_rows_are_the_same_bytes_in_one_launch_and_two():
+    """Rank 16 over a long K: few rows take two launches, many take one."""
+    g = torch.Generator().manual_seed(12)
+    rows, K, N, R, n = 4100, 8456, 200, 13, 3
+    x = torch.randn(rows, K, generator=g).half().to(DEV)
+    a = torch.randn(n, R, K, generator=g).half().to(DEV)
+    b = torch.randn(n, N, R, generator=g).half().to(DEV)
+    ids = torch.randint(-1, n, (rows,), generator=g).to(DEV)
+    with exl3.Profile(8) as p:
+        full = exl3.exl3_lora(x, a, b, ids, out_dtype=torch.float32)
+        part = exl3.exl3_lora(x[1900:2200], a, b, ids[1900:2200], out_dtype=torch.float32)
+    assert [k for k, _ in p.records] == ["lora", "lora_a", "lora_b"]
+    assert torch.equal(part, full[1900:2200])
+
+
 def test_lora_ids_outside_32_bits():
     x, a, b = (torch.ones(s, device=DEV, dtype=torch.float16) for s in ((4, 8), (1, 1, 8),
                                                                          (1, 8, 1)))
@@ -571,8 +586,8 @@ def test_host_tensors_and_rows_zero():
 def test_timing_records_name_the_launches():
     with exl3.Profile(16) as p:
         _all_operators(_step(1))
-    assert [n for n, _ in p.records] == ["lora_a", "lora_b", "route_topk", "balance",
-                                         "balance_sum", "route_backward"]
+    assert [n for n, _ in p.records] == ["lora", "route_topk", "balance", "balance_sum",
+                                         "route_backward"]
 
 
 # ----------------------------------------------------------------- together

@@ -1144,6 +1144,10 @@ int32_t exl3_lora(const exl3_lora_adapters *ad, const uint16_t *x, int32_t x_dty
   p.part = (float *)ws;
   p.tiles = at<LoraTile>(ws, align_up(4 * (size_t)lora_groups(p.K) * (size_t)rows *
                                       (size_t)lora_padded_rank(p.R)));
+  if (lora_one(p)) {
+    ProfScope ps(prof, st, EXL3_K_LORA);
+    return launch_lora_one(p, st) == hipSuccess ? EXL3_OK : EXL3_E_LAUNCH;
+  }
   {
     ProfScope ps(prof, st, EXL3_K_LORA_A);
     if (launch_lora_a(p, st) != hipSuccess) return EXL3_E_LAUNCH;

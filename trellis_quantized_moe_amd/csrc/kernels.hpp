@@ -223,6 +223,8 @@ hipError_t launch_route_backward(const RouterParams &p, hipStream_t s);
 int lora_groups(int K);
 int lora_padded_rank(int R);
 size_t lora_tiles(int rows, int adapters);
+bool lora_one(const LoraParams &p);  // whether the call takes one launch
+hipError_t launch_lora_one(const LoraParams &p, hipStream_t s);
 hipError_t launch_lora_a(const LoraParams &p, hipStream_t s);
 hipError_t launch_lora_b(const LoraParams &p, hipStream_t s);
 

@@ -1,15 +1,16 @@
 // Low-rank adapters of many requests beside a shared projection:
 //   out_t = base_t + scale_a (x_t A_a^T) B_a^T,   a = ids[t]
-// in two launches. lora_a writes s = x A^T (fp32, R values a row) to the
-// workspace; lora_b multiplies s by B^T, adds the base and stores.
+// Many rows take two launches: lora_a writes s = x A^T (fp32, R values a row)
+// to the workspace; lora_b multiplies s by B^T, adds the base and stores. Few
+// rows take one, lora_kernel, whose workgroups each form the s they need.
 //
-// Tiles. A tile is up to 64 rows of one adapter. Every workgroup of lora_a
-// finds its tile by itself: rows are taken in windows of 2048, and the
-// workgroup counts its window's IDs per adapter, scans the tile counts and
-// collects its rows (plan_tile), so that no planning launch goes before it and
-// rows need not be sorted. The first workgroup of a tile leaves it in the
-// workspace for lora_b. Rows without an adapter are one more bucket, whose
-// tiles lora_b copies.
+// Tiles. A tile is up to 64 rows of one adapter (16 in lora_kernel). Every
+// workgroup of lora_a and lora_kernel finds its tile by itself: rows are taken
+// in windows of 2048, and the workgroup counts its window's IDs per adapter,
+// scans the tile counts and collects its rows (plan_tile), so that no planning
+// launch goes before it and rows need not be sorted. The first workgroup of a
+// tile leaves it in the workspace for lora_b. Rows without an adapter are one
+// more bucket, whose tiles are copied.
 //
 // A row's bytes depend on that row alone: the K axis is cut the same way in
 // every call (slices of 256 inputs, eight to a group, groups in ascending
@@ -54,8 +55,8 @@ __device__ __forceinline__ int wave_scan(int v) {
 // Tile `tile` of window `win`: its adapter (p.adapters: rows without one; -1:
 // the window has fewer tiles) and its rows, counted from the window's first,
 // in L.rows[0 .. nrows). Called by
-// all threads of a workgroup of W waves.
-template <int W>
+// all threads of a workgroup of W waves; TR: rows of a tile.
+template <int W, int TR>
 __device__ __forceinline__ int plan_tile(const LoraParams &p, int win, int tile, PlanLds &L,
                                          int &nrows) {
   constexpr int kThreads = 64 * W, kChunks = kWindow / kThreads;
@@ -101,13 +102,13 @@ __device__ __forceinline__ int plan_tile(const LoraParams &p, int win, int tile,
   int ad = -1, skip = 0, size = 0;
   for (int b0 = 0, before = 0; b0 <= p.adapters; b0 += 64) {
     const int rows = b0 + lane <= p.adapters ? L.count[b0 + lane] : 0;
-    const int tiles = (rows + kTileRows - 1) / kTileRows;
+    const int tiles = (rows + TR - 1) / TR;
     const int end = before + wave_scan(tiles);
     const uint64_t past = __ballot(end > tile);
     if (past) {
       const int l = __ffsll((long long)past) - 1;
       ad = b0 + l;
-      skip = (tile - (__shfl(end, l, 64) - __shfl(tiles, l, 64))) * kTileRows;
+      skip = (tile - (__shfl(end, l, 64) - __shfl(tiles, l, 64))) * TR;
       size = __shfl(rows, l, 64);
       break;
     }
@@ -116,7 +117,7 @@ __device__ __forceinline__ int plan_tile(const LoraParams &p, int win, int tile,
   ad = __builtin_amdgcn_readfirstlane(ad);
   if (ad < 0) return -1;
   skip = __builtin_amdgcn_readfirstlane(skip);
-  nrows = min(kTileRows, __builtin_amdgcn_readfirstlane(size) - skip);
+  nrows = min(TR, __builtin_amdgcn_readfirstlane(size) - skip);
   // the bucket's rows in order, from number `skip` on
   uint64_t hit[kChunks];
 #pragma unroll
@@ -133,7 +134,7 @@ __device__ __forceinline__ int plan_tile(const LoraParams &p, int win, int tile,
   for (int i = 0; i < kChunks; ++i) {
     const int at = __builtin_amdgcn_readlane(before, i * W + wave) +
                    __popcll(hit[i] & ((1ull << lane) - 1)) - skip;
-    if (a[i] == ad && at >= 0 && at < kTileRows) L.rows[at] = i * kThreads + tid;
+    if (a[i] == ad && at >= 0 && at < TR) L.rows[at] = i * kThreads + tid;
   }
   __syncthreads();
   return ad;
@@ -294,7 +295,7 @@ __global__ void __launch_bounds__(64 * W) lora_a_kernel(LoraParams p, int chunks
   __shared__ PlanLds L;
   __shared__ __align__(16) char lds[kStages > kSums ? kStages : kSums];
   int nrows = 0;
-  const int ad = plan_tile<W>(p, blockIdx.z, blockIdx.x, L, nrows);
+  const int ad = plan_tile<W, kTileRows>(p, blockIdx.z, blockIdx.x, L, nrows);
   if (blockIdx.y == 0) {
     LoraTile *tile = p.tiles + (int64_t)blockIdx.z * gridDim.x + blockIdx.x;
     if (threadIdx.x == 0) {
@@ -396,46 +397,21 @@ __device__ __forceinline__ void *window_out(const LoraParams &p) {
 // One MFMA takes 32 inner values: the first term of 16 ranks and the second
 // term of the same 16, against B given twice. The third term, if any, is a
 // second MFMA with zeros in the other half.
-template <int RT>
+// TR: rows of the tile, W: waves.
+template <int RT, int TR, int W>
 struct LdsB {
-  static constexpr int kLd = RT * 16 + 8;       // entries of a row: spread over the banks
-  static constexpr int kRow = RT * 32 + 16;     // bytes of a column's B
-  uint16_t s[3][kTileRows][kLd];
-  int e[kTileRows];
-  __align__(16) char b[4][64 * kRow];           // a wave's 64 columns
+  static constexpr int kLd = RT * 16 + 8;    // entries of a row: spread over the banks
+  static constexpr int kRow = RT * 32 + 16;  // bytes of a column's B
+  static constexpr int kStage = W * 64 * kRow;  // every wave's 64 columns
+  uint16_t s[3][TR][kLd];
+  int e[TR];
 };
 
-// The rows' sums from the workspace, four lanes to a row. kParts groups at a
-// time are asked for together; groups and ranks that are not there repeat one
-// that is, and are not added.
-template <int RT, bool BF16>
-__device__ __forceinline__ void load_s(const LoraParams &p, const LoraTile *tile, int nrows,
-                                       int ad, int ra, int groups, LdsB<RT> &S) {
-  const int t = threadIdx.x >> 2, q = threadIdx.x & 3;
-  if (t >= nrows) return;  // rows of the tile past its end are not used
-  const int rp = (p.R + 15) & ~15;
+// Row t of s, four lanes to a row: sum[j] holds ranks 4 (q + 4 j) .. + 3.
+template <int RT, bool BF16, int TR, int W>
+__device__ __forceinline__ void split_s(const LoraParams &p, int t, int q, int ad, int ra,
+                                        const f32x4 (&sum)[RT], LdsB<RT, TR, W> &S) {
   const float scale = p.scale ? p.scale[ad] : 1.0f;
-  const float *from = p.part + (int64_t)(blockIdx.z * kWindow + tile->rows[t]) * rp;
-  constexpr int kParts = RT <= 2 ? 4 : RT == 4 ? 2 : 1;
-  f32x4 sum[RT];
-#pragma unroll
-  for (int j = 0; j < RT; ++j) sum[j] = (f32x4){0.f, 0.f, 0.f, 0.f};
-  for (int i0 = 0; i0 < groups; i0 += kParts) {
-    f32x4 part[kParts][RT];
-#pragma unroll
-    for (int i = 0; i < kParts; ++i)
-#pragma unroll
-      for (int j = 0; j < RT; ++j) {
-        const int r = 4 * (q + 4 * j);
-        part[i][j] = *(const f32x4 *)(from + (int64_t)min(i0 + i, groups - 1) * p.rows * rp +
-                                      (r < ra ? r : 0));
-      }
-#pragma unroll
-    for (int i = 0; i < kParts; ++i)
-#pragma unroll
-      for (int j = 0; j < RT; ++j)
-        if (i0 + i < groups) sum[j] = i0 + i == 0 ? part[i][j] : sum[j] + part[i][j];
-  }
   float v[RT][4];
   float big = 0.0f;
 #pragma unroll
@@ -471,6 +447,39 @@ __device__ __forceinline__ void load_s(const LoraParams &p, const LoraTile *tile
   if (q == 0) S.e[t] = e;
 }
 
+// The rows' sums from the workspace. kParts groups at a time are asked for
+// together; groups and ranks that are not there repeat one that is, and are
+// not added.
+template <int RT, bool BF16>
+__device__ __forceinline__ void load_s(const LoraParams &p, const LoraTile *tile, int nrows,
+                                       int ad, int ra, int groups, LdsB<RT, kTileRows, 4> &S) {
+  const int t = threadIdx.x >> 2, q = threadIdx.x & 3;
+  if (t >= nrows) return;  // rows of the tile past its end are not used
+  const int rp = (p.R + 15) & ~15;
+  const float *from = p.part + (int64_t)(blockIdx.z * kWindow + tile->rows[t]) * rp;
+  constexpr int kParts = RT <= 2 ? 4 : RT == 4 ? 2 : 1;
+  f32x4 sum[RT];
+#pragma unroll
+  for (int j = 0; j < RT; ++j) sum[j] = (f32x4){0.f, 0.f, 0.f, 0.f};
+  for (int i0 = 0; i0 < groups; i0 += kParts) {
+    f32x4 part[kParts][RT];
+#pragma unroll
+    for (int i = 0; i < kParts; ++i)
+#pragma unroll
+      for (int j = 0; j < RT; ++j) {
+        const int r = 4 * (q + 4 * j);
+        part[i][j] = *(const f32x4 *)(from + (int64_t)min(i0 + i, groups - 1) * p.rows * rp +
+                                      (r < ra ? r : 0));
+      }
+#pragma unroll
+    for (int i = 0; i < kParts; ++i)
+#pragma unroll
+      for (int j = 0; j < RT; ++j)
+        if (i0 + i < groups) sum[j] = i0 + i == 0 ? part[i][j] : sum[j] + part[i][j];
+  }
+  split_s<RT, BF16>(p, t, q, ad, ra, sum, S);
+}
+
 // One wave: columns n0 .. n1 - 1, 64 at a time, of TT * 16 tile rows from t0.
 // Tile rows are the MFMA rows and column n + 4 (lane % 16) + i is column
 // (lane % 16) of MFMA i, so that a lane's results of four MFMAs are four
@@ -481,13 +490,14 @@ __device__ __forceinline__ void load_s(const LoraParams &p, const LoraTile *tile
 // 16384 x 4096.) B's rows of 64 columns are one run of memory: they are loaded
 // as such and turned round in LDS. The loads of the next 64 columns are under
 // way while these are worked on.
-template <int RT, int TT, bool BF16, int BASE>
-__device__ __forceinline__ void lora_b_columns(const LoraParams &p, const LoraTile *tile, int nrows,
-                                               int t0, int ad, int ra, int groups, int n0, int n1,
-                                               LdsB<RT> &S) {
+// make_s, called by all threads, leaves s in S.
+template <int RT, int TT, bool BF16, int BASE, int TR, int W, typename F>
+__device__ __forceinline__ void lora_b_columns(const LoraParams &p, const int *tile_rows, int nrows,
+                                               int t0, int ad, int ra, int n0, int n1,
+                                               LdsB<RT, TR, W> &S, char *stages, F make_s) {
   typedef typename Raw4<BASE>::type raw_t;
   const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15, wave = wave_id();
-  constexpr int kRow = LdsB<RT>::kRow;
+  constexpr int kRow = LdsB<RT, TR, W>::kRow;
   // the lane's rows t0 + 16 j + 4 g + r, as element offsets of base and out;
   // past the end the last row again
   uint32_t bo[TT][4], oo[TT][4];
@@ -495,14 +505,14 @@ __device__ __forceinline__ void lora_b_columns(const LoraParams &p, const LoraTi
   for (int j = 0; j < TT; ++j)
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const uint32_t row = tile->rows[t0 + 16 * j + 4 * g + r];
+      const uint32_t row = tile_rows[min(t0 + 16 * j + 4 * g + r, nrows - 1)];
       bo[j][r] = row * (uint32_t)p.ldbase;
       oo[j][r] = row * (uint32_t)p.ldout;
     }
   const void *base0 = window_base(p, BASE);
   void *out0 = window_out(p);
   const uint16_t *b = p.b + (int64_t)ad * p.N * p.R;
-  char *stage = S.b[wave];
+  char *stage = stages + wave * 64 * kRow;
   u32x4 bn[2 * RT];
   raw_t base[TT][4];
   // 16-byte chunk m * 64 + lane of the columns' run of B; N - n is a multiple
@@ -547,8 +557,7 @@ __device__ __forceinline__ void lora_b_columns(const LoraParams &p, const LoraTi
   for (int j = 0; j < TT; ++j)
 #pragma unroll
     for (int r = 0; r < 4; ++r) fetch_base(j, r, n0);
-  load_s<RT, BF16>(p, tile, nrows, ad, ra, groups, S);
-  __syncthreads();
+  make_s();
   const bool three = BF16 && p.out_dtype == 3;
 
   for (int n = n0; n < n1; n += 64) {
@@ -609,17 +618,17 @@ __device__ __forceinline__ void lora_b_columns(const LoraParams &p, const LoraTi
 
 // Rows without an adapter: out = base (or zeros), 8 loads of a thread together.
 template <int BASE>
-__device__ __forceinline__ void copy_rows(const LoraParams &p, const LoraTile *tile, int nrows,
+__device__ __forceinline__ void copy_rows(const LoraParams &p, const int *tile_rows, int nrows,
                                           int n0, int n1) {
   if (p.base == p.out || n0 >= n1) return;
-  const int per_row = (n1 - n0) / 4, total = nrows * per_row;
-  for (int i0 = threadIdx.x; i0 < total; i0 += 256 * 8) {
+  const int per_row = (n1 - n0) / 4, total = nrows * per_row, threads = blockDim.x;
+  for (int i0 = threadIdx.x; i0 < total; i0 += threads * 8) {
     typename Raw4<BASE>::type raw[8];
     uint32_t row[8], n[8];
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
-      const int i = min(i0 + 256 * u, total - 1), t = i / per_row;
-      row[u] = tile->rows[t];
+      const int i = min(i0 + threads * u, total - 1), t = i / per_row;
+      row[u] = tile_rows[t];
       n[u] = n0 + (i - t * per_row) * 4;
     }
 #pragma unroll
@@ -629,7 +638,7 @@ __device__ __forceinline__ void copy_rows(const LoraParams &p, const LoraTile *t
     for (int u = 0; u < 8; ++u) {
       float v[4];
       widen4<BASE>(raw[u], p.base_dtype, v);
-      if (i0 + 256 * u < total)
+      if (i0 + threads * u < total)
         store4(window_out(p), p.out_dtype, row[u] * (uint32_t)p.ldout + n[u], v);
     }
   }
@@ -639,35 +648,88 @@ __device__ __forceinline__ void copy_rows(const LoraParams &p, const LoraTile *t
 // quarter of the columns; more: two waves take each half of the rows.
 template <int RT, bool BF16, int BASE>
 __global__ void __launch_bounds__(256) lora_b_kernel(LoraParams p, int cols, int groups) {
-  __shared__ LdsB<RT> S;
+  __shared__ __align__(16) LdsB<RT, kTileRows, 4> S;
+  __shared__ __align__(16) char stages[LdsB<RT, kTileRows, 4>::kStage];
   const LoraTile *tile = p.tiles + (int64_t)blockIdx.z * gridDim.x + blockIdx.x;
   const int ad = uload_i32(&tile->adapter), nrows = uload_i32(&tile->nrows);
   if (ad < 0) return;
   const int c0 = blockIdx.y * cols, c1 = min(c0 + cols, p.N);
   const int ra = ad < p.adapters ? used_rank(p, ad) : 0;
   if (ra == 0) {
-    copy_rows<BASE>(p, tile, nrows, c0, c1);
+    copy_rows<BASE>(p, tile->rows, nrows, c0, c1);
     return;
   }
+  auto make_s = [&] {
+    load_s<RT, BF16>(p, tile, nrows, ad, ra, groups, S);
+    __syncthreads();
+  };
   const int wave = wave_id();
   if (nrows > 32) {
     const int n0 = c0 + cols / 2 * (wave >> 1), n1 = min(n0 + cols / 2, p.N);
-    lora_b_columns<RT, 2, BF16, BASE>(p, tile, nrows, 32 * (wave & 1), ad, ra, groups, n0, n1, S);
+    lora_b_columns<RT, 2, BF16, BASE>(p, tile->rows, nrows, 32 * (wave & 1), ad, ra, n0, n1, S,
+                                      stages, make_s);
   } else {
     const int n0 = c0 + cols / 4 * wave, n1 = min(n0 + cols / 4, p.N);
     if (nrows <= 16)
-      lora_b_columns<RT, 1, BF16, BASE>(p, tile, nrows, 0, ad, ra, groups, n0, n1, S);
+      lora_b_columns<RT, 1, BF16, BASE>(p, tile->rows, nrows, 0, ad, ra, n0, n1, S, stages, make_s);
     else
-      lora_b_columns<RT, 2, BF16, BASE>(p, tile, nrows, 0, ad, ra, groups, n0, n1, S);
+      lora_b_columns<RT, 2, BF16, BASE>(p, tile->rows, nrows, 0, ad, ra, n0, n1, S, stages, make_s);
   }
 }
 
+// -------------------------------------------------------- both in one launch
+// Up to 16 ranks. Workgroup (tile of 16 rows, `cols` columns, window), eight
+// waves: s over all of K, a group of slices at a time, then the columns. The
+// same sums in the same order as the two launches, so the same bytes, but s
+// never leaves LDS. Workgroups that share a tile each form it.
+template <bool BF16, int BASE>
+__global__ void __launch_bounds__(512) lora_kernel(LoraParams p, int cols) {
+  constexpr int W = kSlices, TR = 16, kLd = LdsA<1, 1>::kLd;
+  // x, A and the sums, and once s is made B's columns
+  constexpr int kBytesA = W * LdsA<1, 1>::kStage, kBytesB = LdsB<1, TR, W>::kStage;
+  static_assert(kBytesA >= 4 * TR * kLd * 4, "the sums take the place of the operands");
+  __shared__ PlanLds L;
+  __shared__ __align__(16) char lds[kBytesA > kBytesB ? kBytesA : kBytesB];
+  __shared__ __align__(16) LdsB<1, TR, W> S;
+  int nrows = 0;
+  const int ad = plan_tile<W, TR>(p, blockIdx.z, blockIdx.x, L, nrows);
+  if (ad < 0) return;
+  const int c0 = blockIdx.y * cols, c1 = min(c0 + cols, p.N);
+  const int ra = ad < p.adapters ? used_rank(p, ad) : 0;
+  if (ra == 0) {
+    copy_rows<BASE>(p, L.rows, nrows, c0, c1);
+    return;
+  }
+  // thread: ranks r .. r + 3 of row t
+  const int t = threadIdx.x >> 2, r = (threadIdx.x & 3) * 4;
+  const bool mine = t < TR;
+  float *sums = (float *)lds + t * kLd + r;
+  constexpr int w = TR * kLd;
+  f32x4 total = {0.f, 0.f, 0.f, 0.f};
+  for (int kg = 0; kg < p.K; kg += kGroup) {
+    if (kg) __syncthreads();  // the sums before are taken
+    lora_a_tile<1, 1, W, BF16>(p, L.rows, nrows, ad, 0, ra, kg, lds);
+    if (mine) {
+      const f32x4 s = (*(const f32x4 *)sums + *(const f32x4 *)(sums + w)) +
+                      (*(const f32x4 *)(sums + 2 * w) + *(const f32x4 *)(sums + 3 * w));
+      total = kg == 0 ? s : total + s;
+    }
+  }
+  auto make_s = [&] {
+    const f32x4 sum[1] = {total};
+    if (t < nrows) split_s<1, BF16>(p, t, threadIdx.x & 3, ad, ra, sum, S);
+    __syncthreads();  // s is there, and the sums' place is free for B
+  };
+  const int n0 = c0 + cols / W * wave_id(), n1 = min(n0 + cols / W, p.N);
+  lora_b_columns<1, 1, BF16, BASE>(p, L.rows, nrows, 0, ad, ra, n0, n1, S, lds, make_s);
+}
+
 int windows(int rows) { return (rows + kWindow - 1) / kWindow; }
-// Tiles a window can have: u buckets in use give at most u + (w - u) / 64.
-int tile_slots(int rows, int adapters) {
+// Tiles a window can have: u buckets in use give at most u + (w - u) / rows.
+int tile_slots(int rows, int adapters, int tile_rows = kTileRows) {
   const int w = rows < kWindow ? rows : kWindow;
   const int u = adapters + 1 < w ? adapters + 1 : w;
-  return u + (w - u) / kTileRows;
+  return u + (w - u) / tile_rows;
 }
 
 template <int RT>
@@ -702,18 +764,34 @@ void run_b(const LoraParams &p, hipStream_t s) {
                      lora_groups(p.K));
 }
 
-template <int RT>
-void run_b(const LoraParams &p, hipStream_t s) {
-  const int base = !p.base ? 0 : p.base_dtype == 3 ? 4 : 2;
-  if (p.bf16) {
-    if (base == 0) run_b<RT, true, 0>(p, s);
-    else if (base == 2) run_b<RT, true, 2>(p, s);
-    else run_b<RT, true, 4>(p, s);
-  } else {
-    if (base == 0) run_b<RT, false, 0>(p, s);
-    else if (base == 2) run_b<RT, false, 2>(p, s);
-    else run_b<RT, false, 4>(p, s);
-  }
+template <bool BF16, int BASE>
+void run_one(const LoraParams &p, hipStream_t s) {
+  // Columns of a workgroup, in units of 512: all of them once there are 192
+  // tiles or so, fewer where that leaves CUs empty (4096 -> 4096, rank 16, one
+  // chunk against eight: 256 rows 17.6 and 10.5 us, 4000 rows 28 and 57)
+  const int tiles = (p.rows + 15) / 16, most = (p.N + 511) / 512;
+  const int chunks = tiles >= 192 ? 1 : 192 / tiles < most ? 192 / tiles : most;
+  const int cols = (most + chunks - 1) / chunks * 512;
+  const dim3 grid(tile_slots(p.rows, p.adapters, 16), (p.N + cols - 1) / cols, windows(p.rows));
+  hipLaunchKernelGGL((lora_kernel<BF16, BASE>), grid, dim3(512), 0, s, p, cols);
+}
+
+// f(16-rank tiles, x in bf16, bytes of a base value)
+template <typename F>
+void by_kind(const LoraParams &p, F f) {
+  auto based = [&](auto rt, auto bf16) {
+    if (!p.base) f(rt, bf16, std::integral_constant<int, 0>());
+    else if (p.base_dtype == 3) f(rt, bf16, std::integral_constant<int, 4>());
+    else f(rt, bf16, std::integral_constant<int, 2>());
+  };
+  auto typed = [&](auto rt) {
+    if (p.bf16) based(rt, std::true_type());
+    else based(rt, std::false_type());
+  };
+  if (p.R <= 16) typed(std::integral_constant<int, 1>());
+  else if (p.R <= 32) typed(std::integral_constant<int, 2>());
+  else if (p.R <= 64) typed(std::integral_constant<int, 4>());
+  else typed(std::integral_constant<int, 8>());
 }
 
 }  // namespace
@@ -724,6 +802,22 @@ size_t lora_tiles(int rows, int adapters) {
   return (size_t)windows(rows) * tile_slots(rows, adapters);
 }
 
+// One launch pays for few ranks: every workgroup reads all of A for 16 rows
+// (in us, one launch and two: 4096 -> 4096 at rank 16, 1 row 9.2 and 9.1, 256
+// rows 10.5 and 14.5, 16384 rows 101 and 108; at rank 64, 18 and 17 at 256 rows,
+// 178 and 145 at 16384), and spares a launch on the host (2.5 us). A long K and
+// few rows leave it too few workgroups for A, which two launches split over K.
+bool lora_one(const LoraParams &p) {
+  return p.R <= 16 && (lora_groups(p.K) <= 4 || p.rows >= 4096);
+}
+hipError_t launch_lora_one(const LoraParams &p, hipStream_t s) {
+  by_kind(p, [&](auto rt, auto bf16, auto base) {
+    if constexpr (decltype(rt)::value == 1)
+      run_one<decltype(bf16)::value, decltype(base)::value>(p, s);
+  });
+  return hipGetLastError();
+}
+
 hipError_t launch_lora_a(const LoraParams &p, hipStream_t s) {
   if (p.R <= 16 || p.rows <= 256) run_a<1>(p, s);
   else if (p.R <= 32) run_a<2>(p, s);
@@ -732,10 +826,9 @@ hipError_t launch_lora_a(const LoraParams &p, hipStream_t s) {
 }
 
 hipError_t launch_lora_b(const LoraParams &p, hipStream_t s) {
-  if (p.R <= 16) run_b<1>(p, s);
-  else if (p.R <= 32) run_b<2>(p, s);
-  else if (p.R <= 64) run_b<4>(p, s);
-  else run_b<8>(p, s);
+  by_kind(p, [&](auto rt, auto bf16, auto base) {
+    run_b<decltype(rt)::value, decltype(bf16)::value, decltype(base)::value>(p, s);
+  });
   return hipGetLastError();
 }
 

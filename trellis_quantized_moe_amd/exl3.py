@@ -117,7 +117,7 @@ _SIGS = {
 KERNEL_NAMES = {1: "route_pack", 2: "rotate", 3: "gemm_gateup", 4: "gemm_down",
                 5: "combine", 6: "gemm_linear", 7: "decode_tiles", 8: "gemm_experts",
                 9: "route_topk", 10: "balance", 11: "balance_sum", 12: "route_backward",
-                13: "lora_a", 14: "lora_b"}
+                13: "lora_a", 14: "lora_b", 15: "lora"}
 
 
 def lib():
