@@ -22,7 +22,7 @@
  *     enqueued [p1 Summary: the device, layout, dtypes, shapes, workspace and
  *     routing are all checked first]. On error
  *     the call returns a negative EXL3_E_* code and enqueues nothing.
- *     rows == 0 is a successful no-op.
+ *     rows == 0 is a successful no-op (exl3_balance_loss: zero results).
  *   - Problems only the device can see (route ID outside [0, E), a stage
  *     with a nonzero scale but a null trellis or a width outside 2..8) drop
  *     the pair / skip the stage and are counted in device status words; the
@@ -58,12 +58,13 @@ enum exl3_status {
   EXL3_OK = 0,
   EXL3_E_NULL = -1,      /* a required pointer is NULL */
   EXL3_E_DTYPE = -2,     /* unsupported dtype enum for that argument */
-  EXL3_E_SHAPE = -3,     /* dimension not a positive multiple of 128, or
-                            gate/up/down shapes inconsistent */
-  EXL3_E_ALIGN = -4,     /* x, out, ws, trellis tensors and projection
-                            tables must be 16-byte aligned; ids, route
-                            weights and route metadata need the natural
-                            alignment of their element type */
+  EXL3_E_SHAPE = -3,     /* dimension not a positive multiple of 128 (of 8:
+                            exl3_lora), gate/up/down shapes inconsistent, or
+                            a row distance out of range */
+  EXL3_E_ALIGN = -4,     /* x, out, base, ws, trellis tensors, adapters and
+                            projection tables must be 16-byte aligned; ids,
+                            logits, route weights and route metadata need
+                            the natural alignment of their element type */
   EXL3_E_DEVICE = -5,    /* a pointer is not device memory of the current
                             device, or no HIP device is usable */
   EXL3_E_WORKSPACE = -6, /* workspace NULL or smaller than *_workspace_size */
@@ -364,8 +365,9 @@ int32_t exl3_route_topk(const exl3_router *router, const void *logits, int32_t l
  * T rows do. With p_te = t_te / (sum of t over the row):
  *   count_e = number of IDs equal to e       prob_e = (sum over rows of p_te) / T
  *   loss = coef * num_experts * sum_e (count_e / (T topk)) * prob_e
- * (T == 0: loss and prob are 0). The router's renorm, scale and bias take no
- * part. Sums run in fp32 in a fixed order: the same call gives the same bytes.
+ * (T == 0: loss and prob are 0; a row that takes part but has no expert left
+ * adds 0 to prob). A t_te below 2^-126 times the row's largest counts as 0. The
+ * router's renorm, scale and bias take no part. Sums run in fp32 in a fixed order: the same call gives the same bytes.
  * ws: exl3_balance_workspace_size(rows, num_experts) bytes, 16-byte aligned;
  * calls that share it must be ordered on one stream.
  * rows == 0 enqueues the zero results.

@@ -328,9 +328,6 @@ __global__ void __launch_bounds__(64 * W) lora_a_kernel(LoraParams p, int chunks
 }
 
 // ------------------------------------------------------------------ s B^T
-__device__ __forceinline__ uint16_t to16(float v, bool bf16) {
-  return bf16 ? f32_to_bf16_bits(v) : f32_to_f16_bits(v);
-}
 __device__ __forceinline__ float from16(uint16_t b, bool bf16) {
   return bf16 ? bf16_bits_to_f32(b) : f16_bits_to_f32(b);
 }
@@ -409,9 +406,8 @@ struct LdsB {
 
 // Row t of s, four lanes to a row: sum[j] holds ranks 4 (q + 4 j) .. + 3.
 template <int RT, bool BF16, int TR, int W>
-__device__ __forceinline__ void split_s(const LoraParams &p, int t, int q, int ad, int ra,
-                                        const f32x4 (&sum)[RT], LdsB<RT, TR, W> &S) {
-  const float scale = p.scale ? p.scale[ad] : 1.0f;
+__device__ __forceinline__ void split_s(int t, int q, float scale, int ra, const f32x4 (&sum)[RT],
+                                        LdsB<RT, TR, W> &S) {
   float v[RT][4];
   float big = 0.0f;
 #pragma unroll
@@ -430,14 +426,14 @@ __device__ __forceinline__ void split_s(const LoraParams &p, int t, int q, int a
   for (int j = 0; j < RT; ++j) {
     uint32_t w[3][2];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      float rest = ldexpf(v[j][u], -e);
+    for (int u = 0; u < 2; ++u) {
+      float lo = ldexpf(v[j][2 * u], -e), hi = ldexpf(v[j][2 * u + 1], -e);
 #pragma unroll
       for (int m = 0; m < (BF16 ? 3 : 2); ++m) {
-        const uint16_t b = to16(rest, BF16);
-        if (u & 1) w[m][u >> 1] |= (uint32_t)b << 16;
-        else w[m][u >> 1] = b;
-        rest = fabsf(rest) < __builtin_inff() ? rest - from16(b, BF16) : 0.0f;
+        const uint32_t b = f32x2_to_out16(lo, hi, BF16);
+        w[m][u] = b;
+        lo = fabsf(lo) < __builtin_inff() ? lo - from16((uint16_t)b, BF16) : 0.0f;
+        hi = fabsf(hi) < __builtin_inff() ? hi - from16((uint16_t)(b >> 16), BF16) : 0.0f;
       }
     }
 #pragma unroll
@@ -451,13 +447,13 @@ __device__ __forceinline__ void split_s(const LoraParams &p, int t, int q, int a
 // together; groups and ranks that are not there repeat one that is, and are
 // not added.
 template <int RT, bool BF16>
-__device__ __forceinline__ void load_s(const LoraParams &p, const LoraTile *tile, int nrows,
-                                       int ad, int ra, int groups, LdsB<RT, kTileRows, 4> &S) {
+__device__ __forceinline__ void load_s(const LoraParams &p, int row, int nrows, float scale, int ra,
+                                       int groups, LdsB<RT, kTileRows, 4> &S) {
   const int t = threadIdx.x >> 2, q = threadIdx.x & 3;
   if (t >= nrows) return;  // rows of the tile past its end are not used
   const int rp = (p.R + 15) & ~15;
-  const float *from = p.part + (int64_t)(blockIdx.z * kWindow + tile->rows[t]) * rp;
-  constexpr int kParts = RT <= 2 ? 4 : RT == 4 ? 2 : 1;
+  const float *from = p.part + (int64_t)(blockIdx.z * kWindow + row) * rp;
+  constexpr int kParts = RT <= 4 ? 4 : 2;
   f32x4 sum[RT];
 #pragma unroll
   for (int j = 0; j < RT; ++j) sum[j] = (f32x4){0.f, 0.f, 0.f, 0.f};
@@ -477,7 +473,7 @@ __device__ __forceinline__ void load_s(const LoraParams &p, const LoraTile *tile
       for (int j = 0; j < RT; ++j)
         if (i0 + i < groups) sum[j] = i0 + i == 0 ? part[i][j] : sum[j] + part[i][j];
   }
-  split_s<RT, BF16>(p, t, q, ad, ra, sum, S);
+  split_s<RT, BF16>(t, q, scale, ra, sum, S);
 }
 
 // One wave: columns n0 .. n1 - 1, 64 at a time, of TT * 16 tile rows from t0.
@@ -490,11 +486,12 @@ __device__ __forceinline__ void load_s(const LoraParams &p, const LoraTile *tile
 // 16384 x 4096.) B's rows of 64 columns are one run of memory: they are loaded
 // as such and turned round in LDS. The loads of the next 64 columns are under
 // way while these are worked on.
-// make_s, called by all threads, leaves s in S.
-template <int RT, int TT, bool BF16, int BASE, int TR, int W, typename F>
-__device__ __forceinline__ void lora_b_columns(const LoraParams &p, const int *tile_rows, int nrows,
-                                               int t0, int ad, int ra, int n0, int n1,
-                                               LdsB<RT, TR, W> &S, char *stages, F make_s) {
+// row_of(i): the tile's row i, past its end any of its rows; make_s, called by
+// all threads, leaves s in S.
+template <int RT, int TT, bool BF16, int BASE, int TR, int W, typename R, typename F>
+__device__ __forceinline__ void lora_b_columns(const LoraParams &p, R row_of, int nrows, int t0,
+                                               int ad, int ra, int n0, int n1, LdsB<RT, TR, W> &S,
+                                               char *stages, F make_s) {
   typedef typename Raw4<BASE>::type raw_t;
   const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15, wave = wave_id();
   constexpr int kRow = LdsB<RT, TR, W>::kRow;
@@ -505,7 +502,7 @@ __device__ __forceinline__ void lora_b_columns(const LoraParams &p, const int *t
   for (int j = 0; j < TT; ++j)
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const uint32_t row = tile_rows[min(t0 + 16 * j + 4 * g + r, nrows - 1)];
+      const uint32_t row = row_of(t0 + 16 * j + 4 * g + r);
       bo[j][r] = row * (uint32_t)p.ldbase;
       oo[j][r] = row * (uint32_t)p.ldout;
     }
@@ -539,14 +536,18 @@ __device__ __forceinline__ void lora_b_columns(const LoraParams &p, const int *t
     } else {  // chunks that span columns: value by value
       int l = lane;
       asm volatile("" : "+v"(l));  // the places are computed here, not kept in registers
+      const int wrap = kRow - 2 * p.R;  // from behind a column's ranks to the next column
 #pragma unroll
       for (int m = 0; m < 2 * RT; ++m) {
-        int row = (m * 64 + l) * 8 / p.R, r = (m * 64 + l) * 8 - row * p.R;
+        const int first = (m * 64 + l) * 8, row = first / p.R;
+        int r = first - row * p.R;
+        char *to = stage + row * kRow + r * 2;
 #pragma unroll
         for (int w = 0; w < 8; ++w) {
-          if (row < 64) *(uint16_t *)(stage + row * kRow + r * 2) = (uint16_t)(bn[m][w >> 1] >> (16 * (w & 1)));
-          r = r + 1 == p.R ? 0 : r + 1;
-          row += r == 0 ? 1 : 0;
+          if (to < stage + 64 * kRow) *(uint16_t *)to = (uint16_t)(bn[m][w >> 1] >> (16 * (w & 1)));
+          const bool end = ++r == p.R;
+          to += end ? wrap + 2 : 2;
+          r = end ? 0 : r;
         }
       }
     }
@@ -580,11 +581,11 @@ __device__ __forceinline__ void lora_b_columns(const LoraParams &p, const int *t
       // ranks from ra on give zero whatever B, or LDS behind it, holds there
       if (rt * 16 + 16 > ra) {
 #pragma unroll
-        for (int w = 0; w < 8; ++w)
-          if (r + w >= ra) {
+        for (int w = 0; w < 4; ++w) {
+          const uint32_t keep = (r + 2 * w < ra ? 0xffffu : 0u) | (r + 2 * w + 1 < ra ? 0xffff0000u : 0u);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) bv[i][w >> 1] &= w & 1 ? 0x0000ffffu : 0xffff0000u;
-          }
+          for (int i = 0; i < 4; ++i) bv[i][w] &= keep;
+        }
       }
 #pragma unroll
       for (int j = 0; j < TT; ++j) {
@@ -651,6 +652,9 @@ __global__ void __launch_bounds__(256) lora_b_kernel(LoraParams p, int cols, int
   __shared__ __align__(16) LdsB<RT, kTileRows, 4> S;
   __shared__ __align__(16) char stages[LdsB<RT, kTileRows, 4>::kStage];
   const LoraTile *tile = p.tiles + (int64_t)blockIdx.z * gridDim.x + blockIdx.x;
+  // the rows are asked for together with what says whether there are any, one
+  // to a lane; lanes get each other's by shuffles
+  const int own_row = tile->rows[threadIdx.x & 63];
   const int ad = uload_i32(&tile->adapter), nrows = uload_i32(&tile->nrows);
   if (ad < 0) return;
   const int c0 = blockIdx.y * cols, c1 = min(c0 + cols, p.N);
@@ -659,22 +663,24 @@ __global__ void __launch_bounds__(256) lora_b_kernel(LoraParams p, int cols, int
     copy_rows<BASE>(p, tile->rows, nrows, c0, c1);
     return;
   }
+  const float scale = p.scale ? uload_f32(p.scale + ad) : 1.0f;
+  auto row_of = [&](int i) { return __shfl(own_row, i, 64); };
+  const int s_row = row_of(threadIdx.x >> 2);
   auto make_s = [&] {
-    load_s<RT, BF16>(p, tile, nrows, ad, ra, groups, S);
+    load_s<RT, BF16>(p, s_row, nrows, scale, ra, groups, S);
     __syncthreads();
   };
+  // one copy of the code for 32 rows, wherever they start: it is run once or
+  // twice, and fetching instructions is part of a small call's time
   const int wave = wave_id();
-  if (nrows > 32) {
-    const int n0 = c0 + cols / 2 * (wave >> 1), n1 = min(n0 + cols / 2, p.N);
-    lora_b_columns<RT, 2, BF16, BASE>(p, tile->rows, nrows, 32 * (wave & 1), ad, ra, n0, n1, S,
-                                      stages, make_s);
-  } else {
-    const int n0 = c0 + cols / 4 * wave, n1 = min(n0 + cols / 4, p.N);
-    if (nrows <= 16)
-      lora_b_columns<RT, 1, BF16, BASE>(p, tile->rows, nrows, 0, ad, ra, n0, n1, S, stages, make_s);
-    else
-      lora_b_columns<RT, 2, BF16, BASE>(p, tile->rows, nrows, 0, ad, ra, n0, n1, S, stages, make_s);
-  }
+  const bool halves = nrows > 32;
+  const int share = halves ? cols / 2 : cols / 4;
+  const int t0 = halves ? 32 * (wave & 1) : 0;
+  const int n0 = c0 + share * (halves ? wave >> 1 : wave), n1 = min(n0 + share, p.N);
+  if (nrows <= 16)
+    lora_b_columns<RT, 1, BF16, BASE>(p, row_of, nrows, 0, ad, ra, n0, n1, S, stages, make_s);
+  else
+    lora_b_columns<RT, 2, BF16, BASE>(p, row_of, nrows, t0, ad, ra, n0, n1, S, stages, make_s);
 }
 
 // -------------------------------------------------------- both in one launch
@@ -700,6 +706,7 @@ __global__ void __launch_bounds__(512) lora_kernel(LoraParams p, int cols) {
     copy_rows<BASE>(p, L.rows, nrows, c0, c1);
     return;
   }
+  const float scale = p.scale ? uload_f32(p.scale + ad) : 1.0f;
   // thread: ranks r .. r + 3 of row t
   const int t = threadIdx.x >> 2, r = (threadIdx.x & 3) * 4;
   const bool mine = t < TR;
@@ -717,11 +724,12 @@ __global__ void __launch_bounds__(512) lora_kernel(LoraParams p, int cols) {
   }
   auto make_s = [&] {
     const f32x4 sum[1] = {total};
-    if (t < nrows) split_s<1, BF16>(p, t, threadIdx.x & 3, ad, ra, sum, S);
+    if (t < nrows) split_s<1, BF16>(t, threadIdx.x & 3, scale, ra, sum, S);
     __syncthreads();  // s is there, and the sums' place is free for B
   };
   const int n0 = c0 + cols / W * wave_id(), n1 = min(n0 + cols / W, p.N);
-  lora_b_columns<1, 1, BF16, BASE>(p, L.rows, nrows, 0, ad, ra, n0, n1, S, lds, make_s);
+  auto row_of = [&](int i) { return L.rows[min(i, nrows - 1)]; };
+  lora_b_columns<1, 1, BF16, BASE>(p, row_of, nrows, 0, ad, ra, n0, n1, S, lds, make_s);
 }
 
 int windows(int rows) { return (rows + kWindow - 1) / kWindow; }
