@@ -154,10 +154,10 @@ struct RouterParams {
 };
 
 // Low-rank adapters (lora.hip).
-struct LoraTile {  // up to 64 rows of one adapter
+struct LoraTile {  // up to 32 rows of one adapter
   int32_t adapter;   // = LoraParams::adapters: rows without one; -1: no tile
   int32_t nrows;
-  int32_t rows[64];  // from the window's first; entries past nrows repeat the last
+  int32_t rows[32];  // from the window's first; entries past nrows repeat the last
 };
 struct LoraParams {
   int K, N, R, adapters;

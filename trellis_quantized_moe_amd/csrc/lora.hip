@@ -4,7 +4,7 @@
 // to the workspace; lora_b multiplies s by B^T, adds the base and stores. Few
 // rows take one, lora_kernel, whose workgroups each form the s they need.
 //
-// Tiles. A tile is up to 64 rows of one adapter (16 in lora_kernel). Every
+// Tiles. A tile is up to 32 rows of one adapter (16 in lora_kernel). Every
 // workgroup of lora_a and lora_kernel finds its tile by itself: rows are taken
 // in windows of 2048, and the workgroup counts its window's IDs per adapter,
 // scans the tile counts and collects its rows (plan_tile), so that no planning
@@ -28,7 +28,7 @@ namespace {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kWindow = 2048;       // rows planned together
-constexpr int kTileRows = 64;       // rows of a tile
+constexpr int kTileRows = 32;       // rows of a tile of two launches
 constexpr int kSlice = 256;         // inputs summed in one run
 constexpr int kSlices = 8;          // slices of a workgroup of lora_a
 constexpr int kGroup = kSlices * kSlice;
@@ -288,7 +288,7 @@ __device__ __forceinline__ void lora_a_tile(const LoraParams &p, const int *tile
   __syncthreads();
 }
 
-// Workgroup (tile, half of its rows, group and rank chunk, window).
+// Workgroup (tile, group and rank chunk, window).
 template <int RT, int W, bool BF16>
 __global__ void __launch_bounds__(64 * W) lora_a_kernel(LoraParams p, int chunks) {
   constexpr int kStages = W * LdsA<RT, 2>::kStage, kSums = 4 * 32 * LdsA<RT, 2>::kLd * 4;
@@ -306,15 +306,12 @@ __global__ void __launch_bounds__(64 * W) lora_a_kernel(LoraParams p, int chunks
       tile->rows[threadIdx.x] = L.rows[min((int)threadIdx.x, max(nrows - 1, 0))];
   }
   if (ad < 0 || ad == p.adapters) return;
-  const int half = blockIdx.y & 1, gc = blockIdx.y >> 1;
-  const int group = gc / chunks, r0 = (gc - group * chunks) * RT * 16;
+  const int group = blockIdx.y / chunks, r0 = (blockIdx.y - group * chunks) * RT * 16;
   const int ra = used_rank(p, ad);
-  const int *tile_rows = L.rows + 32 * half;
-  nrows = min(nrows - 32 * half, 32);
-  if (r0 >= ra || nrows <= 0) return;
+  if (r0 >= ra) return;
   const int kg = group * kGroup;
-  if (nrows <= 16) lora_a_tile<RT, 1, W, BF16>(p, tile_rows, nrows, ad, r0, ra, kg, lds);
-  else lora_a_tile<RT, 2, W, BF16>(p, tile_rows, nrows, ad, r0, ra, kg, lds);
+  if (nrows <= 16) lora_a_tile<RT, 1, W, BF16>(p, L.rows, nrows, ad, r0, ra, kg, lds);
+  else lora_a_tile<RT, 2, W, BF16>(p, L.rows, nrows, ad, r0, ra, kg, lds);
   const int rp = (p.R + 15) & ~15, row0 = blockIdx.z * kWindow;
   const int w = (nrows <= 16 ? 16 : 32) * LdsA<RT, 2>::kLd;
   for (int i = threadIdx.x; i < nrows * RT * 4; i += 64 * W) {
@@ -323,7 +320,7 @@ __global__ void __launch_bounds__(64 * W) lora_a_kernel(LoraParams p, int chunks
     const f32x4 s = (*(const f32x4 *)from + *(const f32x4 *)(from + w)) +
                     (*(const f32x4 *)(from + 2 * w) + *(const f32x4 *)(from + 3 * w));
     if (r0 + r < rp)
-      *(f32x4 *)(p.part + ((int64_t)group * p.rows + row0 + tile_rows[t]) * rp + r0 + r) = s;
+      *(f32x4 *)(p.part + ((int64_t)group * p.rows + row0 + L.rows[t]) * rp + r0 + r) = s;
   }
 }
 
@@ -404,26 +401,28 @@ struct LdsB {
   int e[TR];
 };
 
-// Row t of s, four lanes to a row: sum[j] holds ranks 4 (q + 4 j) .. + 3.
-template <int RT, bool BF16, int TR, int W>
-__device__ __forceinline__ void split_s(int t, int q, float scale, int ra, const f32x4 (&sum)[RT],
-                                        LdsB<RT, TR, W> &S) {
-  float v[RT][4];
+// Row t of s, Q = 4 or 8 lanes to a row: sum[j] holds ranks 4 (q + Q j) .. + 3.
+template <int RT, bool BF16, int Q, int TR, int W>
+__device__ __forceinline__ void split_s(int t, int q, float scale, int ra,
+                                        const f32x4 (&sum)[4 * RT / Q], LdsB<RT, TR, W> &S) {
+  constexpr int J = 4 * RT / Q;
+  float v[J][4];
   float big = 0.0f;
 #pragma unroll
-  for (int j = 0; j < RT; ++j)
+  for (int j = 0; j < J; ++j)
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      v[j][u] = 4 * (q + 4 * j) + u < ra ? sum[j][u] * scale : 0.0f;
+      v[j][u] = 4 * (q + Q * j) + u < ra ? sum[j][u] * scale : 0.0f;
       big = fmaxf(big, fabsf(v[j][u]));
     }
   big = fmaxf(big, __shfl_xor(big, 1, 64));
   big = fmaxf(big, __shfl_xor(big, 2, 64));
+  if (Q == 8) big = fmaxf(big, __shfl_xor(big, 4, 64));
   // fmaxf passes over NaN; the row's finite entries are scaled by the largest
   // (an infinity counts as exponent 255: everything finite stays below 2^14)
   const int e = (int)((__builtin_bit_cast(uint32_t, big) >> 23) & 255u) - 140;
 #pragma unroll
-  for (int j = 0; j < RT; ++j) {
+  for (int j = 0; j < J; ++j) {
     uint32_t w[3][2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
@@ -438,10 +437,14 @@ __device__ __forceinline__ void split_s(int t, int q, float scale, int ra, const
     }
 #pragma unroll
     for (int m = 0; m < (BF16 ? 3 : 2); ++m)
-      *(uint2 *)&S.s[m][t][4 * (q + 4 * j)] = make_uint2(w[m][0], w[m][1]);
+      *(uint2 *)&S.s[m][t][4 * (q + Q * j)] = make_uint2(w[m][0], w[m][1]);
   }
   if (q == 0) S.e[t] = e;
 }
+
+// Lanes that form a row of s in lora_b.
+template <int RT>
+constexpr int kLanesS = RT == 1 ? 4 : 8;
 
 // The rows' sums from the workspace. kParts groups at a time are asked for
 // together; groups and ranks that are not there repeat one that is, and are
@@ -449,34 +452,35 @@ __device__ __forceinline__ void split_s(int t, int q, float scale, int ra, const
 template <int RT, bool BF16>
 __device__ __forceinline__ void load_s(const LoraParams &p, int row, int nrows, float scale, int ra,
                                        int groups, LdsB<RT, kTileRows, 4> &S) {
-  const int t = threadIdx.x >> 2, q = threadIdx.x & 3;
+  constexpr int Q = kLanesS<RT>, J = 4 * RT / Q;
+  const int t = threadIdx.x / Q, q = threadIdx.x % Q;
   if (t >= nrows) return;  // rows of the tile past its end are not used
   const int rp = (p.R + 15) & ~15;
   const float *from = p.part + (int64_t)(blockIdx.z * kWindow + row) * rp;
-  constexpr int kParts = RT <= 4 ? 4 : 2;
-  f32x4 sum[RT];
+  constexpr int kParts = 4;
+  f32x4 sum[J];
 #pragma unroll
-  for (int j = 0; j < RT; ++j) sum[j] = (f32x4){0.f, 0.f, 0.f, 0.f};
+  for (int j = 0; j < J; ++j) sum[j] = (f32x4){0.f, 0.f, 0.f, 0.f};
   for (int i0 = 0; i0 < groups; i0 += kParts) {
-    f32x4 part[kParts][RT];
+    f32x4 part[kParts][J];
 #pragma unroll
     for (int i = 0; i < kParts; ++i)
 #pragma unroll
-      for (int j = 0; j < RT; ++j) {
-        const int r = 4 * (q + 4 * j);
+      for (int j = 0; j < J; ++j) {
+        const int r = 4 * (q + Q * j);
         part[i][j] = *(const f32x4 *)(from + (int64_t)min(i0 + i, groups - 1) * p.rows * rp +
                                       (r < ra ? r : 0));
       }
 #pragma unroll
     for (int i = 0; i < kParts; ++i)
 #pragma unroll
-      for (int j = 0; j < RT; ++j)
+      for (int j = 0; j < J; ++j)
         if (i0 + i < groups) sum[j] = i0 + i == 0 ? part[i][j] : sum[j] + part[i][j];
   }
-  split_s<RT, BF16>(t, q, scale, ra, sum, S);
+  split_s<RT, BF16, Q>(t, q, scale, ra, sum, S);
 }
 
-// One wave: columns n0 .. n1 - 1, 64 at a time, of TT * 16 tile rows from t0.
+// One wave: columns n0 .. n1 - 1, 64 at a time, of the tile's TT * 16 rows.
 // Tile rows are the MFMA rows and column n + 4 (lane % 16) + i is column
 // (lane % 16) of MFMA i, so that a lane's results of four MFMAs are four
 // consecutive columns of a row and 16 lanes have 64: base and output move in
@@ -489,20 +493,20 @@ __device__ __forceinline__ void load_s(const LoraParams &p, int row, int nrows, 
 // row_of(i): the tile's row i, past its end any of its rows; make_s, called by
 // all threads, leaves s in S.
 template <int RT, int TT, bool BF16, int BASE, int TR, int W, typename R, typename F>
-__device__ __forceinline__ void lora_b_columns(const LoraParams &p, R row_of, int nrows, int t0,
-                                               int ad, int ra, int n0, int n1, LdsB<RT, TR, W> &S,
+__device__ __forceinline__ void lora_b_columns(const LoraParams &p, R row_of, int nrows, int ad,
+                                               int ra, int n0, int n1, LdsB<RT, TR, W> &S,
                                                char *stages, F make_s) {
   typedef typename Raw4<BASE>::type raw_t;
   const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15, wave = wave_id();
   constexpr int kRow = LdsB<RT, TR, W>::kRow;
-  // the lane's rows t0 + 16 j + 4 g + r, as element offsets of base and out;
+  // the lane's rows 16 j + 4 g + r, as element offsets of base and out;
   // past the end the last row again
   uint32_t bo[TT][4], oo[TT][4];
 #pragma unroll
   for (int j = 0; j < TT; ++j)
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const uint32_t row = row_of(t0 + 16 * j + 4 * g + r);
+      const uint32_t row = row_of(16 * j + 4 * g + r);
       bo[j][r] = row * (uint32_t)p.ldbase;
       oo[j][r] = row * (uint32_t)p.ldout;
     }
@@ -589,11 +593,11 @@ __device__ __forceinline__ void lora_b_columns(const LoraParams &p, R row_of, in
       }
 #pragma unroll
       for (int j = 0; j < TT; ++j) {
-        const u32x4 s = *(const u32x4 *)&S.s[g >> 1][t0 + j * 16 + c][r];
+        const u32x4 s = *(const u32x4 *)&S.s[g >> 1][j * 16 + c][r];
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[i][j] = mfma16<BF16>(s, bv[i], acc[i][j]);
         if (three) {
-          u32x4 s3 = *(const u32x4 *)&S.s[2][t0 + j * 16 + c][r];
+          u32x4 s3 = *(const u32x4 *)&S.s[2][j * 16 + c][r];
           if (g >> 1) s3 = (u32x4){0, 0, 0, 0};
 #pragma unroll
           for (int i = 0; i < 4; ++i) acc[i][j] = mfma16<BF16>(s3, bv[i], acc[i][j]);
@@ -605,7 +609,7 @@ __device__ __forceinline__ void lora_b_columns(const LoraParams &p, R row_of, in
     for (int j = 0; j < TT; ++j)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int t = t0 + 16 * j + 4 * g + r;
+        const int t = 16 * j + 4 * g + r;
         const int e = S.e[t];
         float v[4];
         widen4<BASE>(base[j][r], p.base_dtype, v);
@@ -645,8 +649,8 @@ __device__ __forceinline__ void copy_rows(const LoraParams &p, const int *tile_r
   }
 }
 
-// Workgroup (tile, `cols` columns, window). Up to 32 rows: each wave takes a
-// quarter of the columns; more: two waves take each half of the rows.
+// Workgroup (tile, `cols` columns, window): each wave takes a quarter of the
+// columns.
 template <int RT, bool BF16, int BASE>
 __global__ void __launch_bounds__(256) lora_b_kernel(LoraParams p, int cols, int groups) {
   __shared__ __align__(16) LdsB<RT, kTileRows, 4> S;
@@ -654,7 +658,7 @@ __global__ void __launch_bounds__(256) lora_b_kernel(LoraParams p, int cols, int
   const LoraTile *tile = p.tiles + (int64_t)blockIdx.z * gridDim.x + blockIdx.x;
   // the rows are asked for together with what says whether there are any, one
   // to a lane; lanes get each other's by shuffles
-  const int own_row = tile->rows[threadIdx.x & 63];
+  const int own_row = tile->rows[threadIdx.x & (kTileRows - 1)];
   const int ad = uload_i32(&tile->adapter), nrows = uload_i32(&tile->nrows);
   if (ad < 0) return;
   const int c0 = blockIdx.y * cols, c1 = min(c0 + cols, p.N);
@@ -665,22 +669,16 @@ __global__ void __launch_bounds__(256) lora_b_kernel(LoraParams p, int cols, int
   }
   const float scale = p.scale ? uload_f32(p.scale + ad) : 1.0f;
   auto row_of = [&](int i) { return __shfl(own_row, i, 64); };
-  const int s_row = row_of(threadIdx.x >> 2);
+  const int s_row = row_of(threadIdx.x / kLanesS<RT>);
   auto make_s = [&] {
     load_s<RT, BF16>(p, s_row, nrows, scale, ra, groups, S);
     __syncthreads();
   };
-  // one copy of the code for 32 rows, wherever they start: it is run once or
-  // twice, and fetching instructions is part of a small call's time
-  const int wave = wave_id();
-  const bool halves = nrows > 32;
-  const int share = halves ? cols / 2 : cols / 4;
-  const int t0 = halves ? 32 * (wave & 1) : 0;
-  const int n0 = c0 + share * (halves ? wave >> 1 : wave), n1 = min(n0 + share, p.N);
+  const int n0 = c0 + cols / 4 * wave_id(), n1 = min(n0 + cols / 4, p.N);
   if (nrows <= 16)
-    lora_b_columns<RT, 1, BF16, BASE>(p, row_of, nrows, 0, ad, ra, n0, n1, S, stages, make_s);
+    lora_b_columns<RT, 1, BF16, BASE>(p, row_of, nrows, ad, ra, n0, n1, S, stages, make_s);
   else
-    lora_b_columns<RT, 2, BF16, BASE>(p, row_of, nrows, t0, ad, ra, n0, n1, S, stages, make_s);
+    lora_b_columns<RT, 2, BF16, BASE>(p, row_of, nrows, ad, ra, n0, n1, S, stages, make_s);
 }
 
 // -------------------------------------------------------- both in one launch
@@ -724,12 +722,12 @@ __global__ void __launch_bounds__(512) lora_kernel(LoraParams p, int cols) {
   }
   auto make_s = [&] {
     const f32x4 sum[1] = {total};
-    if (t < nrows) split_s<1, BF16>(t, threadIdx.x & 3, scale, ra, sum, S);
+    if (t < nrows) split_s<1, BF16, 4>(t, threadIdx.x & 3, scale, ra, sum, S);
     __syncthreads();  // s is there, and the sums' place is free for B
   };
   const int n0 = c0 + cols / W * wave_id(), n1 = min(n0 + cols / W, p.N);
   auto row_of = [&](int i) { return L.rows[min(i, nrows - 1)]; };
-  lora_b_columns<1, 1, BF16, BASE>(p, row_of, nrows, 0, ad, ra, n0, n1, S, lds, make_s);
+  lora_b_columns<1, 1, BF16, BASE>(p, row_of, nrows, ad, ra, n0, n1, S, lds, make_s);
 }
 
 int windows(int rows) { return (rows + kWindow - 1) / kWindow; }
@@ -748,7 +746,7 @@ void run_a(const LoraParams &p, hipStream_t s) {
   // waves 6.1; 16384 rows: no difference).
   constexpr int W = RT == 4 ? 4 : 8;
   const int chunks = (p.R + RT * 16 - 1) / (RT * 16);
-  const dim3 grid(tile_slots(p.rows, p.adapters), lora_groups(p.K) * chunks * 2, windows(p.rows));
+  const dim3 grid(tile_slots(p.rows, p.adapters), lora_groups(p.K) * chunks, windows(p.rows));
   if (p.bf16)
     hipLaunchKernelGGL((lora_a_kernel<RT, W, true>), grid, dim3(64 * W), 0, s, p, chunks);
   else

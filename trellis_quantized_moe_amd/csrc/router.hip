@@ -433,14 +433,17 @@ __global__ void __launch_bounds__(balance_threads(I)) balance_kernel(RouterParam
 }
 
 // Adds the partial sums and forms the loss. Workgroup b takes experts 16 b ..
-// 16 b + 15: 16 threads to an expert, each over every 16th partial sum, then
-// the 16 in order. The workgroup that arrives last (part_arrived, zeroed by
+// 16 b + 15: 64 threads to an expert, each over every 64th partial sum, then
+// the 64 in order. The workgroup that arrives last (part_arrived, zeroed by
 // balance_kernel) adds the workgroups' shares of the loss in their order.
 // One workgroup for all experts took 66 us on 256 partial sums of 256 experts,
-// a chain of dependent loads; spread out, 6.6.
-__global__ void __launch_bounds__(256) balance_sum_kernel(RouterParams p) {
-  __shared__ float s_prob[16][17];
-  __shared__ int s_count[16][17];
+// a chain of dependent loads; 16 threads to an expert 7.5 us on 512, these 6.6,
+// of which a launch that does nothing is 2.5.
+constexpr int kSumSlices = 64;
+
+__global__ void __launch_bounds__(16 * kSumSlices) balance_sum_kernel(RouterParams p) {
+  __shared__ float s_prob[kSumSlices][17];
+  __shared__ int s_count[kSumSlices][17];
   __shared__ float s_share[16];
   __shared__ int s_tokens, s_last;
   const int c = threadIdx.x & 15, slice = threadIdx.x >> 4;
@@ -449,10 +452,10 @@ __global__ void __launch_bounds__(256) balance_sum_kernel(RouterParams p) {
   __syncthreads();
   float prob = 0.0f;
   int count = 0, tokens = 0;
-  for (int b = threadIdx.x; b < p.nblk; b += 256) tokens += p.part_tokens[b];
+  for (int b = threadIdx.x; b < p.nblk; b += 16 * kSumSlices) tokens += p.part_tokens[b];
   if (e < p.E) {
 #pragma unroll 8
-    for (int b = slice; b < p.nblk; b += 16) {
+    for (int b = slice; b < p.nblk; b += kSumSlices) {
       prob += p.part_prob[(int64_t)b * p.E + e];
       count += p.part_count[(int64_t)b * p.E + e];
     }
@@ -465,8 +468,8 @@ __global__ void __launch_bounds__(256) balance_sum_kernel(RouterParams p) {
   if (threadIdx.x < 16) {
     prob = 0.0f;
     count = 0;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
+#pragma unroll 16
+    for (int i = 0; i < kSumSlices; ++i) {
       prob += s_prob[i][c];
       count += s_count[i][c];
     }
@@ -514,7 +517,9 @@ __global__ void __launch_bounds__(256) balance_sum_kernel(RouterParams p) {
 // [E] row per 16 lanes, zeroed and filled by the row's own lanes (LDS
 // operations of a wave stay in order, so no barrier is needed). Comparing
 // every chosen expert with every lane's experts took 24 of 45 instructions
-// per logit and 28 us on 32768 x 256, against 9.
+// per logit and 28 us on 32768 x 256; so it is 17, 2 TB/s, of which the vector
+// instructions (37 per logit, a third of them exp2 and rcp at a quarter of the
+// rate) are about 11.
 template <int I, int DT>
 __global__ void __launch_bounds__(256) route_backward_kernel(RouterParams p) {
   __shared__ __align__(16) float s_add[kRowsPerWg][64 * I];
@@ -732,7 +737,7 @@ hipError_t launch_balance(const RouterParams &p, hipStream_t s) {
 }
 
 hipError_t launch_balance_sum(const RouterParams &p, hipStream_t s) {
-  hipLaunchKernelGGL(balance_sum_kernel, dim3((p.E + 15) / 16), dim3(256), 0, s, p);
+  hipLaunchKernelGGL(balance_sum_kernel, dim3((p.E + 15) / 16), dim3(16 * kSumSlices), 0, s, p);
   return hipGetLastError();
 }
 
