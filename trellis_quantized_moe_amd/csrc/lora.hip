@@ -1,8 +1,13 @@
 // Low-rank adapters of many requests beside a shared projection:
 //   out_t = base_t + scale_a (x_t A_a^T) B_a^T,   a = ids[t]
-// Many rows take two launches: lora_a writes s = x A^T (fp32, R values a row)
-// to the workspace; lora_b multiplies s by B^T, adds the base and stores. Few
-// rows take one, lora_kernel, whose workgroups each form the s they need.
+// Two launches: lora_a writes s = x A^T (fp32, R values a row) to the workspace;
+// lora_b multiplies s by B^T, adds the base and stores. Up to 16 ranks mostly
+// take one, lora_kernel, whose workgroups each form the s they need (lora_one).
+// x, base and out are each moved once and the products are under 1% of the
+// matrix rate, so many rows are bound by memory: 16384 rows of 4096 -> 4096 at
+// rank 16, fp32 base, 545 MB: 121 us, 4.5 TB/s (a large copy: 5.0). Few rows
+// are bound by latency: one row 8.9 us, of which an empty launch is 2.5 and
+// finding the tile about 3.
 //
 // Tiles. A tile is up to 32 rows of one adapter (16 in lora_kernel). Every
 // workgroup of lora_a and lora_kernel finds its tile by itself: rows are taken
@@ -169,7 +174,8 @@ __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
 // with four waves, w + 4 of its group. Ranks are the MFMA rows, tile rows its
 // columns. A lane's operand is 16 bytes of row (lane % 16), so loading operands
 // as they are used puts 64 lanes on 64 cache lines, and the cache looks up one
-// line a cycle: that took 58 us on 16384 x 4096 where the bytes need 27.
+// line a cycle: that took 58 us on 16384 x 4096 where the bytes need 27, and this
+// way 43.
 // Instead eight lanes take 128 bytes of a row, 64 inputs of 8 rows to a load,
 // and the wave turns them round in LDS that it shares with no other: chunk k of
 // row r lies at place k ^ (r % 8) of the row, so that the writes of eight lanes
@@ -486,8 +492,8 @@ __device__ __forceinline__ void load_s(const LoraParams &p, int row, int nrows, 
 // consecutive columns of a row and 16 lanes have 64: base and output move in
 // runs of 128 bytes (16-bit) or 256 (fp32) with neighbouring lanes side by side.
 // (With tile rows as the MFMA columns, neighbouring lanes held different rows
-// and every load and store touched 64 cache lines: 128 us instead of 90 on
-// 16384 x 4096.) B's rows of 64 columns are one run of memory: they are loaded
+// and every load and store touched 64 cache lines: 128 us instead of 105 on
+// 16384 x 4096 with an fp32 base.) B's rows of 64 columns are one run of memory: they are loaded
 // as such and turned round in LDS. The loads of the next 64 columns are under
 // way while these are worked on.
 // row_of(i): the tile's row i, past its end any of its rows; make_s, called by
@@ -650,7 +656,10 @@ __device__ __forceinline__ void copy_rows(const LoraParams &p, const int *tile_r
 }
 
 // Workgroup (tile, `cols` columns, window): each wave takes a quarter of the
-// columns.
+// columns. 4001 rows of 2048 columns at rank 64, bf16, 34 MB: 19.5 us, a chain
+// of loads (tile, sums, B, base) that two workgroups to a CU do not hide: without
+// base 2 us less, without the sums 3, without B 1, without the stores 5. 16384
+// rows of 4096 columns, fp16, 276 MB: 89 us, 3.1 TB/s.
 template <int RT, bool BF16, int BASE>
 __global__ void __launch_bounds__(256) lora_b_kernel(LoraParams p, int cols, int groups) {
   __shared__ __align__(16) LdsB<RT, kTileRows, 4> S;
@@ -741,9 +750,10 @@ int tile_slots(int rows, int adapters, int tile_rows = kTileRows) {
 template <int RT>
 void run_a(const LoraParams &p, hipStream_t s) {
   // 64 ranks: four waves with two slices each, so that two workgroups fit on a
-  // CU (6144 -> 64 ranks, 4001 rows: 18.5 us; eight waves 21.7). Fewer ranks:
-  // eight waves, which finish a few rows sooner (16 ranks, one row: 5.6 us, four
-  // waves 6.1; 16384 rows: no difference).
+  // CU (6144 -> 64 ranks, 4001 rows: 18.6 us; eight waves 21.7; eight waves and
+  // 64 rows 16.9, but 143 against 127 on 16384 rows of 8192 -> 128 ranks).
+  // Fewer ranks: eight waves, which finish a few rows sooner (16 ranks, one row:
+  // 5.6 us, four waves 6.1; 16384 rows: no difference).
   constexpr int W = RT == 4 ? 4 : 8;
   const int chunks = (p.R + RT * 16 - 1) / (RT * 16);
   const dim3 grid(tile_slots(p.rows, p.adapters), lora_groups(p.K) * chunks, windows(p.rows));
@@ -809,9 +819,9 @@ size_t lora_tiles(int rows, int adapters) {
 }
 
 // One launch pays for few ranks: every workgroup reads all of A for 16 rows
-// (in us, one launch and two: 4096 -> 4096 at rank 16, 1 row 9.2 and 9.1, 256
-// rows 10.5 and 14.5, 16384 rows 101 and 108; at rank 64, 18 and 17 at 256 rows,
-// 178 and 145 at 16384), and spares a launch on the host (2.5 us). A long K and
+// (in us, one launch and two, fp16 base: 4096 -> 4096 at rank 16, 1 row 8.9 and
+// 9.1, 256 rows 10.2 and 12.3, 16384 rows 100 and 108; at rank 64, 18 and 14 at
+// 256 rows, 178 and 139 at 16384), and spares a launch on the host (2.5 us). A long K and
 // few rows leave it too few workgroups for A, which two launches split over K.
 bool lora_one(const LoraParams &p) {
   return p.R <= 16 && (lora_groups(p.K) <= 4 || p.rows >= 4096);

@@ -226,6 +226,9 @@ struct Key<true> {
   typedef double type;
 };
 
+// Bound by the chain of k selections, not by bytes: 8192 x 192 fp32 (6.7 MB, 1.3
+// us at 5 TB/s), k = 8: 6.4 us; a few rows 3.5 (an empty launch: 2.5). With a
+// bias the fp64 scores take most of a small call: 61 rows of 256 experts 9.2.
 template <int I, int DT, bool BIAS>
 __global__ void __launch_bounds__(256) route_topk_kernel(RouterParams p) {
   typedef typename Key<BIAS>::type key_t;
@@ -360,7 +363,9 @@ __device__ __forceinline__ float bits_to_f32(uint32_t b, int dtype) {
 // go to part_prob[b][E], part_count[b][E] and part_tokens[b]; they are added
 // in the order of b by balance_sum_kernel, so the same call gives the same
 // bytes.
-// The next rows' loads are under way while a row is summed up.
+// The next rows' loads are under way while a row is summed up. 65536 x 256 bf16
+// (35.7 MB): 14.5 us, 2.5 TB/s, bound by the vector instructions (exp2 and rcp
+// run at a quarter of the rate); with expf, division and no rows ahead 50 us.
 template <int I, int DT>
 __global__ void __launch_bounds__(balance_threads(I)) balance_kernel(RouterParams p) {
   constexpr int kThreads = balance_threads(I), kWaves = kThreads / 64, kRows = kThreads / 16;
