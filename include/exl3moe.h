@@ -324,8 +324,9 @@ int32_t exl3_moe_layout(int32_t rows, int32_t topk, int32_t num_experts,
  * exl3_moe_forward, the balance loss of that routing, and the gradient of
  * both with respect to the logits.
  *
- * logits: [rows][num_experts] fp16, bf16 or fp32, consecutive rows ld_logits
- * elements apart (>= num_experts); natural alignment of the element type.
+ * rows * topk is at most 2^30. logits: [rows][num_experts] fp16, bf16 or fp32,
+ * consecutive rows ld_logits elements apart (num_experts .. 2^32); natural
+ * alignment of the element type.
  * A logit of -inf or NaN takes its expert out of that row (never chosen,
  * probability and gradient 0); +inf counts as the largest finite fp32. With
  *   t_e = exp(l_e) (EXL3_SOFTMAX) or 1 / (1 + exp(-l_e)) (EXL3_SIGMOID),
@@ -367,7 +368,8 @@ int32_t exl3_route_topk(const exl3_router *router, const void *logits, int32_t l
  *   loss = coef * num_experts * sum_e (count_e / (T topk)) * prob_e
  * (T == 0: loss and prob are 0; a row that takes part but has no expert left
  * adds 0 to prob). A t_te below 2^-126 times the row's largest counts as 0. The
- * router's renorm, scale and bias take no part. Sums run in fp32 in a fixed order: the same call gives the same bytes.
+ * router's renorm, scale and bias take no part. Sums run in fp32 in a fixed
+ * order: the same call gives the same bytes.
  * ws: exl3_balance_workspace_size(rows, num_experts) bytes, 16-byte aligned;
  * calls that share it must be ordered on one stream.
  * rows == 0 enqueues the zero results.
@@ -426,12 +428,12 @@ typedef struct exl3_lora_adapters {
                            (clamped to [0, R]); the rest is not used */
 } exl3_lora_adapters;
 /*
- * rows: at most EXL3_LORA_MAX_ROWS. x: [rows][K], rows ld_x elements apart. ids: [rows] EXL3_I32 or EXL3_I64.
- * base: [rows][N] fp16, bf16 or fp32, ld_base apart, or NULL (zeros); out:
- * [rows][N] fp16, bf16 or fp32, ld_out apart. x, base, out: 16-byte aligned,
- * their row distances at least a row, at most EXL3_LORA_MAX_LD elements and a
- * multiple of 16 bytes. out may be
- * base itself (same dtype and row distance), otherwise it overlaps no input.
+ * rows: at most EXL3_LORA_MAX_ROWS. x: [rows][K], rows ld_x elements apart.
+ * ids: [rows] EXL3_I32 or EXL3_I64. base: [rows][N] fp16, bf16 or fp32, ld_base
+ * apart, or NULL (zeros); out: [rows][N] fp16, bf16 or fp32, ld_out apart. x,
+ * base, out: 16-byte aligned, their row distances at least a row, at most
+ * EXL3_LORA_MAX_LD elements and a multiple of 16 bytes. out may be base itself
+ * (same dtype and row distance), otherwise it overlaps no input.
  * ws: exl3_lora_workspace_size(rows, in_features, rank, num_adapters) bytes,
  * 16-byte aligned (the inner products and the row tiles); calls that share it
  * must be ordered on one stream.

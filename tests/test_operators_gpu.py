@@ -4,8 +4,8 @@ against float64 oracles (MI355X only).
 Tolerances. An output is off by at most half a step of its type (relative
 eps / 2, absolute half the smallest subnormal) plus what fp32 arithmetic loses
 before it:
-  u = 2^-24 per rounding. exp(l - m) loses |l - m| u from its rounded argument
-  and 2 u of its own; a sum over a row adds one rounding per addition (4 I + 4
+  u = 2^-24 per rounding. exp(l - m) loses 2 |l - m| u from its argument, which
+  is rounded twice, and 2 u of its own; a sum over a row adds one rounding per addition (4 I + 4
   of them: a lane's values, then four steps), divisions and products one each.
 Adapter sums of small integers are exact in fp32 and in the 16-bit terms, so
 those tests compare bytes; sums of general values use the rounding count of
@@ -150,6 +150,20 @@ def test_route_topk_near_ties_with_bias():
     ids, _ = exl3.exl3_route_topk(l.to(DEV), 8, "sigmoid", True, 1.0, b.to(DEV))
     want = list(range(E - 1, E - 9, -1))
     assert _ids(ids)[3].tolist() == want
+
+
+def test_route_topk_more_rows_than_one_axis_of_a_launch_holds():
+    rows = (1 << 28) + 37  # 16 threads a row: over 2^32 threads
+    l = torch.zeros(rows, 1, dtype=torch.float16, device=DEV)
+    ids = torch.full((rows, 1), 7, dtype=torch.int32, device=DEV)
+    without = [0, 15, (1 << 26) - 1, 1 << 28, rows - 1]
+    l[without] = float("-inf")
+    _, w = exl3.exl3_route_topk(l, 1, "softmax", True, 0.5, ids=ids, w_dtype=torch.float16)
+    torch.cuda.synchronize()
+    out = torch.nonzero(ids[:, 0] != 0).flatten()
+    assert out.tolist() == without and (ids[without] == -1).all()
+    w = w[:, 0]
+    assert not w[without].any() and int((w == 0.5).sum()) == rows - len(without)
 
 
 # ----------------------------------------------------------------- balance
@@ -508,6 +522,46 @@ def test_lora_ids_outside_32_bits():
     ids = torch.tensor([0, 1 << 32, -(1 << 40), 1 << 62], device=DEV)
     y = exl3.exl3_lora(x, a, b, ids)
     assert (y[0] == 8).all() and not y[1:].any()
+
+
+def _far(t, ld):
+    """t with its rows `ld` elements apart (what lies between is not set)."""
+    buf = torch.empty(t.shape[0], ld, dtype=t.dtype, device=DEV)
+    buf[:, :t.shape[1]] = t
+    return buf[:, :t.shape[1]]
+
+
+@pytest.mark.parametrize("R", [9, 24])
+def test_lora_rows_at_the_largest_distance(R):
+    """Byte offsets past 2^31 within a window of rows and past 2^32 in all."""
+    g = torch.Generator().manual_seed(R)
+    rows, K, N, n, ld = 2500, 264, 72, 4, 1 << 19
+    x = torch.randn(rows, K, generator=g).half().to(DEV)
+    a = torch.randn(n, R, K, generator=g).half().to(DEV)
+    b = torch.randn(n, N, R, generator=g).half().to(DEV)
+    ids = torch.randint(-1, n, (rows,), generator=g).to(DEV)
+    base = torch.randn(rows, N, generator=g).to(DEV)
+    want = exl3.exl3_lora(x, a, b, ids, base=base)
+    far = _far(base, ld)
+    got = exl3.exl3_lora(_far(x, ld), a, b, ids, base=far, out=far)
+    assert torch.equal(got, want)
+
+
+def test_router_rows_at_a_large_distance():
+    """Element offsets past 2^32."""
+    g = torch.Generator().manual_seed(3)
+    rows, E, k, ld = 9001, 12, 3, 1 << 19
+    l = torch.randn(rows, E, generator=g).to(DEV)
+    far = _far(l, ld)
+    ids, w = exl3.exl3_route_topk(l, k)
+    for p, q in zip(exl3.exl3_route_topk(far, k), (ids, w)):
+        assert torch.equal(p, q)
+    bal, fbal = (exl3.exl3_balance_loss(t, ids, "softmax", 0.1) for t in (l, far))
+    for key in bal:
+        assert torch.equal(bal[key], fbal[key])
+    want = exl3.exl3_route_backward(l, ids, w, balance=bal, coef=0.1)
+    exl3.exl3_route_backward(far, ids, w, balance=bal, coef=0.1, dlogits=far)
+    assert torch.equal(far, want)
 
 
 # ------------------------------------------------- streams, graphs, devices

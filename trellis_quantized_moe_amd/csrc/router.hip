@@ -233,7 +233,8 @@ template <int I, int DT, bool BIAS>
 __global__ void __launch_bounds__(256) route_topk_kernel(RouterParams p) {
   typedef typename Key<BIAS>::type key_t;
   const int lane = threadIdx.x & 15;
-  const int64_t row = (int64_t)blockIdx.x * kRowsPerWg + (threadIdx.x >> 4);
+  const int64_t row =
+      ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * kRowsPerWg + (threadIdx.x >> 4);
   const bool in = row < p.rows;
   const bool live = in && (!p.row_mask || p.row_mask[row] != 0);
   const int64_t at = (live ? row : 0) * p.ld_logits;
@@ -724,7 +725,9 @@ unsigned row_groups(int rows) { return (unsigned)((rows + kRowsPerWg - 1) / kRow
 hipError_t launch_route_topk(const RouterParams &p, hipStream_t s) {
   return by_row(p, [&](auto I, auto D) {
     constexpr int i = decltype(I)::value, d = decltype(D)::value;
-    const dim3 grid(row_groups(p.rows));
+    // an axis of a launch holds fewer than 2^32 threads
+    const unsigned groups = row_groups(p.rows), x = min(groups, 1u << 22);
+    const dim3 grid(x, (groups + x - 1) / x);
     if (p.bias) hipLaunchKernelGGL((route_topk_kernel<i, d, true>), grid, dim3(256), 0, s, p);
     else hipLaunchKernelGGL((route_topk_kernel<i, d, false>), grid, dim3(256), 0, s, p);
   });
