@@ -195,9 +195,25 @@ __device__ __forceinline__ void fast_strengths(bool sigmoid, const float (&l)[N]
       t[j] = fast_exp(fminf(l[j], 0.0f) - m) * __builtin_amdgcn_rcpf(1.0f + fast_exp(-fabsf(l[j])));
   }
 }
-__device__ __forceinline__ float fast_slope(float l) {  // sigmoid
-  const float z = fast_exp(-fabsf(l));
-  return (l < 0.0f ? 1.0f : z) * __builtin_amdgcn_rcpf(1.0f + z);
+// The same of sigmoid scores, with h = d log t / d l = 1 - sigmoid(l).
+template <int N>
+__device__ __forceinline__ void fast_strengths_slopes(const float (&l)[N], float m, float (&t)[N],
+                                                      float (&h)[N]) {
+  if (!__any(m != 0.0f)) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const float z = fast_exp(-l[j]);  // infinite where t is 0
+      t[j] = __builtin_amdgcn_rcpf(1.0f + z);
+      h[j] = fminf(z, kFltMax) * t[j];
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const float z = fast_exp(-fabsf(l[j])), r = __builtin_amdgcn_rcpf(1.0f + z);
+      t[j] = fast_exp(fminf(l[j], 0.0f) - m) * r;
+      h[j] = (l[j] < 0.0f ? 1.0f : z) * r;
+    }
+  }
 }
 // d log t / d l: 1, or 1 - sigmoid(l) computed without cancellation.
 __device__ __forceinline__ float slope(bool sigmoid, float l) {
@@ -523,14 +539,19 @@ __global__ void __launch_bounds__(16 * kSumSlices) balance_sum_kernel(RouterPara
 // [E] row per 16 lanes, zeroed and filled by the row's own lanes (LDS
 // operations of a wave stay in order, so no barrier is needed). Comparing
 // every chosen expert with every lane's experts took 24 of 45 instructions
-// per logit and 28 us on 32768 x 256; so it is 17, 2 TB/s, of which the vector
-// instructions (37 per logit, a third of them exp2 and rcp at a quarter of the
-// rate) are about 11.
-template <int I, int DT>
+// per logit and 28 us on 32768 x 256.
+//
+// SIG, the scores, is a template argument: with a branch on it 32768 x 256 took
+// 20 us in bf16 (softmax), 22 in fp32 and 23 with sigmoid scores; so it is 18.7,
+// 18.8 and 20.1, and 131072 rows 49 and 54 (2.7 TB/s). Bound by the vector
+// instructions, and at a few iterations a wave by reading, working and writing
+// being done by all waves at the same time. More than 128 registers cost more
+// than they give (sigmoid slopes kept beside the logits: 72 instead of 54).
+template <int I, int DT, bool SIG>
 __global__ void __launch_bounds__(256) route_backward_kernel(RouterParams p) {
   __shared__ __align__(16) float s_add[kRowsPerWg][64 * I];
   const int lane = threadIdx.x & 15;
-  const bool sig = p.sigmoid;
+  constexpr bool sig = SIG;
   const bool need_all = p.count != nullptr || (!sig && !p.renorm);
   const bool two = p.topk > 16;  // else no lane has a second entry
   float *add = s_add[threadIdx.x >> 4];
@@ -575,11 +596,30 @@ __global__ void __launch_bounds__(256) route_backward_kernel(RouterParams p) {
     if (r0 + step <= last) fetch(min(row + step, last));
     const bool live = row_any(id[0] >= 0 || id[1] >= 0);
     const float m = shift(sig, row_max(max_of(l)));
-    float pe[4 * I], inv = 0.0f;  // p_e
+    // the chosen entries' logits, from the lanes that hold them (before the
+    // probabilities, which then take the logits' registers)
+    float lp[2] = {kNegInf, kNegInf};
+    if (p.dw) {
+#pragma unroll
+      for (int j = 0; j < I; ++j)
+        *(f32x4 *)(add + 64 * j + 4 * lane) =
+            (f32x4){l[4 * j], l[4 * j + 1], l[4 * j + 2], l[4 * j + 3]};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (h == 1 && !two) break;
+        if (id[h] >= 0) lp[h] = add[id[h]];
+        if (lp[h] == kNegInf) g[h] = 0.0f;  // an expert that takes no part
+      }
+#pragma unroll
+      for (int j = 0; j < I; ++j)
+        *(f32x4 *)(add + 64 * j + 4 * lane) = (f32x4){0.f, 0.f, 0.f, 0.f};
+    }
+    float pe[4 * I], h[4 * I], inv = 0.0f;  // p_e, and with sigmoid scores h_e
     float mean = 0.0f;  // c sum f p, and for softmax over all experts scale sum p g
     if (need_all) {
       float total = 0.0f;
-      fast_strengths(sig, l, m, pe);
+      if constexpr (sig) fast_strengths_slopes(l, m, pe, h);
+      else fast_strengths(false, l, m, pe);
 #pragma unroll
       for (int j = 0; j < 4 * I; ++j) total += pe[j];
       inv = live ? inv_or_0(row_sum(total)) : 0.0f;
@@ -591,28 +631,12 @@ __global__ void __launch_bounds__(256) route_backward_kernel(RouterParams p) {
       mean = row_sum(mean);
     } else {
 #pragma unroll
-      for (int j = 0; j < 4 * I; ++j) pe[j] = 0.0f;
+      for (int j = 0; j < 4 * I; ++j) pe[j] = h[j] = 0.0f;
     }
 
     if (p.dw) {
-      // the chosen entries: logit (from the lane that holds it), strength,
-      // gradient; v: what each adds to its expert's gradient
-#pragma unroll
-      for (int j = 0; j < I; ++j)
-        *(f32x4 *)(add + 64 * j + 4 * lane) =
-            (f32x4){l[4 * j], l[4 * j + 1], l[4 * j + 2], l[4 * j + 3]};
-      float lp[2], v[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        lp[h] = kNegInf;
-        v[h] = 0.0f;
-        if (h == 1 && !two) break;
-        if (id[h] >= 0) lp[h] = add[id[h]];
-        if (lp[h] == kNegInf) g[h] = 0.0f;  // an expert that takes no part
-      }
-#pragma unroll
-      for (int j = 0; j < I; ++j)
-        *(f32x4 *)(add + 64 * j + 4 * lane) = (f32x4){0.f, 0.f, 0.f, 0.f};
+      // v: what each chosen entry adds to its expert's gradient
+      float v[2] = {0.0f, 0.0f};
       if (p.renorm) {
         const float mc = shift(sig, row_max(fmaxf(lp[0], lp[1])));
         float q[2] = {0.0f, 0.0f};
@@ -668,7 +692,8 @@ __global__ void __launch_bounds__(256) route_backward_kernel(RouterParams p) {
     }
 
     // A row or an expert that takes no part has gradient 0: its p and its
-    // added value are 0, so only a row whose mean is not finite needs to look.
+    // added value are 0, so only a row whose mean is not finite needs to look
+    // (0 times infinity).
     const bool odd = __any(!(fabsf(mean) < __builtin_inff()));
     if (row > last) continue;
     const int64_t to = row * p.ld_dlogits;
@@ -680,8 +705,8 @@ __global__ void __launch_bounds__(256) route_backward_kernel(RouterParams p) {
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
         const float x = cf[4 * j + v] - mean;
-        d[v] += pe[4 * j + v] * (sig ? fast_slope(l[4 * j + v]) * x : x);
-        if (odd && (!live || l[4 * j + v] == kNegInf)) d[v] = 0.0f;
+        const float y = pe[4 * j + v] * (sig ? h[4 * j + v] * x : x);
+        d[v] += odd && pe[4 * j + v] == 0.0f ? 0.0f : y;
       }
       if (p.dvec4 && e0 + 4 <= p.E) {
         if (p.dlogits_dtype == 3)
@@ -751,8 +776,10 @@ hipError_t launch_balance_sum(const RouterParams &p, hipStream_t s) {
 
 hipError_t launch_route_backward(const RouterParams &p, hipStream_t s) {
   return by_row(p, [&](auto I, auto D) {
-    hipLaunchKernelGGL((route_backward_kernel<decltype(I)::value, decltype(D)::value>),
-                       dim3(min(row_groups(p.rows), 1024u)), dim3(256), 0, s, p);
+    constexpr int i = decltype(I)::value, d = decltype(D)::value;
+    const dim3 grid(min(row_groups(p.rows), 1024u));
+    if (p.sigmoid) hipLaunchKernelGGL((route_backward_kernel<i, d, true>), grid, dim3(256), 0, s, p);
+    else hipLaunchKernelGGL((route_backward_kernel<i, d, false>), grid, dim3(256), 0, s, p);
   });
 }
 
