@@ -353,7 +353,8 @@ typedef struct exl3_router {
  * ids: [rows][topk] EXL3_I32 or EXL3_I64; w: [rows][topk] fp16, bf16 or fp32.
  * row_mask: NULL, or device uint8 [rows]; a row whose entry is 0 (padding)
  * gets ID -1 and weight 0 throughout, as do the entries of a row that has
- * fewer than topk experts left: the pack drops and counts those pairs.
+ * fewer than topk experts left: the pack drops and counts those pairs. A row's
+ * output bytes do not depend on the other rows or their number.
  */
 int32_t exl3_route_topk(const exl3_router *router, const void *logits, int32_t logits_dtype,
                         int64_t ld_logits, int32_t rows, const uint8_t *row_mask, void *ids,

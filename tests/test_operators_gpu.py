@@ -91,6 +91,9 @@ def _ids(t):
     (9, 600, 22, "f16", "f32", "i32", "sigmoid", False, False, 0, False),
     (5, 1024, 32, "f32", "f32", "i32", "sigmoid", True, True, 0, False),
     (6, 1001, 1, "bf16", "f32", "i32", "softmax", True, False, 0, True),
+    (1025, 256, 8, "f32", "f32", "i32", "sigmoid", True, True, 0, True),
+    (1030, 300, 32, "bf16", "f32", "i32", "softmax", True, False, 1, False),
+    (1026, 1024, 9, "f16", "f32", "i64", "sigmoid", False, True, 0, False),
 ])
 def test_route_topk(rows, E, k, dt, wdt, idt, scoring, renorm, bias, pad, mask):
     _say("route", rows, E, k, dt, scoring, renorm, bias, pad)
@@ -150,6 +153,21 @@ def test_route_topk_near_ties_with_bias():
     ids, _ = exl3.exl3_route_topk(l.to(DEV), 8, "sigmoid", True, 1.0, b.to(DEV))
     want = list(range(E - 1, E - 9, -1))
     assert _ids(ids)[3].tolist() == want
+
+
+@pytest.mark.parametrize("E,k,dt", [(65, 8, "f32"), (256, 8, "bf16"), (1023, 32, "f32")])
+def test_route_topk_rows_are_the_same_bytes_among_few_and_many(E, k, dt):
+    """Up to 1024 rows and more take rows of 64 and of 16 lanes."""
+    g = torch.Generator().manual_seed(E)
+    l = (2 * torch.randn(1500, E, generator=g)).to(DEV).to(DT[dt])
+    l[3, ::2], l[4], l[5, 1] = float("-inf"), float("nan"), float("inf")
+    b = (0.2 * torch.randn(E, generator=g)).to(DEV)
+    for scoring, renorm, bias in (("softmax", True, None), ("softmax", False, None),
+                                  ("sigmoid", True, b), ("sigmoid", False, None)):
+        ids, w = exl3.exl3_route_topk(l, k, scoring, renorm, 1.5, bias)
+        for lo, hi in ((0, 1), (1, 7), (7, 1031), (1031, 1500)):
+            i, v = exl3.exl3_route_topk(l[lo:hi], k, scoring, renorm, 1.5, bias)
+            assert torch.equal(i, ids[lo:hi]) and torch.equal(v, w[lo:hi]), (scoring, renorm, lo)
 
 
 def test_route_topk_more_rows_than_one_axis_of_a_launch_holds():

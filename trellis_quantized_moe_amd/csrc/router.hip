@@ -2,7 +2,7 @@
 // routing with its per-expert counts, and the gradient of both with respect to
 // the logits. Every one reads each logit once.
 //
-// Layout: 16 lanes hold one row, four rows to a wave. Lane i of a row holds
+// Layout: 16 lanes hold one row, four rows to a wave (a few rows of the top-k: 64). Lane i of a row holds
 // experts 64 j + 4 i + v (v = 0..3) of block j in l[4 j + v]: 16 bytes of fp32
 // or 8 of a 16-bit type in one load, and a block of a row is one run of 256 or
 // 128 bytes. Reductions over a row are four rotations inside the 16 lanes of a
@@ -64,6 +64,50 @@ __device__ __forceinline__ float row_sum(float v) {
   v += ror16<2>(v);
   return v + ror16<1>(v);
 }
+// Rows of L = 16 or 64 lanes. A swap of v with itself leaves each 16 (32) lanes
+// and their neighbours in the same lanes of two registers.
+template <int N>
+__device__ __forceinline__ void swap_rows(uint32_t v, uint32_t &a, uint32_t &b) {
+  typedef uint32_t pair __attribute__((ext_vector_type(2)));
+  pair r;
+  if constexpr (N == 16) r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  else r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  a = r[0];
+  b = r[1];
+}
+template <int N>
+__device__ __forceinline__ float pair_max(float v) {
+  uint32_t a, b;
+  swap_rows<N>(__builtin_bit_cast(uint32_t, v), a, b);
+  return kmax(__builtin_bit_cast(float, a), __builtin_bit_cast(float, b));
+}
+template <int N>
+__device__ __forceinline__ double pair_max(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  uint32_t la, lb, ha, hb;
+  swap_rows<N>((uint32_t)u, la, lb);
+  swap_rows<N>((uint32_t)(u >> 32), ha, hb);
+  return kmax(__builtin_bit_cast(double, ((uint64_t)ha << 32) | la),
+              __builtin_bit_cast(double, ((uint64_t)hb << 32) | lb));
+}
+template <int N>
+__device__ __forceinline__ int pair_min(int v) {
+  uint32_t a, b;
+  swap_rows<N>((uint32_t)v, a, b);
+  return min((int)a, (int)b);
+}
+template <int L, typename T>
+__device__ __forceinline__ T wide_max(T v) {
+  v = row_max(v);
+  if constexpr (L == 64) v = pair_max<32>(pair_max<16>(v));
+  return v;
+}
+template <int L>
+__device__ __forceinline__ int wide_min(int v) {
+  v = row_min(v);
+  if constexpr (L == 64) v = pair_min<32>(pair_min<16>(v));
+  return v;
+}
 __device__ __forceinline__ bool row_any(bool b) {
   const int shift = (threadIdx.x & 48);
   return ((__ballot(b) >> shift) & 0xffffull) != 0;
@@ -98,7 +142,7 @@ using RawRow = typename Raw<DT>::type[I];
 // E is a multiple of four and every group of four starts on one, so a group is
 // one load. Groups and values past E read the last ones again: no branch stands
 // between the loads, which would make each wait for the one before.
-template <int I, int DT>
+template <int I, int DT, int L = 16>
 __device__ __forceinline__ void load_raw(const RouterParams &p, int64_t at, int lane,
                                          RawRow<I, DT> &raw) {
   typedef typename Raw<DT>::type raw_t;
@@ -106,7 +150,7 @@ __device__ __forceinline__ void load_raw(const RouterParams &p, int64_t at, int 
     const char *q = (const char *)p.logits + at * (DT == 3 ? 4 : 2);
 #pragma unroll
     for (int j = 0; j < I; ++j)
-      raw[j] = *(const raw_t *)(q + min(64 * j + 4 * lane, p.E - 4) * (DT == 3 ? 4 : 2));
+      raw[j] = *(const raw_t *)(q + min(4 * L * j + 4 * lane, p.E - 4) * (DT == 3 ? 4 : 2));
   } else {
     asm volatile("" : "+v"(lane));  // 4 I indexes are computed here, not kept in registers
 #pragma unroll
@@ -114,7 +158,7 @@ __device__ __forceinline__ void load_raw(const RouterParams &p, int64_t at, int 
       uint32_t w[4];
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
-        const int64_t e = at + min(64 * j + 4 * lane + v, p.E - 1);
+        const int64_t e = at + min(4 * L * j + 4 * lane + v, p.E - 1);
         if constexpr (DT == 3) w[v] = ((const uint32_t *)p.logits)[e];
         else w[v] = ((const uint16_t *)p.logits)[e];
       }
@@ -123,7 +167,7 @@ __device__ __forceinline__ void load_raw(const RouterParams &p, int64_t at, int 
     }
   }
 }
-template <int I, int DT>
+template <int I, int DT, int L = 16>
 __device__ __forceinline__ void unpack_row(const RouterParams &p, int lane,
                                            const RawRow<I, DT> &raw, float (&l)[4 * I]) {
 #pragma unroll
@@ -139,10 +183,10 @@ __device__ __forceinline__ void unpack_row(const RouterParams &p, int lane,
         l[4 * j + v] = clean(DT == 2 ? bf16_bits_to_f32(b) : f16_bits_to_f32(b));
       }
     }
-    if (64 * (j + 1) > p.E) {  // the block that E ends in
+    if (4 * L * (j + 1) > p.E) {  // the block that E ends in
 #pragma unroll
       for (int v = 0; v < 4; ++v)
-        l[4 * j + v] = 64 * j + 4 * lane + v < p.E ? l[4 * j + v] : kNegInf;
+        l[4 * j + v] = 4 * L * j + 4 * lane + v < p.E ? l[4 * j + v] : kNegInf;
     }
   }
 }
@@ -242,29 +286,30 @@ struct Key<true> {
   typedef double type;
 };
 
-// Bound by the chain of k selections, not by bytes: 8192 x 192 fp32 (6.7 MB, 1.3
-// us at 5 TB/s), k = 8: 6.4 us; a few rows 3.5 (an empty launch: 2.5). With a
-// bias the fp64 scores take most of a small call: 61 rows of 256 experts 9.2.
-template <int I, int DT, bool BIAS>
+// L = 16 or 64 lanes to a row. Bound by the chain of k selections, not by bytes:
+// 8192 x 192 fp32 (6.7 MB, 1.3 us at 5 TB/s), k = 8: 6.4 us; a few rows 4 (an
+// empty launch: 2.5), with a bias, for the fp64 scores, 6.
+template <int I, int DT, bool BIAS, int L>
 __global__ void __launch_bounds__(256) route_topk_kernel(RouterParams p) {
   typedef typename Key<BIAS>::type key_t;
-  const int lane = threadIdx.x & 15;
+  const int lane = threadIdx.x & (L - 1);
   const int64_t row =
-      ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * kRowsPerWg + (threadIdx.x >> 4);
+      ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * (256 / L) + threadIdx.x / L;
   const bool in = row < p.rows;
   const bool live = in && (!p.row_mask || p.row_mask[row] != 0);
   const int64_t at = (live ? row : 0) * p.ld_logits;
   RawRow<I, DT> raw;
-  load_raw<I, DT>(p, at, lane, raw);
+  load_raw<I, DT, L>(p, at, lane, raw);
   float l[4 * I];
-  unpack_row<I, DT>(p, lane, raw, l);
+  unpack_row<I, DT, L>(p, lane, raw, l);
   if (!live) {
 #pragma unroll
     for (int j = 0; j < 4 * I; ++j) l[j] = kNegInf;
   }
   const bool sig = p.sigmoid;
-  // softmax over all experts: its sum, while the logits are at hand
-  const float m_all = shift(sig, row_max(max_of(l)));
+  // softmax over all experts (rows of 16 lanes): its sum, while the logits are
+  // at hand
+  const float m_all = shift(sig, wide_max<L>(max_of(l)));
   float total = 0.0f;
   if (!sig && !p.renorm) {
 #pragma unroll
@@ -274,7 +319,7 @@ __global__ void __launch_bounds__(256) route_topk_kernel(RouterParams p) {
   key_t s[4 * I];
 #pragma unroll
   for (int j = 0; j < 4 * I; ++j) {
-    const int e = 64 * (j >> 2) + 4 * lane + (j & 3);
+    const int e = 4 * L * (j >> 2) + 4 * lane + (j & 3);
     if constexpr (BIAS) {
       const double b = e < p.E ? (double)p.bias[e] : 0.0;
       const double v = 1.0 / (1.0 + exp(-(double)l[j])) + b;
@@ -296,20 +341,20 @@ __global__ void __launch_bounds__(256) route_topk_kernel(RouterParams p) {
 #pragma unroll
       for (int j = 1; j < I; ++j) top[v] = kmax(top[v], s[4 * j + v]);
     }
-    const key_t best = row_max(kmax(kmax(top[0], top[1]), kmax(top[2], top[3])));
+    const key_t best = wide_max<L>(kmax(kmax(top[0], top[1]), kmax(top[2], top[3])));
     int first[4];
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
       first[v] = 0x7fffffff;
 #pragma unroll
       for (int j = I - 1; j >= 0; --j)
-        first[v] = s[4 * j + v] == best ? 64 * j + 4 * lane + v : first[v];
+        first[v] = s[4 * j + v] == best ? 4 * L * j + 4 * lane + v : first[v];
     }
-    const int e = row_min(min(min(first[0], first[1]), min(first[2], first[3])));
+    const int e = wide_min<L>(min(min(first[0], first[1]), min(first[2], first[3])));
     const bool some = best > (key_t)kNegInf;
 #pragma unroll
     for (int j = 0; j < 4 * I; ++j)
-      s[j] = 64 * (j >> 2) + 4 * lane + (j & 3) == e ? (key_t)kNegInf : s[j];
+      s[j] = 4 * L * (j >> 2) + 4 * lane + (j & 3) == e ? (key_t)kNegInf : s[j];
     if ((k & 15) == lane) pick[k >> 4] = some ? e : -1;
   }
   // weights of the picks, from their logits
@@ -321,7 +366,7 @@ __global__ void __launch_bounds__(256) route_topk_kernel(RouterParams p) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) t[h] = pick[h] >= 0 ? strength(sig, lp[h], m) : 0.0f;
   if (p.renorm) total = row_sum(t[0] + t[1]);
-  if (!in) return;
+  if (!in || lane >= 16) return;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int k = lane + 16 * h;
@@ -724,16 +769,17 @@ __global__ void __launch_bounds__(256) route_backward_kernel(RouterParams p) {
   }
 }
 
-// f(blocks of 64 experts a kernel instance holds per row, logit type)
+// f(blocks of 64 (rows of 64 lanes: 256) experts a kernel instance holds per
+// row, logit type)
 template <typename F>
-hipError_t by_row(const RouterParams &p, F f) {
+hipError_t by_row(const RouterParams &p, int block, F f) {
   auto typed = [&](auto I) {
     if (p.logits_dtype == 1) f(I, std::integral_constant<int, 1>());
     else if (p.logits_dtype == 2) f(I, std::integral_constant<int, 2>());
     else f(I, std::integral_constant<int, 3>());
     return hipGetLastError();
   };
-  const int blocks = (p.E + 63) / 64;
+  const int blocks = (p.E + block - 1) / block;
   if (blocks <= 1) return typed(std::integral_constant<int, 1>());
   if (blocks <= 2) return typed(std::integral_constant<int, 2>());
   if (blocks <= 3) return typed(std::integral_constant<int, 3>());
@@ -748,13 +794,28 @@ unsigned row_groups(int rows) { return (unsigned)((rows + kRowsPerWg - 1) / kRow
 }  // namespace
 
 hipError_t launch_route_topk(const RouterParams &p, hipStream_t s) {
-  return by_row(p, [&](auto I, auto D) {
+  // Rows of 64 lanes while there are waves to spare (in us, 64 lanes and 16: 256
+  // rows of 256 experts 4.5 and 5.4, with a bias 6.0 and 9.6; 1024 rows 4.7 and
+  // 5.5, 6.0 and 9.7; 4096 rows 7.2 and 5.7, 10.1 and 10.0; 1024 experts, k = 16,
+  // 256 rows 8.3 and 19.9). The sum of a softmax over all experts would change
+  // its order, and a row's bytes with the number of rows: it stays with 16.
+  if (p.E > 64 && p.rows <= 1024 && (p.sigmoid || p.renorm)) {
+    const dim3 grid((p.rows + 3) / 4);
+    return by_row(p, 256, [&](auto I, auto D) {
+      constexpr int i = decltype(I)::value, d = decltype(D)::value;
+      if constexpr (i <= 4) {
+        if (p.bias) hipLaunchKernelGGL((route_topk_kernel<i, d, true, 64>), grid, dim3(256), 0, s, p);
+        else hipLaunchKernelGGL((route_topk_kernel<i, d, false, 64>), grid, dim3(256), 0, s, p);
+      }
+    });
+  }
+  // an axis of a launch holds fewer than 2^32 threads
+  const unsigned groups = row_groups(p.rows), x = min(groups, 1u << 22);
+  const dim3 grid(x, (groups + x - 1) / x);
+  return by_row(p, 64, [&](auto I, auto D) {
     constexpr int i = decltype(I)::value, d = decltype(D)::value;
-    // an axis of a launch holds fewer than 2^32 threads
-    const unsigned groups = row_groups(p.rows), x = min(groups, 1u << 22);
-    const dim3 grid(x, (groups + x - 1) / x);
-    if (p.bias) hipLaunchKernelGGL((route_topk_kernel<i, d, true>), grid, dim3(256), 0, s, p);
-    else hipLaunchKernelGGL((route_topk_kernel<i, d, false>), grid, dim3(256), 0, s, p);
+    if (p.bias) hipLaunchKernelGGL((route_topk_kernel<i, d, true, 16>), grid, dim3(256), 0, s, p);
+    else hipLaunchKernelGGL((route_topk_kernel<i, d, false, 16>), grid, dim3(256), 0, s, p);
   });
 }
 
@@ -763,7 +824,7 @@ int balance_blocks(int rows) {
 }
 
 hipError_t launch_balance(const RouterParams &p, hipStream_t s) {
-  return by_row(p, [&](auto I, auto D) {
+  return by_row(p, 64, [&](auto I, auto D) {
     hipLaunchKernelGGL((balance_kernel<decltype(I)::value, decltype(D)::value>), dim3(p.nblk),
                        dim3(balance_threads(decltype(I)::value)), 0, s, p);
   });
@@ -775,7 +836,7 @@ hipError_t launch_balance_sum(const RouterParams &p, hipStream_t s) {
 }
 
 hipError_t launch_route_backward(const RouterParams &p, hipStream_t s) {
-  return by_row(p, [&](auto I, auto D) {
+  return by_row(p, 64, [&](auto I, auto D) {
     constexpr int i = decltype(I)::value, d = decltype(D)::value;
     const dim3 grid(min(row_groups(p.rows), 1024u));
     if (p.sigmoid) hipLaunchKernelGGL((route_backward_kernel<i, d, true>), grid, dim3(256), 0, s, p);
