@@ -373,6 +373,9 @@ LORA = [
     (1, 4096, 4096, 16, 8, "f16", "f32", "f16", "one", 0),
     (2, 40, 24, 3, 2, "bf16", "bf16", "bf16", "rows", 8),
     (16, 512, 64, 8, 3, "bf16", "f32", "f32", "rows", 0),
+    (12, 264, 72, 40, 5, "f16", "f32", "bf16", "rows", 8),
+    (15, 8200, 136, 12, 700, "bf16", "bf16", "f32", "rows", 0),
+    (16, 136, 72, 33, 2, "bf16", "f16", "f32", "requests", 0),
     (17, 520, 72, 17, 3, "f16", "f16", "f16", "one", 0),
     (61, 2048, 192, 32, 48, "bf16", "f32", "f32", "rows", 0),
     (63, 2056, 264, 24, 2, "f16", "none", "bf16", "requests", 0),

@@ -6,8 +6,8 @@
 // x, base and out are each moved once and the products are under 1% of the
 // matrix rate, so many rows are bound by memory: 16384 rows of 4096 -> 4096 at
 // rank 16, fp32 base, 545 MB: 121 us, 4.5 TB/s (a large copy: 5.0). Few rows
-// are bound by latency: one row 8.9 us, of which an empty launch is 2.5 and
-// finding the tile about 3.
+// are bound by latency: one row 7.8 us, of which an empty launch is 2.5; beyond
+// 16 rows finding the tile is about 3.
 //
 // Tiles. A tile is up to 32 rows of one adapter (16 in lora_kernel). Every
 // workgroup of lora_a and lora_kernel finds its tile by itself: rows are taken
@@ -66,6 +66,35 @@ __device__ __forceinline__ int plan_tile(const LoraParams &p, int win, int tile,
                                          int &nrows) {
   constexpr int kThreads = 64 * W, kChunks = kWindow / kThreads;
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_id();
+  if (p.rows <= 16) {
+    // One row to a lane; every wave goes through the adapters as they appear,
+    // with no counts in LDS to wait for (4096 -> 4096 at rank 16, 1 row 7.8 us
+    // instead of 8.9, 16 rows 8.7 instead of 9.6; 61 rows of 40 adapters, rank
+    // 32, would take 1.6 us more).
+    const int r = min(lane, p.rows - 1);
+    int a;
+    if (p.ids_i64) {
+      const int64_t id = ((const int64_t *)p.ids)[r];
+      a = id >= 0 && id < p.adapters ? (int)id : p.adapters;
+    } else {
+      a = ((const int32_t *)p.ids)[r];
+      a = (uint32_t)a < (uint32_t)p.adapters ? a : p.adapters;
+    }
+    for (uint64_t left = (1ull << p.rows) - 1; left;) {
+      const int ad = __builtin_amdgcn_readlane(a, __ffsll((long long)left) - 1);
+      const uint64_t same = __ballot(a == ad) & left;
+      if (tile == 0) {
+        static_assert(TR >= 16, "a bucket is one tile");
+        nrows = __popcll(same);
+        if (wave == 0 && ((same >> lane) & 1)) L.rows[__popcll(same & ((1ull << lane) - 1))] = lane;
+        __syncthreads();
+        return ad;
+      }
+      --tile;
+      left &= ~same;
+    }
+    return -1;
+  }
   const int row0 = win * kWindow;
   const int n = min(p.rows - row0, kWindow);
   // lanes past the window read its last ID and drop it: loads without a branch
@@ -819,9 +848,10 @@ size_t lora_tiles(int rows, int adapters) {
 }
 
 // One launch pays for few ranks: every workgroup reads all of A for 16 rows
-// (in us, one launch and two, fp16 base: 4096 -> 4096 at rank 16, 1 row 8.9 and
-// 9.1, 256 rows 10.2 and 12.3, 16384 rows 100 and 108; at rank 64, 18 and 14 at
-// 256 rows, 178 and 139 at 16384), and spares a launch on the host (2.5 us). A long K and
+// (in us, one launch and two, fp16 base: 4096 -> 4096 at rank 16, 1 row 7.8 and
+// 8.1, 256 rows 10.6 and 12.4, 16384 rows 100 and 107; 6144 -> 192 at rank 8, 9.2
+// and 7.4, 11.3 and 11.5, 54 and 56; at rank 64, 4096 -> 4096, 18 and 14 at 256
+// rows, 178 and 139 at 16384), and spares a launch on the host (2.5 us). A long K and
 // few rows leave it too few workgroups for A, which two launches split over K.
 bool lora_one(const LoraParams &p) {
   return p.R <= 16 && (lora_groups(p.K) <= 4 || p.rows >= 4096);
