@@ -59,8 +59,8 @@ __device__ __forceinline__ int wave_scan(int v) {
 
 // Tile `tile` of window `win`: its adapter (p.adapters: rows without one; -1:
 // the window has fewer tiles) and its rows, counted from the window's first,
-// in L.rows[0 .. nrows). Called by
-// all threads of a workgroup of W waves; TR: rows of a tile.
+// in L.rows[0 .. nrows). Called by all threads of a workgroup of W waves; TR:
+// rows of a tile. The order of the tiles does not matter to anybody.
 template <int W, int TR>
 __device__ __forceinline__ int plan_tile(const LoraParams &p, int win, int tile, PlanLds &L,
                                          int &nrows) {
@@ -851,8 +851,8 @@ size_t lora_tiles(int rows, int adapters) {
 // (in us, one launch and two, fp16 base: 4096 -> 4096 at rank 16, 1 row 7.8 and
 // 8.1, 256 rows 10.6 and 12.4, 16384 rows 100 and 107; 6144 -> 192 at rank 8, 9.2
 // and 7.4, 11.3 and 11.5, 54 and 56; at rank 64, 4096 -> 4096, 18 and 14 at 256
-// rows, 178 and 139 at 16384), and spares a launch on the host (2.5 us). A long K and
-// few rows leave it too few workgroups for A, which two launches split over K.
+// rows, 178 and 139 at 16384), and spares a launch on the host (2.5 us). A long K
+// and few rows leave it too few workgroups for A, which two launches split over K.
 bool lora_one(const LoraParams &p) {
   return p.R <= 16 && (lora_groups(p.K) <= 4 || p.rows >= 4096);
 }
