@@ -28,3 +28,29 @@ def magnitude(x, a, b, ids, scale=None, ranks=None, base=None):
     return lora(np.abs(x), np.abs(a), np.abs(b), ids,
                 None if scale is None else np.abs(scale), ranks,
                 None if base is None else np.abs(base))
+
+
+def cancelling(seed, rows, K, N, R, n):
+    """Integer data whose adapter sums base takes back but for a small rest.
+
+    Every entry of x A^T is an integer of 18 to 20 bits (16 products of two
+    integers of 8 bits), so a bf16 or fp16 rounding of it, or a bf16 one of
+    what the first left over, shows in the rest. A column of B has at most 8
+    entries, all 1 or -1: every partial sum stays below 2^24, exact in fp32.
+    Returns x, a, b, ids, base, rest as float64 / int64; out equals rest,
+    integers up to 100, exact in every type."""
+    rng = np.random.default_rng(seed)
+    used = min(16, K)
+    x = np.zeros((rows, K))
+    for t in range(rows):
+        x[t, rng.choice(K, used, replace=False)] = rng.integers(128, 256, used)
+    a = rng.integers(128, 256, (n, R, K)).astype(np.float64)
+    b = np.zeros((n, N, R))
+    for i in range(n):
+        for c in range(N):
+            at = rng.choice(R, min(8, R), replace=False)
+            b[i, c, at] = rng.integers(0, 2, at.size) * 2 - 1
+    ids = rng.integers(-1, n, rows)
+    rest = rng.integers(-100, 101, (rows, N)).astype(np.float64)
+    base = rest - lora(x, a, b, ids)
+    return x, a, b, ids, base, rest

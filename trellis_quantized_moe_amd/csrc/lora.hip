@@ -417,15 +417,16 @@ __device__ __forceinline__ void *window_out(const LoraParams &p) {
 
 // s as MFMA operands. The matrix cores take 16-bit inputs, so s is written as
 // a sum of 16-bit terms, each the rounded rest of the ones before: two fp16
-// terms hold 2^-23 of the row's largest entry, two bf16 terms 2^-17 (enough
-// below the last bit of a 16-bit output: 2^-8 or 2^-11), three 2^-26 (fp32
-// outputs). The row is first scaled by a power of two to [2^13, 2^14), so
-// fp16 terms neither overflow nor lose small entries; exact, and undone on the
+// terms hold an entry to 2^-23, three bf16 terms to 2^-26 (two would hold 2^-17:
+// enough below the last bit of a 16-bit output, but not where the ranks, or the
+// sum and the base, cancel). The row is first scaled by a power of two to
+// [2^13, 2^14), so fp16 terms neither overflow nor lose small entries (those
+// below 2^-15 of the row's largest hold 2^-38 of it); exact, and undone on the
 // fp32 sum. An infinite or NaN entry is its first term alone.
 //
 // One MFMA takes 32 inner values: the first term of 16 ranks and the second
-// term of the same 16, against B given twice. The third term, if any, is a
-// second MFMA with zeros in the other half.
+// term of the same 16, against B given twice. The third term is a second MFMA
+// with zeros in the other half.
 // TR: rows of the tile, W: waves.
 template <int RT, int TR, int W>
 struct LdsB {
@@ -598,7 +599,6 @@ __device__ __forceinline__ void lora_b_columns(const LoraParams &p, R row_of, in
 #pragma unroll
     for (int r = 0; r < 4; ++r) fetch_base(j, r, n0);
   make_s();
-  const bool three = BF16 && p.out_dtype == 3;
 
   for (int n = n0; n < n1; n += 64) {
     if (!kNextB) fetch_b(n);
@@ -631,7 +631,7 @@ __device__ __forceinline__ void lora_b_columns(const LoraParams &p, R row_of, in
         const u32x4 s = *(const u32x4 *)&S.s[g >> 1][j * 16 + c][r];
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[i][j] = mfma16<BF16>(s, bv[i], acc[i][j]);
-        if (three) {
+        if constexpr (BF16) {
           u32x4 s3 = *(const u32x4 *)&S.s[2][j * 16 + c][r];
           if (g >> 1) s3 = (u32x4){0, 0, 0, 0};
 #pragma unroll
