@@ -389,6 +389,14 @@ __device__ __forceinline__ uint16_t f32_to_bf16_bits(float x) {
 __device__ __forceinline__ float bf16_bits_to_f32(uint16_t b) {
   return __builtin_bit_cast(float, (uint32_t)b << 16);
 }
+// Between the steps of an exchange among the lanes of a wave through LDS: the
+// hardware keeps a wave's LDS operations in order, this keeps the compiler's
+// (it may otherwise hand a lane the value it stored itself, or move a load
+// before another lane's store). No instruction.
+__device__ __forceinline__ void lds_exchange() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+  __builtin_amdgcn_wave_barrier();
+}
 // Two of them in one dword, by the packed conversions (a NaN stays one; its
 // payload may differ from the scalar conversion's).
 __device__ __forceinline__ uint32_t f32x2_to_out16(float a, float b, int bf16) {

@@ -581,8 +581,8 @@ __global__ void __launch_bounds__(16 * kSumSlices) balance_sum_kernel(RouterPara
 // (h = slope, g = 0 where not chosen). Both in one pass over the row.
 //
 // The chosen entries reach the lanes that hold their experts through LDS, one
-// [E] row per 16 lanes, zeroed and filled by the row's own lanes (LDS
-// operations of a wave stay in order, so no barrier is needed). Comparing
+// [E] row per 16 lanes, zeroed and filled by the row's own lanes (a wave's LDS
+// operations stay in order: lds_exchange() between the steps, no barrier). Comparing
 // every chosen expert with every lane's experts took 24 of 45 instructions
 // per logit and 28 us on 32768 x 256.
 //
@@ -649,15 +649,18 @@ __global__ void __launch_bounds__(256) route_backward_kernel(RouterParams p) {
       for (int j = 0; j < I; ++j)
         *(f32x4 *)(add + 64 * j + 4 * lane) =
             (f32x4){l[4 * j], l[4 * j + 1], l[4 * j + 2], l[4 * j + 3]};
+      lds_exchange();
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         if (h == 1 && !two) break;
         if (id[h] >= 0) lp[h] = add[id[h]];
         if (lp[h] == kNegInf) g[h] = 0.0f;  // an expert that takes no part
       }
+      lds_exchange();
 #pragma unroll
       for (int j = 0; j < I; ++j)
         *(f32x4 *)(add + 64 * j + 4 * lane) = (f32x4){0.f, 0.f, 0.f, 0.f};
+      lds_exchange();
     }
     float pe[4 * I], h[4 * I], inv = 0.0f;  // p_e, and with sigmoid scores h_e
     float mean = 0.0f;  // c sum f p, and for softmax over all experts scale sum p g
@@ -713,11 +716,13 @@ __global__ void __launch_bounds__(256) route_backward_kernel(RouterParams p) {
         if (h == 1 && !two) break;
         if (id[h] >= 0) add[id[h]] = (float)(lane + 16 * h);
       }
+      lds_exchange();
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         if (h == 1 && !two) break;
         if (id[h] >= 0) twice |= add[id[h]] != (float)(lane + 16 * h);
       }
+      lds_exchange();
       if (!__any(twice)) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -731,9 +736,11 @@ __global__ void __launch_bounds__(256) route_backward_kernel(RouterParams p) {
         for (int k = 0; k < p.topk; ++k) {
           const int i = k < 16 ? id[0] : id[1];
           const float a = k < 16 ? v[0] : v[1];
+          lds_exchange();
           if ((k & 15) == lane && i >= 0) add[i] += a;
         }
       }
+      lds_exchange();
     }
 
     // A row or an expert that takes no part has gradient 0: its p and its
