@@ -397,7 +397,8 @@ int32_t exl3_balance_loss(const exl3_router *router, const void *logits, int32_t
  * Counts and the choice of experts are held constant. dlogits:
  * [rows][num_experts] fp16, bf16 or fp32, ld_dlogits elements apart, every
  * element written, computed in fp32 and rounded once; it must not overlap
- * logits unless it is the same array with the same dtype and row distance.
+ * logits unless it is the same array with the same dtype and row distance. A
+ * row's bytes do not depend on the other rows or their number.
  */
 int32_t exl3_route_backward(const exl3_router *router, const void *logits, int32_t logits_dtype,
                             int64_t ld_logits, int32_t rows, const void *ids, int32_t ids_dtype,

@@ -136,3 +136,33 @@ def test_more_rows_than_one_pass(E, k, scoring, dt):
         for lo in range(0, MANY, 9600):
             hi = min(lo + 9600, MANY)
             assert torch.equal(grad(lo, hi).view(i), full[lo:hi].view(i)), (renorm, lo)
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_gradient_rows_are_the_same_bytes_in_any_company(scoring):
+    """Rows that take another path (below zero throughout, an infinite
+    gradient, an expert named twice) change nothing in the rows beside them."""
+    g = torch.Generator().manual_seed(21)
+    rows, E, k = 64, 70, 4
+    l = torch.randn(rows, E, generator=g)
+    l[::5] = -3 - 2 * l[::5].abs()
+    ids = torch.stack([torch.randperm(E, generator=g)[:k] for _ in range(rows)]).to(torch.int32)
+    ids[3::7, 1] = ids[3::7, 0]
+    ids[6::9] = -1
+    dw = torch.randn(rows, k, generator=g)
+    dw[9::16, 2] = inf
+    dw[::3] = 0.0
+    dw[1::6, 1] = -0.0
+    l, ids, dw = l.to(DEV), ids.to(DEV), dw.to(DEV)
+    bal = exl3.exl3_balance_loss(l, ids, scoring, 0.4)
+    for renorm in (True, False):
+        for b in (bal, None):
+            for scale in (1.3, -1.3):
+                full = exl3.exl3_route_backward(l, ids, dw, scoring, renorm, scale, b, 0.4)
+                for step in (1, 3):
+                    for lo in range(0, rows, step):
+                        s = slice(lo, lo + step)
+                        part = exl3.exl3_route_backward(l[s], ids[s], dw[s], scoring, renorm,
+                                                        scale, b, 0.4)
+                        assert torch.equal(part.view(torch.int32), full[s].view(torch.int32)), (
+                            renorm, b is None, scale, lo, step)

@@ -230,7 +230,7 @@ __device__ __forceinline__ void fast_strengths(bool sigmoid, const float (&l)[N]
   if (!sigmoid) {
 #pragma unroll
     for (int j = 0; j < N; ++j) t[j] = fast_exp(l[j] - m);
-  } else if (!__any(m != 0.0f)) {  // no row of the wave lies below zero throughout
+  } else if (m == 0.0f) {  // the row's own: its bytes do not depend on the wave's other rows
 #pragma unroll
     for (int j = 0; j < N; ++j) t[j] = __builtin_amdgcn_rcpf(1.0f + fast_exp(-l[j]));
   } else {
@@ -243,7 +243,7 @@ __device__ __forceinline__ void fast_strengths(bool sigmoid, const float (&l)[N]
 template <int N>
 __device__ __forceinline__ void fast_strengths_slopes(const float (&l)[N], float m, float (&t)[N],
                                                       float (&h)[N]) {
-  if (!__any(m != 0.0f)) {
+  if (m == 0.0f) {
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       const float z = fast_exp(-l[j]);  // infinite where t is 0
@@ -723,7 +723,7 @@ __global__ void __launch_bounds__(256) route_backward_kernel(RouterParams p) {
         if (id[h] >= 0) twice |= add[id[h]] != (float)(lane + 16 * h);
       }
       lds_exchange();
-      if (!__any(twice)) {
+      if (!row_any(twice)) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           if (h == 1 && !two) break;
@@ -746,7 +746,7 @@ __global__ void __launch_bounds__(256) route_backward_kernel(RouterParams p) {
     // A row or an expert that takes no part has gradient 0: its p and its
     // added value are 0, so only a row whose mean is not finite needs to look
     // (0 times infinity).
-    const bool odd = __any(!(fabsf(mean) < __builtin_inff()));
+    const bool odd = !(fabsf(mean) < __builtin_inff());
     if (row > last) continue;
     const int64_t to = row * p.ld_dlogits;
 #pragma unroll
