@@ -209,7 +209,8 @@ __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
 // and the wave turns them round in LDS that it shares with no other: chunk k of
 // row r lies at place k ^ (r % 8) of the row, so that the writes of eight lanes
 // (one row) and the reads of eight (one chunk of eight rows) fall into
-// different banks. red[i], i < 4, gets the sum of slices i and i + 4.
+// different banks. lds_exchange() stands between the writes and the reads: no
+// barrier. red[i], i < 4, gets the sum of slices i and i + 4.
 template <int RT, int TT>
 struct LdsA {
   static constexpr int kLd = RT * 16 + 4;
@@ -293,6 +294,7 @@ __device__ __forceinline__ void lora_a_tile(const LoraParams &p, const int *tile
         *(u32x4 *)(put + i * 2048 + h * 1024) = there ? v[n % kAhead][i][h] : zero;
       }
     if (n + kAhead < kPairs) fetch(n + kAhead);
+    lds_exchange();
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
@@ -306,6 +308,7 @@ __device__ __forceinline__ void lora_a_tile(const LoraParams &p, const int *tile
 #pragma unroll
         for (int j = 0; j < TT; ++j) acc[i][j] = mfma16<BF16>(a[i], x[j], acc[i][j]);
     }
+    lds_exchange();
   }
   __syncthreads();  // the sums take the place of the staged operands
   // lane: ranks 4 g .. 4 g + 3 of row c
@@ -604,6 +607,7 @@ __device__ __forceinline__ void lora_b_columns(const LoraParams &p, R row_of, in
     if (!kNextB) fetch_b(n);
     put_b();
     if (kNextB) fetch_b(n + 64);
+    lds_exchange();
     __builtin_amdgcn_sched_barrier(0);
     f32x4 acc[4][TT];
 #pragma unroll
@@ -653,6 +657,7 @@ __device__ __forceinline__ void lora_b_columns(const LoraParams &p, R row_of, in
         for (int i = 0; i < 4; ++i) v[i] += ldexpf(acc[i][j][r], e);
         if (t < nrows && col < p.N) store4(out0, p.out_dtype, oo[j][r] + col, v);
       }
+    lds_exchange();
   }
 }
 
