@@ -422,10 +422,16 @@ __device__ __forceinline__ void *window_out(const LoraParams &p) {
 // a sum of 16-bit terms, each the rounded rest of the ones before: two fp16
 // terms hold an entry to 2^-23, three bf16 terms to 2^-26 (two would hold 2^-17:
 // enough below the last bit of a 16-bit output, but not where the ranks, or the
-// sum and the base, cancel). The row is first scaled by a power of two to
-// [2^13, 2^14), so fp16 terms neither overflow nor lose small entries (those
-// below 2^-15 of the row's largest hold 2^-38 of it); exact, and undone on the
-// fp32 sum. An infinite or NaN entry is its first term alone.
+// sum and the base, cancel). An infinite or NaN entry is its first term alone.
+//
+// The row is first scaled by a power of two (exact, and undone on the fp32 sum).
+// fp16: to [2^13, 2^14), so that the terms neither overflow nor lose small
+// entries (those below 2^-15 of the row's largest hold 2^-38 of it); B is below
+// 2^16 and the sum below 2^37. bf16 has fp32's range, in B too, so a factor
+// would overflow sums that are finite, or lose small ones: there is none, but
+// for rows whose largest entry is below 2^-63, whose last terms would be
+// subnormal (2^48: then below 2^-15, and the sum of 128 products below 2^120),
+// and for those from 2^127 on, whose first term could round to infinity (2^-8).
 //
 // One MFMA takes 32 inner values: the first term of 16 ranks and the second
 // term of the same 16, against B given twice. The third term is a second MFMA
@@ -459,7 +465,8 @@ __device__ __forceinline__ void split_s(int t, int q, float scale, int ra,
   if (Q == 8) big = fmaxf(big, __shfl_xor(big, 4, 64));
   // fmaxf passes over NaN; the row's finite entries are scaled by the largest
   // (an infinity counts as exponent 255: everything finite stays below 2^14)
-  const int e = (int)((__builtin_bit_cast(uint32_t, big) >> 23) & 255u) - 140;
+  const int field = (int)((__builtin_bit_cast(uint32_t, big) >> 23) & 255u);
+  const int e = !BF16 ? field - 140 : field < 64 ? -48 : field < 254 ? 0 : 8;
 #pragma unroll
   for (int j = 0; j < J; ++j) {
     uint32_t w[3][2];
