@@ -414,7 +414,8 @@ int32_t exl3_route_backward(const exl3_router *router, const void *logits, int32
  *   out_t = base_t + scale_a * (x_t A_a^T) B_a^T      a = ids[t]
  * and a row whose ID lies outside [0, num_adapters) keeps base_t. x, A and B
  * share one dtype (fp16 or bf16); the inner product x A^T and all sums are
- * kept to fp32 accuracy and the output is rounded once. A row's output bytes
+ * kept to fp32 accuracy and the output is rounded once (fp16: an entry of
+ * x A^T below 2^-38 of its row's largest counts as 0). A row's output bytes
  * do not depend on the other rows, their number or their order.
  */
 typedef struct exl3_lora_adapters {

@@ -1,6 +1,7 @@
 """GPU: adapters whose values lie at the ends of their type's range, against
 the definition in float64 (MI355X only)."""
 
+import numpy as np
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -54,3 +55,41 @@ def test_lora_inner_product_past_the_largest_bf16():
     s = float(a.to(f).double()[0, 0, :2].sum())
     assert s < float(torch.finfo(torch.float32).max)
     assert (y.double().cpu() * 2.0 ** 100 / s - 1).abs().max() <= 4 * 2.0 ** -23
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("rows,K,R", [(1, 72, 8), (40, 72, 16), (90, 8200, 13), (33, 264, 24),
+                                      (90, 72, 64), (70, 40, 128)])
+def test_lora_infinite_entries(rows, K, R, dt):
+    """An infinite entry of B, of an adapter that rows name: what the
+    definition gives in its column (infinite, or NaN where infinities meet or
+    x A^T is 0), and every other column's bytes as without it."""
+    print("infinite", rows, K, R, dt, flush=True)
+    inf = float("inf")
+    g = torch.Generator().manual_seed(R)
+    n, N = 2, 136
+    f = DT[dt]
+    x = torch.randn(rows, K, generator=g).to(f)
+    a = torch.randn(n, R, K, generator=g).to(f)
+    b = torch.randn(n, N, R, generator=g).to(f)
+    ids = torch.zeros(rows, dtype=torch.long)
+    ids[1::3], ids[5::11] = 1, -1
+    if rows > 8:
+        x[3] = 0.0  # x A^T is 0: 0 times infinity
+        x[6, 2], x[8, 4] = inf, float("nan")
+    plain = b.clone()
+    b[0, 5, R - 1], b[0, 70, 0], b[0, 135, R // 2] = inf, -inf, inf
+    b[0, 71, 0], b[0, 71, R - 1] = -inf, inf
+    b[1, 64, 1], b[1, 9, R - 1], b[1, 100, 2] = -inf, inf, float("nan")
+    base = torch.randn(rows, N, generator=g)
+    clean, got = (exl3.exl3_lora(x.to(DEV), a.to(DEV), v.to(DEV), ids.to(DEV), base=base.to(DEV))
+                  .cpu() for v in (plain, b))
+    s = torch.einsum("tk,trk->tr", x.double(), a.double()[ids.clamp(min=0)])
+    ref = (s[:, None, :] * b.double()[ids.clamp(min=0)]).sum(2) + base.double()
+    ref = torch.where((ids >= 0)[:, None], ref, base.double())
+    odd = ~torch.isfinite(b.float()).all(2)[ids.clamp(min=0)] & (ids >= 0)[:, None]
+    i = torch.int32
+    assert torch.equal(got.view(i)[~odd], clean.view(i)[~odd])
+    assert np.array_equal(np.isnan(got[odd].numpy()), np.isnan(ref[odd].numpy()))
+    some = odd & ~torch.isnan(ref)
+    assert torch.equal(got[some].double(), ref[some])

@@ -488,6 +488,17 @@ __device__ __forceinline__ void split_s(int t, int q, float scale, int ra,
   if (q == 0) S.e[t] = e;
 }
 
+// Eight entries of B with zeros in the place of infinities.
+template <bool BF16>
+__device__ __forceinline__ u32x4 without_infinities(u32x4 b) {
+  constexpr uint32_t kInf = BF16 ? 0x7f80u : 0x7c00u;
+#pragma unroll
+  for (int w = 0; w < 4; ++w)
+    b[w] &= ((b[w] & 0x7fffu) == kInf ? 0u : 0xffffu) |
+            ((b[w] & 0x7fff0000u) == kInf << 16 ? 0u : 0xffff0000u);
+  return b;
+}
+
 // Lanes that form a row of s in lora_b.
 template <int RT>
 constexpr int kLanesS = RT == 1 ? 4 : 8;
@@ -610,9 +621,65 @@ __device__ __forceinline__ void lora_b_columns(const LoraParams &p, R row_of, in
     for (int r = 0; r < 4; ++r) fetch_base(j, r, n0);
   make_s();
 
+  // Whether the columns of B on their way hold an infinity or a NaN. An infinity
+  // meets the first term of s alone: with a later one, 0 or of the other sign,
+  // it would give NaN. (Looking for NaN among the results instead keeps the
+  // matrix instructions from running beside what follows: 51 us instead of 34 at
+  // 128 ranks, 4000 rows of 1024 columns; without either 31.)
+  auto odd_b = [&] {
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+    u16x2 top[4] = {};
+#pragma unroll
+    for (int m = 0; m < 2 * RT; ++m)
+#pragma unroll
+      for (int w = 0; w < 4; ++w)
+        top[w] = __builtin_elementwise_max(top[w], __builtin_bit_cast(u16x2, bn[m][w] & 0x7fff7fffu));
+    const u16x2 t = __builtin_elementwise_max(__builtin_elementwise_max(top[0], top[1]),
+                                              __builtin_elementwise_max(top[2], top[3]));
+    constexpr uint16_t kInf = BF16 ? 0x7f80 : 0x7c00;
+    return __any(t[0] >= kInf || t[1] >= kInf);
+  };
+  // acc += s B^T of the staged columns, ranks 16 rt ..: B's operands of COUNT
+  // MFMAs from `first` on at a time
+  auto multiply = [&](f32x4(&acc)[4][TT], int rt, auto first, auto count, auto clean) {
+    constexpr int i0 = decltype(first)::value, i1 = i0 + decltype(count)::value;
+    constexpr bool CLEAN = decltype(clean)::value;
+    const int r = rt * 16 + 8 * (g & 1);
+    u32x4 bv[4];
+#pragma unroll
+    for (int i = i0; i < i1; ++i) bv[i] = *(const u32x4 *)(stage + (4 * c + i) * kRow + r * 2);
+    // ranks from ra on give zero whatever B, or LDS behind it, holds there
+    if (rt * 16 + 16 > ra) {
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const uint32_t keep = (r + 2 * w < ra ? 0xffffu : 0u) | (r + 2 * w + 1 < ra ? 0xffff0000u : 0u);
+#pragma unroll
+        for (int i = i0; i < i1; ++i) bv[i][w] &= keep;
+      }
+    }
+    if (CLEAN && g >> 1) {
+#pragma unroll
+      for (int i = i0; i < i1; ++i) bv[i] = without_infinities<BF16>(bv[i]);
+    }
+#pragma unroll
+    for (int j = 0; j < TT; ++j) {
+      const u32x4 s = *(const u32x4 *)&S.s[g >> 1][j * 16 + c][r];
+#pragma unroll
+      for (int i = i0; i < i1; ++i) acc[i][j] = mfma16<BF16>(s, bv[i], acc[i][j]);
+      if constexpr (BF16) {
+        u32x4 s3 = *(const u32x4 *)&S.s[2][j * 16 + c][r];
+        if (g >> 1) s3 = (u32x4){0, 0, 0, 0};
+#pragma unroll
+        for (int i = i0; i < i1; ++i)
+          acc[i][j] = mfma16<BF16>(s3, CLEAN ? without_infinities<BF16>(bv[i]) : bv[i], acc[i][j]);
+      }
+    }
+  };
+
   for (int n = n0; n < n1; n += 64) {
     if (!kNextB) fetch_b(n);
     put_b();
+    const bool odd = odd_b();
     if (kNextB) fetch_b(n + 64);
     lds_exchange();
     __builtin_amdgcn_sched_barrier(0);
@@ -621,33 +688,24 @@ __device__ __forceinline__ void lora_b_columns(const LoraParams &p, R row_of, in
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < TT; ++j) acc[i][j] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    typedef std::integral_constant<int, 0> zero;
+    if (!odd) {
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      const int r = rt * 16 + 8 * (g & 1);
-      if (RT >= 4) __builtin_amdgcn_sched_barrier(0);
-      u32x4 bv[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) bv[i] = *(const u32x4 *)(stage + (4 * c + i) * kRow + r * 2);
-      // ranks from ra on give zero whatever B, or LDS behind it, holds there
-      if (rt * 16 + 16 > ra) {
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const uint32_t keep = (r + 2 * w < ra ? 0xffffu : 0u) | (r + 2 * w + 1 < ra ? 0xffff0000u : 0u);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) bv[i][w] &= keep;
-        }
+      for (int rt = 0; rt < RT; ++rt) {
+        if (RT >= 4) __builtin_amdgcn_sched_barrier(0);
+        multiply(acc, rt, zero(), std::integral_constant<int, 4>(), std::false_type());
       }
-#pragma unroll
-      for (int j = 0; j < TT; ++j) {
-        const u32x4 s = *(const u32x4 *)&S.s[g >> 1][j * 16 + c][r];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i][j] = mfma16<BF16>(s, bv[i], acc[i][j]);
-        if constexpr (BF16) {
-          u32x4 s3 = *(const u32x4 *)&S.s[2][j * 16 + c][r];
-          if (g >> 1) s3 = (u32x4){0, 0, 0, 0};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[i][j] = mfma16<BF16>(s3, bv[i], acc[i][j]);
-        }
+    } else {  // one after the other: no more registers than above
+      typedef std::integral_constant<int, 1> one;
+#pragma unroll 1
+      for (int rt = 0; rt < RT; ++rt) {
+        multiply(acc, rt, zero(), one(), std::true_type());
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(acc, rt, one(), one(), std::true_type());
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(acc, rt, std::integral_constant<int, 2>(), one(), std::true_type());
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(acc, rt, std::integral_constant<int, 3>(), one(), std::true_type());
       }
     }
     const int col = n + 4 * c;
@@ -701,8 +759,10 @@ __device__ __forceinline__ void copy_rows(const LoraParams &p, const int *tile_r
 // of loads (tile, sums, B, base) that two workgroups to a CU do not hide: without
 // base 2 us less, without the sums 3, without B 1, without the stores 5. 16384
 // rows of 4096 columns, fp16, 276 MB: 89 us, 3.1 TB/s.
+// 32 ranks with a 16-bit base: three waves a SIMD (70 us instead of 80 on 16384
+// rows of 4096 columns, bf16); more ranks or an fp32 base do not fit.
 template <int RT, bool BF16, int BASE>
-__global__ void __launch_bounds__(256) lora_b_kernel(LoraParams p, int cols, int groups) {
+__global__ void __launch_bounds__(256, RT == 2 && BASE <= 2 ? 3 : 1) lora_b_kernel(LoraParams p, int cols, int groups) {
   __shared__ __align__(16) LdsB<RT, kTileRows, 4> S;
   __shared__ __align__(16) char stages[LdsB<RT, kTileRows, 4>::kStage];
   const LoraTile *tile = p.tiles + (int64_t)blockIdx.z * gridDim.x + blockIdx.x;
