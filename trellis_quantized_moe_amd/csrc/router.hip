@@ -307,11 +307,12 @@ __global__ void __launch_bounds__(256) route_topk_kernel(RouterParams p) {
     for (int j = 0; j < 4 * I; ++j) l[j] = kNegInf;
   }
   const bool sig = p.sigmoid;
-  // softmax over all experts (rows of 16 lanes): its sum, while the logits are
-  // at hand
-  const float m_all = shift(sig, wide_max<L>(max_of(l)));
-  float total = 0.0f;
-  if (!sig && !p.renorm) {
+  // softmax over all experts: its sum, while the logits are at hand. Rows of 64
+  // lanes have no such form (launch_route_topk).
+  const bool over_all = L == 16 && !sig && !p.renorm;
+  float m_all = 0.0f, total = 0.0f;
+  if (over_all) {
+    m_all = shift(false, row_max(max_of(l)));
 #pragma unroll
     for (int j = 0; j < 4 * I; ++j) total += fast_exp(l[j] - m_all);
     total = row_sum(total);
@@ -362,7 +363,7 @@ __global__ void __launch_bounds__(256) route_topk_kernel(RouterParams p) {
 #pragma unroll
   for (int h = 0; h < 2; ++h)
     lp[h] = pick[h] >= 0 ? clean(load_as_f32(p.logits, DT, at + pick[h])) : kNegInf;
-  const float m = p.renorm ? shift(sig, row_max(fmaxf(lp[0], lp[1]))) : sig ? 0.0f : m_all;
+  const float m = p.renorm ? shift(sig, row_max(fmaxf(lp[0], lp[1]))) : m_all;
 #pragma unroll
   for (int h = 0; h < 2; ++h) t[h] = pick[h] >= 0 ? strength(sig, lp[h], m) : 0.0f;
   if (p.renorm) total = row_sum(t[0] + t[1]);
