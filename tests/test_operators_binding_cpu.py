@@ -26,3 +26,17 @@ def test_sizes_past_32_bits():
                  lambda: exl3.lora_workspace_size(FAR, 8, 1, 1)):
         with pytest.raises(exl3.Exl3Error, match="a size of 4294967300 is out of range"):
             call()
+
+
+def test_workspaces_whose_bytes_lie_apart():
+    """One byte expanded has as many elements as a workspace, and no room."""
+    ws = torch.empty(1, dtype=torch.uint8).expand(1 << 24)
+    x = torch.zeros(4, 64, dtype=torch.float16)
+    a, b = torch.zeros(2, 8, 64, dtype=torch.float16), torch.zeros(2, 32, 8, dtype=torch.float16)
+    ids = torch.zeros(4, 1, dtype=torch.int32)
+    for bad in (ws, torch.empty(1 << 24, dtype=torch.uint8)[::2]):
+        with pytest.raises(exl3.Exl3Error, match="ws must be contiguous"):
+            exl3.exl3_lora(x, a, b, ids[:, 0], ws=bad)
+        with pytest.raises(exl3.Exl3Error, match="ws must be contiguous"):
+            exl3.exl3_balance_loss(torch.zeros(4, 16), ids, balance=exl3.alloc_balance(16, "cpu"),
+                                   ws=bad)

@@ -355,6 +355,15 @@ def _vector(t, n, dtype, name):
     return t.data_ptr()
 
 
+def _workspace(ws, need, device):
+    """The caller's workspace, or a new one: its bytes lie side by side."""
+    if ws is None:
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    if not ws.is_contiguous():
+        _refuse("ws must be contiguous")
+    return ws
+
+
 def _pairs(t, rows, topk, name):
     if t.shape != (rows, topk) or not t.is_contiguous():
         _refuse("%s must be contiguous [%d, %d], got %s", name, rows, topk, list(t.shape))
@@ -430,8 +439,7 @@ def exl3_balance_loss(logits, ids, scoring="softmax", coef=1.0, balance=None, ws
     topk, idp = _ids_of(ids, rows)
     if balance is None:
         balance = alloc_balance(E, logits.device)
-    if ws is None:
-        ws = torch.empty(balance_workspace_size(rows, E), dtype=torch.uint8, device=logits.device)
+    ws = _workspace(ws, balance_workspace_size(rows, E), logits.device)
     rc = _router_c(E, topk, scoring)
     bc = BalanceC(_vector(balance["count"], E, torch.int32, "count"),
                   _vector(balance["tokens"], 1, torch.int32, "tokens"),
@@ -511,9 +519,7 @@ def exl3_lora(x, a, b, ids, scale=None, ranks=None, base=None, out_dtype=None, o
     if out is None:
         out = torch.empty(rows, N, device=x.device,
                           dtype=out_dtype or (base.dtype if base is not None else x.dtype))
-    if ws is None:
-        ws = torch.empty(max(lora_workspace_size(rows, K, R, n), 256), dtype=torch.uint8,
-                         device=x.device)
+    ws = _workspace(ws, max(lora_workspace_size(rows, K, R, n), 256), x.device)
     lc = LoraC(K, N, R, n, a.data_ptr(), b.data_ptr(), scale, ranks)
     _check(lib().exl3_lora(ctypes.byref(lc), x.data_ptr(), _dt(x), _matrix(x, rows, K, "x"), rows,
                            ids.data_ptr(), _dt(ids), basep, baset, ldb, out.data_ptr(), _dt(out),
