@@ -40,3 +40,8 @@ def test_workspaces_whose_bytes_lie_apart():
         with pytest.raises(exl3.Exl3Error, match="ws must be contiguous"):
             exl3.exl3_balance_loss(torch.zeros(4, 16), ids, balance=exl3.alloc_balance(16, "cpu"),
                                    ws=bad)
+
+
+def test_balance_workspace_of_the_largest_row_count():
+    """Rounding the row count up to whole workgroups stays in range."""
+    assert exl3.balance_workspace_size((1 << 31) - 1, 8) == exl3.balance_workspace_size(1 << 30, 8)

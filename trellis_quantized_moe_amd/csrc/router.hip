@@ -797,7 +797,7 @@ hipError_t by_row(const RouterParams &p, int block, F f) {
   return hipErrorInvalidValue;
 }
 
-unsigned row_groups(int rows) { return (unsigned)((rows + kRowsPerWg - 1) / kRowsPerWg); }
+unsigned row_groups(int rows) { return ((unsigned)rows + kRowsPerWg - 1) / kRowsPerWg; }
 
 }  // namespace
 
