@@ -333,10 +333,11 @@ def _refuse(what, *args):
     raise Exl3Error(what % args)
 
 
-def _sizes(*sizes):
-    """Sizes that the C ABI takes in 32 bits (ctypes would cut them off)."""
-    if max(sizes) > 0x7fffffff:
-        _refuse("a size of %d is out of range", max(sizes))
+_MAX = 0x7fffffff  # sizes of the C ABI: ctypes would cut a larger one off to 32 bits
+
+
+def _too_large(*sizes):
+    _refuse("a size of %d is out of range", max(sizes))
 
 
 def _matrix(t, rows, cols, name):
@@ -373,7 +374,8 @@ def _pairs(t, rows, topk, name):
 def _router_c(E, topk, scoring, renorm=True, scale=1.0, bias=None):
     if scoring not in SCORING:
         _refuse("scoring must be 'softmax' or 'sigmoid', got %r", scoring)
-    _sizes(topk)
+    if topk > _MAX:
+        _too_large(topk)
     return RouterC(E, topk, SCORING[scoring], 1 if renorm else 0, scale, bias)
 
 
@@ -381,7 +383,8 @@ def _logits(logits):
     if logits.dim() != 2:
         _refuse("logits must be [rows, experts], got %s", list(logits.shape))
     rows, E = logits.shape
-    _sizes(rows, E)
+    if rows > _MAX or E > _MAX:
+        _too_large(rows, E)
     return rows, E, _matrix(logits, rows, E, "logits")
 
 
@@ -421,7 +424,8 @@ def alloc_balance(num_experts, device="cuda"):
 
 @functools.lru_cache(maxsize=1024)
 def balance_workspace_size(rows, num_experts):
-    _sizes(rows, num_experts)
+    if rows > _MAX or num_experts > _MAX:
+        _too_large(rows, num_experts)
     return lib().exl3_balance_workspace_size(rows, num_experts)
 
 
@@ -481,7 +485,8 @@ def exl3_route_backward(logits, ids, dw=None, scoring="softmax", renorm=True, sc
 
 @functools.lru_cache(maxsize=1024)
 def lora_workspace_size(rows, in_f, rank, num_adapters):
-    _sizes(rows, in_f, rank, num_adapters)
+    if max(rows, in_f, rank, num_adapters) > _MAX:
+        _too_large(rows, in_f, rank, num_adapters)
     return lib().exl3_lora_workspace_size(rows, in_f, rank, num_adapters)
 
 
@@ -499,7 +504,8 @@ def exl3_lora(x, a, b, ids, scale=None, ranks=None, base=None, out_dtype=None, o
         _refuse("x must have two dimensions, a and b three")
     rows, K = x.shape
     n, N, R = b.shape
-    _sizes(rows, K, n, N, R)
+    if rows > _MAX or K > _MAX or n > _MAX or N > _MAX or R > _MAX:
+        _too_large(rows, K, n, N, R)
     if a.shape != (n, R, K):
         _refuse("a must be [adapters, rank, in] and b [adapters, out, rank], got %s and %s",
                 list(a.shape), list(b.shape))
