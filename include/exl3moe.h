@@ -368,9 +368,11 @@ int32_t exl3_route_topk(const exl3_router *router, const void *logits, int32_t l
  *   count_e = number of IDs equal to e       prob_e = (sum over rows of p_te) / T
  *   loss = coef * num_experts * sum_e (count_e / (T topk)) * prob_e
  * (T == 0: loss and prob are 0; a row that takes part but has no expert left
- * adds 0 to prob). A t_te below 2^-126 times the row's largest counts as 0. The
- * router's renorm, scale and bias take no part. Sums run in fp32 in a fixed
- * order: the same call gives the same bytes.
+ * adds 0 to prob). t_te is formed in fp32 with the hardware's exp2 and
+ * reciprocal, to (|l_e - m| + 4) 2^-23 of itself, m the row's largest logit
+ * (sigmoid: at most 0); one below 2^-126 times the row's largest counts as 0
+ * (here and in the gradient). The router's renorm, scale and bias take no part.
+ * Sums run in fp32 in a fixed order: the same call gives the same bytes.
  * ws: exl3_balance_workspace_size(rows, num_experts) bytes, 16-byte aligned;
  * calls that share it must be ordered on one stream.
  * rows == 0 enqueues the zero results.
@@ -389,7 +391,8 @@ int32_t exl3_balance_loss(const exl3_router *router, const void *logits, int32_t
 
 /*
  * Gradient with respect to the logits, of the weights (dw: [rows][topk] fp16,
- * bf16 or fp32, the gradient of w; NULL: none), of the balance loss (balance
+ * bf16 or fp32, the gradient of w, which the caller forms: exl3_moe_forward has
+ * no backward pass; NULL: none), of the balance loss (balance
  * with its count and tokens as exl3_balance_loss wrote them, prob and loss not
  * read; dloss: device fp32 [1], the gradient of loss, NULL = 1; balance NULL:
  * none), or of both in one pass. ids name the chosen experts (those outside

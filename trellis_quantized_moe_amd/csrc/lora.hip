@@ -3,11 +3,13 @@
 // Two launches: lora_a writes s = x A^T (fp32, R values a row) to the workspace;
 // lora_b multiplies s by B^T, adds the base and stores. Up to 16 ranks mostly
 // take one, lora_kernel, whose workgroups each form the s they need (lora_one).
-// x, base and out are each moved once and the products are under 1% of the
-// matrix rate, so many rows are bound by memory: 16384 rows of 4096 -> 4096 at
-// rank 16, fp32 base, 545 MB: 121 us, 4.5 TB/s (a large copy: 5.0). Few rows
-// are bound by latency: one row 7.8 us, of which an empty launch is 2.5; beyond
-// 16 rows finding the tile is about 3.
+// base and out are moved once; x is read by lora_kernel once for every chunk of
+// columns, by lora_a once for every 64 ranks (every 16 up to 256 rows). The
+// products take 3% of the matrix rate at rank 16 and 9% at rank 64 (before the
+// terms of s are counted), so many rows are bound by memory: 16384 rows of
+// 4096 -> 4096 at rank 16, fp32 base, 545 MB: 124 us, 4.4 TB/s (a large copy:
+// 5.0). Few rows are bound by latency: one row 8.2 us, of which an empty launch
+// is 2.5; beyond 16 rows finding the tile is about 3.
 //
 // Tiles. A tile is up to 32 rows of one adapter (16 in lora_kernel). Every
 // workgroup of lora_a and lora_kernel finds its tile by itself: rows are taken
@@ -755,10 +757,11 @@ __device__ __forceinline__ void copy_rows(const LoraParams &p, const int *tile_r
 }
 
 // Workgroup (tile, `cols` columns, window): each wave takes a quarter of the
-// columns. 4001 rows of 2048 columns at rank 64, bf16, 34 MB: 19.5 us, a chain
-// of loads (tile, sums, B, base) that two workgroups to a CU do not hide: without
-// base 2 us less, without the sums 3, without B 1, without the stores 5. 16384
-// rows of 4096 columns, fp16, 276 MB: 89 us, 3.1 TB/s.
+// columns. 4001 rows of 2048 columns at rank 64, bf16, 34 MB: 21.8 us, a chain
+// of loads (tile, sums, B, base) that two workgroups to a CU do not hide (at 19.5
+// us, with two terms of s: without base 2 us less, without the sums 3, without B
+// 1, without the stores 5). 16384 rows of 4096 columns, fp16, 276 MB: 91 us, 3.0
+// TB/s.
 // 32 ranks with a 16-bit base: three waves a SIMD (70 us instead of 80 on 16384
 // rows of 4096 columns, bf16); more ranks or an fp32 base do not fit.
 template <int RT, bool BF16, int BASE>
@@ -923,8 +926,10 @@ size_t lora_tiles(int rows, int adapters) {
 // (in us, one launch and two, fp16 base: 4096 -> 4096 at rank 16, 1 row 7.8 and
 // 8.1, 256 rows 10.6 and 12.4, 16384 rows 100 and 107; 6144 -> 192 at rank 8, 9.2
 // and 7.4, 11.3 and 11.5, 54 and 56; at rank 64, 4096 -> 4096, 18 and 14 at 256
-// rows, 178 and 139 at 16384), and spares a launch on the host (2.5 us). A long K
-// and few rows leave it too few workgroups for A, which two launches split over K.
+// rows, 178 and 139 at 16384), and spares a launch on the host (2.5 us), which
+// outweighs the 1.8 lost on one row of 6144 -> 192; a replayed graph does not
+// pay it, and loses them. A long K and few rows leave one launch too few
+// workgroups for A, which two launches split over K.
 bool lora_one(const LoraParams &p) {
   return p.R <= 16 && (lora_groups(p.K) <= 4 || p.rows >= 4096);
 }

@@ -426,9 +426,11 @@ __device__ __forceinline__ float bits_to_f32(uint32_t b, int dtype) {
 // go to part_prob[b][E], part_count[b][E] and part_tokens[b]; they are added
 // in the order of b by balance_sum_kernel, so the same call gives the same
 // bytes.
-// The next rows' loads are under way while a row is summed up. 65536 x 256 bf16
-// (35.7 MB): 14.5 us, 2.5 TB/s, bound by the vector instructions (exp2 and rcp
-// run at a quarter of the rate); with expf, division and no rows ahead 50 us.
+// The next rows' loads are under way while a row is summed up. 65536 x 256 bf16,
+// sigmoid (35.7 MB): 14.8 us, 2.4 TB/s. The counters show 22 vector instructions
+// a logit, two of them (exp2, rcp) at a quarter of the rate, and the vector units
+// at work for 10 us of it; the rest is filling up and the last sums. With expf,
+// division and no rows ahead 50 us.
 template <int I, int DT>
 __global__ void __launch_bounds__(balance_threads(I)) balance_kernel(RouterParams p) {
   constexpr int kThreads = balance_threads(I), kWaves = kThreads / 64, kRows = kThreads / 16;
@@ -588,11 +590,13 @@ __global__ void __launch_bounds__(16 * kSumSlices) balance_sum_kernel(RouterPara
 // per logit and 28 us on 32768 x 256.
 //
 // SIG, the scores, is a template argument: with a branch on it 32768 x 256 took
-// 20 us in bf16 (softmax), 22 in fp32 and 23 with sigmoid scores; so it is 18.7,
-// 18.8 and 20.1, and 131072 rows 49 and 54 (2.7 TB/s). Bound by the vector
-// instructions, and at a few iterations a wave by reading, working and writing
-// being done by all waves at the same time. More than 128 registers cost more
-// than they give (sigmoid slopes kept beside the logits: 72 instead of 54).
+// 20 us in bf16 (softmax), 22 in fp32 and 23 with sigmoid scores; so it is 18.2,
+// 19.3 and 19.3, and 131072 rows of bf16 48 (2.8 TB/s). The counters show 33
+// vector instructions a logit: the vector units are at work for 29 us of those 48
+// and for 7 of the 18, where reading, working and writing are done by all waves
+// at the same time and a row's entries cross LDS three times. More than 128
+// registers cost more than they give (sigmoid slopes kept beside the logits: 72
+// instead of 54).
 template <int I, int DT, bool SIG>
 __global__ void __launch_bounds__(256) route_backward_kernel(RouterParams p) {
   __shared__ __align__(16) float s_add[kRowsPerWg][64 * I];

@@ -393,7 +393,9 @@ def exl3_route_topk(logits, topk, scoring="softmax", renorm=True, scale=1.0, bia
     """Router logits [rows, experts] -> (ids, w), both [rows, topk]: the topk
     best experts of every row and their route weights, as exl3_moe_forward
     takes them. ``bias`` (fp32 [experts]) moves the choice only; rows whose
-    ``row_mask`` (bool or uint8 [rows]) is 0 get ID -1 and weight 0."""
+    ``row_mask`` (bool or uint8 [rows]) is 0 get ID -1 and weight 0. The results
+    are not part of autograd's graph: a program that trains the router calls
+    exl3_route_backward itself."""
     rows, E, ld = _logits(logits)
     if bias is not None:
         bias = _vector(bias, E, torch.float32, "bias")
@@ -438,7 +440,8 @@ def _ids_of(ids, rows):
 
 def exl3_balance_loss(logits, ids, scoring="softmax", coef=1.0, balance=None, ws=None):
     """Balance loss of a routing and its per-expert statistics: a dict with
-    "loss" [1], "count" [experts], "prob" [experts] and "tokens" [1]."""
+    "loss" [1], "count" [experts], "prob" [experts] and "tokens" [1]. Not part
+    of autograd's graph; exl3_route_backward gives the gradient."""
     rows, E, ld = _logits(logits)
     topk, idp = _ids_of(ids, rows)
     if balance is None:
@@ -460,7 +463,8 @@ def exl3_route_backward(logits, ids, dw=None, scoring="softmax", renorm=True, sc
     """Gradient with respect to the router's logits: of the route weights
     (``dw`` [rows, topk]), of the balance loss (``balance`` as
     exl3_balance_loss returned it, with ``dloss`` fp32 [1] or None for 1), or
-    of both together."""
+    of both together. ``dw`` is the caller's: exl3_moe_forward has no backward
+    pass."""
     rows, E, ld = _logits(logits)
     topk, idp = _ids_of(ids, rows)
     dwp, dwt = None, 0
@@ -499,7 +503,8 @@ def exl3_lora(x, a, b, ids, scale=None, ranks=None, base=None, out_dtype=None, o
     16-bit dtype; ``scale`` (fp32) and ``ranks`` (int32, the ranks in use) hold
     one value per adapter. ``base`` and ``out`` [rows, out] may be column
     slices of wider tensors; ``out=base`` adds in place. Without ``out`` the
-    result has ``out_dtype``, by default that of ``base`` or else of ``x``."""
+    result has ``out_dtype``, by default that of ``base`` or else of ``x``. The
+    result is not part of autograd's graph."""
     if x.dim() != 2 or a.dim() != 3 or b.dim() != 3:
         _refuse("x must have two dimensions, a and b three")
     rows, K = x.shape
