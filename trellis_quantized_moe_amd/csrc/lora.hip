@@ -641,8 +641,9 @@ __device__ __forceinline__ void lora_b_columns(const LoraParams &p, R row_of, in
     constexpr uint16_t kInf = BF16 ? 0x7f80 : 0x7c00;
     return __any(t[0] >= kInf || t[1] >= kInf);
   };
-  // acc += s B^T of the staged columns, ranks 16 rt ..: B's operands of COUNT
-  // MFMAs from `first` on at a time
+
+  // acc += s B^T of the staged columns, ranks 16 rt ..: `count` column MFMAs from
+  // `first` on
   auto multiply = [&](f32x4(&acc)[4][TT], int rt, auto first, auto count, auto clean) {
     constexpr int i0 = decltype(first)::value, i1 = i0 + decltype(count)::value;
     constexpr bool CLEAN = decltype(clean)::value;
@@ -765,7 +766,8 @@ __device__ __forceinline__ void copy_rows(const LoraParams &p, const int *tile_r
 // 32 ranks with a 16-bit base: three waves a SIMD (70 us instead of 80 on 16384
 // rows of 4096 columns, bf16); more ranks or an fp32 base do not fit.
 template <int RT, bool BF16, int BASE>
-__global__ void __launch_bounds__(256, RT == 2 && BASE <= 2 ? 3 : 1) lora_b_kernel(LoraParams p, int cols, int groups) {
+__global__ void __launch_bounds__(256, RT == 2 && BASE <= 2 ? 3 : 1)
+    lora_b_kernel(LoraParams p, int cols, int groups) {
   __shared__ __align__(16) LdsB<RT, kTileRows, 4> S;
   __shared__ __align__(16) char stages[LdsB<RT, kTileRows, 4>::kStage];
   const LoraTile *tile = p.tiles + (int64_t)blockIdx.z * gridDim.x + blockIdx.x;
