@@ -59,12 +59,16 @@ enum exl3_status {
   EXL3_E_NULL = -1,      /* a required pointer is NULL */
   EXL3_E_DTYPE = -2,     /* unsupported dtype enum for that argument */
   EXL3_E_SHAPE = -3,     /* dimension not a positive multiple of 128 (of 8:
-                            exl3_lora), gate/up/down shapes inconsistent, or
-                            a row distance out of range */
-  EXL3_E_ALIGN = -4,     /* x, out, base, ws, trellis tensors, adapters and
-                            projection tables must be 16-byte aligned; ids,
-                            logits, route weights and route metadata need
-                            the natural alignment of their element type */
+                            exl3_lora, exl3_permute and the calls after it; of
+                            the group size: in_features of exl3_w4_linear),
+                            gate/up/down shapes inconsistent, or a row
+                            distance out of range */
+  EXL3_E_ALIGN = -4,     /* x, y, out, dout, dy, base, ws, trellis tensors,
+                            adapters, 4-bit weights with their scales and
+                            zeros, and projection tables must be 16-byte
+                            aligned; ids, logits, route weights and route
+                            metadata need the natural alignment of their
+                            element type */
   EXL3_E_DEVICE = -5,    /* a pointer is not device memory of the current
                             device, or no HIP device is usable */
   EXL3_E_WORKSPACE = -6, /* workspace NULL or smaller than *_workspace_size */
@@ -84,6 +88,7 @@ enum exl3_status {
 #define EXL3_MAX_RANK 128
 #define EXL3_LORA_MAX_ROWS (1 << 26)
 #define EXL3_LORA_MAX_LD (1 << 19)
+#define EXL3_MAX_PAIRS (1 << 30) /* exl3_permute and the calls after it */
 
 int32_t exl3_abi_version(void);
 /* Static string for a status code (host; never NULL). */
@@ -169,7 +174,8 @@ enum exl3_kernel_id {
   EXL3_K_EXPERTS = 8, /* 128-row tiles: gate/up and down of a single pass in one launch, or one
                          launch of the passes pipelined across launches */
   EXL3_K_ROUTE = 9, EXL3_K_BALANCE = 10, EXL3_K_BALANCE_SUM = 11, EXL3_K_ROUTE_BACKWARD = 12,
-  EXL3_K_LORA_A = 13, EXL3_K_LORA_B = 14, EXL3_K_LORA = 15 /* both in one */
+  EXL3_K_LORA_A = 13, EXL3_K_LORA_B = 14, EXL3_K_LORA = 15, /* both in one */
+  EXL3_K_PERMUTE = 16, EXL3_K_UNPERMUTE = 17, EXL3_K_UNPERMUTE_BACKWARD = 18, EXL3_K_W4 = 19
 };
 typedef struct exl3_profile {
   void **events;        /* host: 2 * cap event handles (hipEvent_t) */
@@ -451,6 +457,91 @@ int32_t exl3_lora(const exl3_lora_adapters *adapters, const uint16_t *x, int32_t
                   const void *base, int32_t base_dtype, int64_t ld_base, void *out,
                   int32_t out_dtype, int64_t ld_out, void *ws, size_t ws_bytes, void *stream,
                   exl3_profile *prof);
+
+/*
+ * Rows carried to experts of any kind and back, and the gradient of that.
+ * pos_of_pair: [rows][topk] as exl3_route_pack writes it: the packed position
+ * of choice (t, j). A position outside [0, rows * topk) (-1: dropped) takes no
+ * part; no two choices share one. Every packed tensor (out of exl3_permute, y,
+ * dy) has rows * topk rows, of which those at no choice's position (past the
+ * last kept pair) are neither read nor written. Sums are kept in fp32 and
+ * results rounded once; a row's bytes do not depend on the other rows or
+ * their number.
+ *
+ * rows * topk: at most EXL3_MAX_PAIRS. features: multiple of 8, at most
+ * EXL3_MAX_FEATURES. Row distances: in elements, at least a row, at most 2^32
+ * and a multiple of 16 bytes. Outputs overlap no input.
+ *
+ * exl3_permute: out[pos(t, j)] = x[t], bytes as they are. dtype (of both):
+ * fp16, bf16 or fp32.
+ */
+int32_t exl3_permute(const void *x, int32_t dtype, int64_t ld_x, int32_t rows, int32_t topk,
+                     int32_t features, const int32_t *pos_of_pair, void *out, int64_t ld_out,
+                     void *stream, exl3_profile *prof);
+/*
+ * out[t] = sum over j, ascending, of w[t][j] y[pos(t, j)]; a row without a
+ * choice that takes part is zeros. w: [rows][topk] fp16, bf16 or fp32, or NULL
+ * (all 1), which makes it the gradient of exl3_permute with respect to x (y: the
+ * gradient of its out). y, out: fp16, bf16 or fp32 each.
+ */
+int32_t exl3_unpermute(const void *y, int32_t y_dtype, int64_t ld_y, int32_t rows, int32_t topk,
+                       int32_t features, const int32_t *pos_of_pair, const void *w,
+                       int32_t w_dtype, void *out, int32_t out_dtype, int64_t ld_out,
+                       void *stream, exl3_profile *prof);
+/*
+ * Gradient of exl3_unpermute, dout [rows] being that of its out:
+ *   dy[pos(t, j)] = w[t][j] dout[t]          (w NULL: all 1)
+ *   dw[t][j]      = sum over h of dout[t][h] y[pos(t, j)][h]
+ * and 0 for a choice that takes no part: the dw of exl3_route_backward. dy has
+ * y's dtype. y and dw both NULL: dy alone (y_dtype is then dy's; ld_y and
+ * dw_dtype are not used). dw: [rows][topk] fp16, bf16 or fp32.
+ */
+int32_t exl3_unpermute_backward(const void *dout, int32_t dout_dtype, int64_t ld_dout,
+                                int32_t rows, int32_t topk, int32_t features,
+                                const int32_t *pos_of_pair, const void *y, int32_t y_dtype,
+                                int64_t ld_y, const void *w, int32_t w_dtype, void *dy,
+                                int64_t ld_dy, void *dw, int32_t dw_dtype, void *stream,
+                                exl3_profile *prof);
+
+/*
+ * Products with 4-bit weights and group scales, from one row to a prompt: of
+ * packed rows with their experts' weights (expert_offset [num_experts + 1] as
+ * exl3_route_pack writes it), or of all rows with one projection's
+ * (num_experts 1, expert_offset NULL):
+ *   out[p][n] = sum over k of x[p][k] scale[e][n][k / G] (q[e][n][k] - zero[e][n][k / G])
+ * for expert_offset[e] <= p < expert_offset[e + 1]. The weights enter the sums
+ * as the whole numbers q - zero and the scales in fp32: no weight is rounded.
+ * Rows outside every expert's range are not written; offsets are clamped to
+ * [0, rows], and ranges that overlap or descend leave rows unwritten or
+ * written by either expert. A row's bytes do not depend on the other rows,
+ * their number or their order. A serving operator: it has no backward pass.
+ *
+ * Layout, KT = ceil(K / 128), NT = ceil(N / 16), what lies past K or N zeros:
+ *   q     [E][NT][KT][64][4] words: word i of lane 16 kg + n of tile (nt, kt)
+ *         holds inputs 128 kt + 32 i + 8 kg + 0..7 of output 16 nt + n, those
+ *         numbered 0, 2, 4, 6, 1, 3, 5, 7 in bits 0-3, 4-7, .. 28-31
+ *   scale [E][NT][KT][128 / G][16] fp16 or bf16: group 128 / G * kt + g of
+ *         output 16 nt + n
+ *   zero  the same order, uint8 (its lower 4 bits), or NULL (all 8)
+ */
+typedef struct exl3_w4 {
+  int32_t in_features;  /* K: multiple of group_size, at most EXL3_MAX_FEATURES */
+  int32_t out_features; /* N: multiple of 8, at most EXL3_MAX_FEATURES */
+  int32_t num_experts;  /* 1 .. EXL3_MAX_EXPERTS */
+  int32_t group_size;   /* G: 32, 64 or 128 */
+  const uint32_t *q;
+  const uint16_t *scale;
+  const uint8_t *zero;
+  int32_t scale_dtype;
+} exl3_w4;
+/*
+ * x: [rows][K] fp16 or bf16, ld_x elements apart; out: [rows][N] fp16, bf16 or
+ * fp32, ld_out apart (row distances as exl3_permute); out overlaps no input.
+ * rows: at most EXL3_MAX_PAIRS.
+ */
+int32_t exl3_w4_linear(const exl3_w4 *weight, const uint16_t *x, int32_t x_dtype, int64_t ld_x,
+                       int32_t rows, const int32_t *expert_offset, void *out, int32_t out_dtype,
+                       int64_t ld_out, void *stream, exl3_profile *prof);
 
 /*
  * Diagnostic: decode `ntiles` consecutive trellis tiles of width K with the

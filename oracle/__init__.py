@@ -27,6 +27,8 @@ Modules:
   moe       routed-experts layer (gate/up, SwiGLU, down, top-k combine)
   router    top-k router, balance loss and their gradient (own definitions)
   lora      low-rank adapters beside a shared projection (own definition)
+  permute   rows to experts and back, and the gradient (own definitions)
+  w4        products with 4-bit weights and group scales (own definition)
   brute     dense dequantise-then-matmul brute force for tiny shapes
 
 Every function here is pinned by ``tests/test_oracle_*.py`` (``-m "not gpu"``)
@@ -34,4 +36,5 @@ against closed forms, library routines, brute force or the format's printed
 test vectors; none is "parity unpinned".
 """
 
-from . import trellis, hadamard, linear, route, moe, router, lora, brute  # noqa: F401
+from . import trellis, hadamard, linear, route, moe, router, lora  # noqa: F401
+from . import permute, w4, brute  # noqa: F401

@@ -488,7 +488,7 @@ const char *exl3_status_string(int32_t s) {
     case EXL3_E_DTYPE: return "unsupported dtype";
     case EXL3_E_SHAPE:
       return "bad or inconsistent shape (features must be positive multiples of 128, of 8 for "
-             "exl3_lora; row distances at least a row)";
+             "exl3_lora, exl3_permute and the calls after it; row distances at least a row)";
     case EXL3_E_ALIGN: return "pointer or row distance not aligned (16 bytes, or the element type's size)";
     case EXL3_E_DEVICE: return "pointer not on the current HIP device (or no device)";
     case EXL3_E_WORKSPACE: return "workspace missing or too small";
@@ -1154,6 +1154,185 @@ int32_t exl3_lora(const exl3_lora_adapters *ad, const uint16_t *x, int32_t x_dty
   }
   ProfScope ps(prof, st, EXL3_K_LORA_B);
   return launch_lora_b(p, st) == hipSuccess ? EXL3_OK : EXL3_E_LAUNCH;
+}
+
+}  // extern "C"
+
+// ------------------------------------------- rows to experts and their products
+namespace {
+
+// What every call that carries rows is given.
+int32_t check_move(int32_t rows, int32_t topk, int32_t features) {
+  if (rows < 0 || topk < 1 || topk > EXL3_MAX_TOPK) return EXL3_E_ARG;
+  if ((int64_t)rows * topk > EXL3_MAX_PAIRS) return EXL3_E_ARG;
+  if (features < 8 || features > EXL3_MAX_FEATURES || features % 8) return EXL3_E_SHAPE;
+  return EXL3_OK;
+}
+// A matrix of `cols` values a row, `ld` elements apart.
+int32_t check_rows(const void *p, int32_t dtype, int64_t ld, int64_t cols) {
+  if (ld < cols || ld > kMaxLd) return EXL3_E_SHAPE;
+  if (!aligned16(p) || ld * (int64_t)float_size(dtype) % 16) return EXL3_E_ALIGN;
+  return EXL3_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int32_t exl3_permute(const void *x, int32_t dtype, int64_t ld_x, int32_t rows, int32_t topk,
+                     int32_t features, const int32_t *pos_of_pair, void *out, int64_t ld_out,
+                     void *stream, exl3_profile *prof) {
+  if (int32_t s = check_move(rows, topk, features)) return s;
+  if (!float_dtype_ok(dtype)) return EXL3_E_DTYPE;
+  if (rows == 0) return EXL3_OK;
+  if (!x || !pos_of_pair || !out) return EXL3_E_NULL;
+  if (int32_t s = check_rows(x, dtype, ld_x, features)) return s;
+  if (int32_t s = check_rows(out, dtype, ld_out, features)) return s;
+  if (!aligned_to(pos_of_pair, 4)) return EXL3_E_ALIGN;
+  if (x == out) return EXL3_E_ARG;
+  for (const void *q : {x, (const void *)pos_of_pair, (const void *)out})
+    if (check_device(q)) return EXL3_E_DEVICE;
+
+  MoveParams p{};
+  p.pos = pos_of_pair;
+  p.rows = rows;
+  p.topk = topk;
+  p.pairs = rows * topk;
+  p.features = features;
+  p.x = x;
+  p.esize = (int)float_size(dtype);
+  p.ldx = ld_x;
+  p.out = out;
+  p.ldout = ld_out;
+  ProfScope ps(prof, (hipStream_t)stream, EXL3_K_PERMUTE);
+  return launch_permute(p, (hipStream_t)stream) == hipSuccess ? EXL3_OK : EXL3_E_LAUNCH;
+}
+
+int32_t exl3_unpermute(const void *y, int32_t y_dtype, int64_t ld_y, int32_t rows, int32_t topk,
+                       int32_t features, const int32_t *pos_of_pair, const void *w,
+                       int32_t w_dtype, void *out, int32_t out_dtype, int64_t ld_out,
+                       void *stream, exl3_profile *prof) {
+  if (int32_t s = check_move(rows, topk, features)) return s;
+  if (!float_dtype_ok(y_dtype) || !float_dtype_ok(out_dtype) || (w && !float_dtype_ok(w_dtype)))
+    return EXL3_E_DTYPE;
+  if (rows == 0) return EXL3_OK;
+  if (!y || !pos_of_pair || !out) return EXL3_E_NULL;
+  if (int32_t s = check_rows(y, y_dtype, ld_y, features)) return s;
+  if (int32_t s = check_rows(out, out_dtype, ld_out, features)) return s;
+  if (!aligned_to(pos_of_pair, 4) || (w && !aligned_to(w, w_align(w_dtype)))) return EXL3_E_ALIGN;
+  if (y == out) return EXL3_E_ARG;
+  for (const void *q : {y, (const void *)pos_of_pair, w, (const void *)out})
+    if (q && check_device(q)) return EXL3_E_DEVICE;
+
+  MoveParams p{};
+  p.pos = pos_of_pair;
+  p.rows = rows;
+  p.topk = topk;
+  p.pairs = rows * topk;
+  p.features = features;
+  p.x = y;
+  p.x_dtype = y_dtype;
+  p.ldx = ld_y;
+  p.w = w;
+  p.w_dtype = w_dtype;
+  p.out = out;
+  p.o_dtype = out_dtype;
+  p.ldout = ld_out;
+  ProfScope ps(prof, (hipStream_t)stream, EXL3_K_UNPERMUTE);
+  return launch_unpermute(p, (hipStream_t)stream) == hipSuccess ? EXL3_OK : EXL3_E_LAUNCH;
+}
+
+int32_t exl3_unpermute_backward(const void *dout, int32_t dout_dtype, int64_t ld_dout,
+                                int32_t rows, int32_t topk, int32_t features,
+                                const int32_t *pos_of_pair, const void *y, int32_t y_dtype,
+                                int64_t ld_y, const void *w, int32_t w_dtype, void *dy,
+                                int64_t ld_dy, void *dw, int32_t dw_dtype, void *stream,
+                                exl3_profile *prof) {
+  if (int32_t s = check_move(rows, topk, features)) return s;
+  if (!float_dtype_ok(dout_dtype) || !float_dtype_ok(y_dtype) || (w && !float_dtype_ok(w_dtype)) ||
+      (dw && !float_dtype_ok(dw_dtype)))
+    return EXL3_E_DTYPE;
+  if (rows == 0) return EXL3_OK;
+  if (!dout || !pos_of_pair || !dy || !y != !dw) return EXL3_E_NULL;
+  if (int32_t s = check_rows(dout, dout_dtype, ld_dout, features)) return s;
+  if (int32_t s = check_rows(dy, y_dtype, ld_dy, features)) return s;
+  if (y)
+    if (int32_t s = check_rows(y, y_dtype, ld_y, features)) return s;
+  if (!aligned_to(pos_of_pair, 4) || (w && !aligned_to(w, w_align(w_dtype))) ||
+      (dw && !aligned_to(dw, w_align(dw_dtype))))
+    return EXL3_E_ALIGN;
+  if (dy == dout || dy == y || (dw && dw == w)) return EXL3_E_ARG;
+  for (const void *q : {dout, (const void *)pos_of_pair, y, w, (const void *)dy, (const void *)dw})
+    if (q && check_device(q)) return EXL3_E_DEVICE;
+
+  MoveParams p{};
+  p.pos = pos_of_pair;
+  p.rows = rows;
+  p.topk = topk;
+  p.pairs = rows * topk;
+  p.features = features;
+  p.x = y;
+  p.x_dtype = y_dtype;
+  p.ldx = ld_y;
+  p.w = w;
+  p.w_dtype = w_dtype;
+  p.out = dy;
+  p.ldout = ld_dy;
+  p.dout = dout;
+  p.o_dtype = dout_dtype;
+  p.lddout = ld_dout;
+  p.dw = dw;
+  p.dw_dtype = dw_dtype;
+  ProfScope ps(prof, (hipStream_t)stream, EXL3_K_UNPERMUTE_BACKWARD);
+  return launch_unpermute_backward(p, (hipStream_t)stream) == hipSuccess ? EXL3_OK
+                                                                         : EXL3_E_LAUNCH;
+}
+
+int32_t exl3_w4_linear(const exl3_w4 *weight, const uint16_t *x, int32_t x_dtype, int64_t ld_x,
+                       int32_t rows, const int32_t *expert_offset, void *out, int32_t out_dtype,
+                       int64_t ld_out, void *stream, exl3_profile *prof) {
+  if (rows < 0 || rows > EXL3_MAX_PAIRS) return EXL3_E_ARG;
+  if (!weight) return EXL3_E_NULL;
+  const int64_t K = weight->in_features, N = weight->out_features, G = weight->group_size;
+  if (weight->num_experts < 1 || weight->num_experts > EXL3_MAX_EXPERTS) return EXL3_E_ARG;
+  if (G != 32 && G != 64 && G != 128) return EXL3_E_ARG;
+  if (K < 1 || K > EXL3_MAX_FEATURES || K % G) return EXL3_E_SHAPE;
+  if (N < 8 || N > EXL3_MAX_FEATURES || N % 8) return EXL3_E_SHAPE;
+  if (!x_dtype_ok(x_dtype) || !x_dtype_ok(weight->scale_dtype) || !out_dtype_ok(out_dtype))
+    return EXL3_E_DTYPE;
+  if (rows == 0) return EXL3_OK;
+  if (!weight->q || !weight->scale || !x || !out) return EXL3_E_NULL;
+  if (!expert_offset && weight->num_experts != 1) return EXL3_E_NULL;
+  if (int32_t s = check_rows(x, x_dtype, ld_x, K)) return s;
+  if (int32_t s = check_rows(out, out_dtype, ld_out, N)) return s;
+  if (!aligned16(weight->q) || !aligned16(weight->scale) || !aligned16(weight->zero) ||
+      !aligned_to(expert_offset, 4))
+    return EXL3_E_ALIGN;
+  if ((const void *)x == out) return EXL3_E_ARG;
+  for (const void *q : {(const void *)weight->q, (const void *)weight->scale,
+                        (const void *)weight->zero, (const void *)x, (const void *)expert_offset,
+                        (const void *)out})
+    if (q && check_device(q)) return EXL3_E_DEVICE;
+
+  W4Params p{};
+  p.K = (int)K;
+  p.N = (int)N;
+  p.E = weight->num_experts;
+  p.group = (int)G;
+  p.q = weight->q;
+  p.scale = weight->scale;
+  p.zero = weight->zero;
+  p.scale_bf16 = weight->scale_dtype == EXL3_BF16;
+  p.x = x;
+  p.bf16 = x_dtype == EXL3_BF16;
+  p.ldx = ld_x;
+  p.rows = rows;
+  p.offset = expert_offset;
+  p.out = out;
+  p.out_dtype = out_dtype;
+  p.ldout = ld_out;
+  ProfScope ps(prof, (hipStream_t)stream, EXL3_K_W4);
+  return launch_w4(p, (hipStream_t)stream) == hipSuccess ? EXL3_OK : EXL3_E_LAUNCH;
 }
 
 }  // extern "C"

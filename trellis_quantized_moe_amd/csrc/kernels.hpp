@@ -180,6 +180,43 @@ struct LoraParams {
   LoraTile *tiles;  // [lora_tiles(rows, adapters)]
 };
 
+// Rows carried to experts and back (permute.hip). dtype codes as RouterParams.
+struct MoveParams {
+  const int32_t *pos;  // [rows][topk] packed position, outside [0, pairs): dropped
+  int rows, topk, pairs, features;
+  const void *x;  // permute: [rows], else y: [pairs], ldx apart (backward: null without dw)
+  int x_dtype;    // of y and dy
+  int esize;      // permute: bytes of a value
+  int64_t ldx;
+  const void *w;  // [rows][topk] or null (all 1)
+  int w_dtype;
+  void *out;  // permute: [pairs], unpermute: [rows], backward: dy [pairs]
+  int o_dtype;  // of out, of dout in backward
+  int64_t ldout;
+  const void *dout;  // backward: [rows]
+  int64_t lddout;
+  void *dw;  // backward: [rows][topk] or null
+  int dw_dtype;
+};
+
+// Products with 4-bit weights (w4.hip).
+struct W4Params {
+  int K, N, E, group;
+  const uint32_t *q;      // [E][ceil(N / 16)][ceil(K / 128)][64][4]
+  const uint16_t *scale;  // [E][ceil(N / 16)][ceil(K / 128)][128 / group][16]
+  const uint8_t *zero;    // the same, or null (all 8)
+  int scale_bf16;
+  const uint16_t *x;  // [rows][K], rows ldx apart
+  int bf16;
+  int64_t ldx;
+  int rows;
+  const int32_t *offset;  // [E + 1] or null (one expert)
+  int first_tile;         // of row tiles, set by the launcher
+  void *out;              // [rows][N], rows ldout apart; dtype codes as RouterParams
+  int out_dtype;
+  int64_t ldout;
+};
+
 hipError_t launch_gemm(int epi, const GemmParams &p, int tiles, int nblocks,
                        hipStream_t s, bool wide);
 // 128-row tiles (gemm_wide.hip); called by launch_gemm.
@@ -227,6 +264,10 @@ bool lora_one(const LoraParams &p);  // whether the call takes one launch
 hipError_t launch_lora_one(const LoraParams &p, hipStream_t s);
 hipError_t launch_lora_a(const LoraParams &p, hipStream_t s);
 hipError_t launch_lora_b(const LoraParams &p, hipStream_t s);
+hipError_t launch_permute(const MoveParams &p, hipStream_t s);
+hipError_t launch_unpermute(const MoveParams &p, hipStream_t s);
+hipError_t launch_unpermute_backward(const MoveParams &p, hipStream_t s);
+hipError_t launch_w4(const W4Params &p, hipStream_t s);
 
 constexpr int kBM = 16;       // rows per narrow GEMM work tile
 constexpr int kMaxTopk = 32;  // EXL3_MAX_TOPK

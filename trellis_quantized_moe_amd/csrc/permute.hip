@@ -1,0 +1,272 @@
+// Rows carried to experts and back. Row t has topk choices; choice (t, j) stands
+// at position pos(t, j) of the packed rows (pos_of_pair, -1: dropped).
+//   permute    xs[pos(t, j)] = x[t]
+//   unpermute  out[t] = sum_j w[t, j] y[pos(t, j)]     in fp32, j ascending
+//   backward   dy[pos(t, j)] = w[t, j] dout[t],  dw[t, j] = <dout[t], y[pos(t, j)]>
+// Nothing is computed that costs time: all three are bound by the bytes they
+// move. Work is cut by row t, so that the side that has one row per token (x,
+// out, dout) is moved once, and its topk packed rows are whole rows wherever
+// they stand. A lane moves 16 bytes (8 values) at a time; a row takes the lanes
+// it fills (up to 256), so short rows share a wave.
+#include "common.hpp"
+#include "kernels.hpp"
+
+namespace exl3 {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kBatch = 8;  // choices whose packed rows are in flight together
+
+// Eight consecutive values as stored (dtype codes: 1 fp16, 2 bf16, 3 fp32).
+template <int DT>
+struct Eight {
+  u32x4 v[DT == 3 ? 2 : 1];
+};
+template <int DT>
+__device__ __forceinline__ Eight<DT> load_eight(const char *p) {
+  Eight<DT> r;
+  r.v[0] = *(const u32x4 *)p;
+  if constexpr (DT == 3) r.v[1] = *(const u32x4 *)(p + 16);
+  return r;
+}
+template <int DT>
+__device__ __forceinline__ void unpack(const Eight<DT> &e, float (&f)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if constexpr (DT == 3) {
+      const uint32_t b = e.v[i >> 2][i & 3];
+      f[i] = __builtin_bit_cast(float, b);
+    } else {
+      const uint16_t b = (uint16_t)(e.v[0][i >> 1] >> (16 * (i & 1)));
+      f[i] = DT == 2 ? bf16_bits_to_f32(b) : f16_bits_to_f32(b);
+    }
+  }
+}
+template <int DT>
+__device__ __forceinline__ void store_eight(char *p, const float (&f)[8]) {
+  if constexpr (DT == 3) {
+    *(f32x4 *)p = (f32x4){f[0], f[1], f[2], f[3]};
+    *(f32x4 *)(p + 16) = (f32x4){f[4], f[5], f[6], f[7]};
+  } else {
+    u32x4 v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = f32x2_to_out16(f[2 * i], f[2 * i + 1], DT == 2);
+    *(u32x4 *)p = v;
+  }
+}
+__device__ __forceinline__ float load_weight(const void *w, int dtype, int64_t i) {
+  if (dtype == 3) return ((const float *)w)[i];
+  const uint16_t b = ((const uint16_t *)w)[i];
+  return dtype == 2 ? bf16_bits_to_f32(b) : f16_bits_to_f32(b);
+}
+
+// A block holds blockDim.y rows of blockDim.x lanes; blocks step over groups of
+// rows, since one axis of a launch is shorter than the longest call.
+__device__ __forceinline__ int64_t row_groups(const MoveParams &p) {
+  return ((int64_t)p.rows + blockDim.y - 1) / blockDim.y;
+}
+
+__global__ void __launch_bounds__(kThreads) permute_kernel(MoveParams p) {
+  const int units = (int)((int64_t)p.features * p.esize / 16);
+  const int u = blockIdx.y * blockDim.x + threadIdx.x;
+  for (int64_t g = blockIdx.x; g < row_groups(p); g += gridDim.x) {
+    const int64_t t = g * blockDim.y + threadIdx.y;
+    if (t >= p.rows || u >= units) continue;
+    const u32x4 v = *(const u32x4 *)((const char *)p.x + t * p.ldx * p.esize + 16 * (int64_t)u);
+    for (int j = 0; j < p.topk; ++j) {
+      const int q = p.pos[t * p.topk + j];
+      if ((uint32_t)q < (uint32_t)p.pairs)
+        *(u32x4 *)((char *)p.out + q * p.ldout * p.esize + 16 * (int64_t)u) = v;
+    }
+  }
+}
+
+// DY: type of y, DO: of out. B choices at once.
+template <int DY, int DO, int B>
+__global__ void __launch_bounds__(kThreads) unpermute_kernel(MoveParams p) {
+  constexpr int SY = DY == 3 ? 4 : 2, SO = DO == 3 ? 4 : 2;
+  const int u = blockIdx.y * blockDim.x + threadIdx.x;
+  for (int64_t g = blockIdx.x; g < row_groups(p); g += gridDim.x) {
+    const int64_t t = g * blockDim.y + threadIdx.y;
+    if (t >= p.rows || 8 * u >= p.features) continue;
+    float acc[8] = {};
+    for (int j0 = 0; j0 < p.topk; j0 += B) {
+      Eight<DY> raw[B];
+      bool held[B];
+      float w[B];
+#pragma unroll
+      for (int i = 0; i < B; ++i) {
+        const int64_t pair = t * p.topk + min(j0 + i, p.topk - 1);
+        const int q = p.pos[pair];
+        held[i] = j0 + i < p.topk && (uint32_t)q < (uint32_t)p.pairs;
+        w[i] = p.w ? load_weight(p.w, p.w_dtype, pair) : 1.f;
+        // a dropped choice reads row 0 and is not added
+        raw[i] = load_eight<DY>((const char *)p.x + ((held[i] ? q : 0) * p.ldx + 8 * u) * SY);
+      }
+#pragma unroll
+      for (int i = 0; i < B; ++i) {
+        float y[8];
+        unpack<DY>(raw[i], y);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) acc[k] = held[i] ? fmaf(w[i], y[k], acc[k]) : acc[k];
+      }
+    }
+    store_eight<DO>((char *)p.out + (t * p.ldout + 8 * u) * SO, acc);
+  }
+}
+
+// DY: type of y and dy, DO: of dout. WITH_DW: y is read and dw written. A
+// block's lanes cover a whole row, so that <dout, y> needs no second launch.
+template <int DY, int DO, bool WITH_DW>
+__global__ void __launch_bounds__(kThreads) unpermute_backward_kernel(MoveParams p) {
+  constexpr int SY = DY == 3 ? 4 : 2, SO = DO == 3 ? 4 : 2;
+  __shared__ float part[kThreads / 64][kBatch];
+  const int lanes = blockDim.x;  // a power of two
+  const int units = p.features / 8;
+  for (int64_t g = blockIdx.x; g < row_groups(p); g += gridDim.x) {
+    const int64_t t = g * blockDim.y + threadIdx.y;
+    const bool in = t < p.rows;
+    for (int j0 = 0; j0 < p.topk; j0 += kBatch) {
+      float dot[kBatch] = {};
+      int64_t at[kBatch];  // packed row, -1: none
+      float w[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        at[i] = -1;
+        w[i] = 0.f;
+        if (in && j0 + i < p.topk) {
+          const int64_t pair = t * p.topk + j0 + i;
+          const int q = p.pos[pair];
+          if ((uint32_t)q < (uint32_t)p.pairs) at[i] = q;
+          w[i] = p.w ? load_weight(p.w, p.w_dtype, pair) : 1.f;
+        }
+      }
+      if (in) {
+        for (int u = threadIdx.x; u < units; u += lanes) {
+          float d[8];
+          unpack<DO>(load_eight<DO>((const char *)p.dout + (t * p.lddout + 8 * u) * SO), d);
+          Eight<DY> raw[kBatch];
+          if constexpr (WITH_DW) {
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+              if (at[i] >= 0)
+                raw[i] = load_eight<DY>((const char *)p.x + (at[i] * p.ldx + 8 * u) * SY);
+          }
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
+            if (at[i] < 0) continue;
+            float o[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) o[k] = w[i] * d[k];
+            store_eight<DY>((char *)p.out + (at[i] * p.ldout + 8 * u) * SY, o);
+            if constexpr (WITH_DW) {
+              float y[8];
+              unpack<DY>(raw[i], y);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) dot[i] = fmaf(d[k], y[k], dot[i]);
+            }
+          }
+        }
+      }
+      if constexpr (WITH_DW) {
+        const int within = min(lanes, 64);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+          for (int s = within / 2; s; s >>= 1) dot[i] += __shfl_xor(dot[i], s, 64);
+        if (lanes > 64) {
+          // a row takes all of the block: one value per wave and choice
+          __syncthreads();
+          if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) part[threadIdx.x >> 6][i] = dot[i];
+          }
+          __syncthreads();
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
+            dot[i] = part[0][i];
+            for (int v = 1; v < lanes / 64; ++v) dot[i] += part[v][i];
+          }
+        }
+        if (in && threadIdx.x == 0) {
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
+            if (j0 + i >= p.topk) break;
+            const int64_t pair = t * p.topk + j0 + i;
+            const float v = at[i] >= 0 ? dot[i] : 0.f;
+            if (p.dw_dtype == 3) ((float *)p.dw)[pair] = v;
+            else ((uint16_t *)p.dw)[pair] = f32_to_out16(v, p.dw_dtype == 2);
+          }
+        }
+      }
+    }
+  }
+}
+
+// Lanes of a row of `units` pieces: the power of two that holds them, at most
+// a block, in powers that a block holds a whole number of.
+struct Shape {
+  dim3 grid, block;
+};
+Shape shape(const MoveParams &p, int units, bool whole_row) {
+  int lanes = 1;
+  while (lanes < units && lanes < kThreads) lanes *= 2;
+  if (lanes == kThreads / 2) lanes = kThreads;  // a block's barrier is one row's
+  const int per = kThreads / lanes;
+  const int64_t groups = ((int64_t)p.rows + per - 1) / per;
+  Shape s;
+  s.block = dim3(lanes, per);
+  s.grid = dim3((unsigned)(groups < (1 << 22) ? groups : 1 << 22),
+                whole_row ? 1 : (units + lanes - 1) / lanes);
+  return s;
+}
+
+template <int DY, int DO>
+void unpermute(const MoveParams &p, const Shape &s, hipStream_t st) {
+  if (p.topk == 1) unpermute_kernel<DY, DO, 1><<<s.grid, s.block, 0, st>>>(p);
+  else if (p.topk == 2) unpermute_kernel<DY, DO, 2><<<s.grid, s.block, 0, st>>>(p);
+  else if (p.topk <= 4) unpermute_kernel<DY, DO, 4><<<s.grid, s.block, 0, st>>>(p);
+  else unpermute_kernel<DY, DO, kBatch><<<s.grid, s.block, 0, st>>>(p);
+}
+template <int DY, int DO>
+void backward(const MoveParams &p, const Shape &s, hipStream_t st) {
+  if (p.dw) unpermute_backward_kernel<DY, DO, true><<<s.grid, s.block, 0, st>>>(p);
+  else unpermute_backward_kernel<DY, DO, false><<<s.grid, s.block, 0, st>>>(p);
+}
+
+}  // namespace
+
+hipError_t launch_permute(const MoveParams &p, hipStream_t st) {
+  const Shape s = shape(p, (int)((int64_t)p.features * p.esize / 16), false);
+  permute_kernel<<<s.grid, s.block, 0, st>>>(p);
+  return hipGetLastError();
+}
+
+// Calls F<x_dtype, o_dtype>(p, s, st).
+#define EXL3_BY_TYPES(F)                                  \
+  switch (4 * p.x_dtype + p.o_dtype) {                    \
+    case 5: F<1, 1>(p, s, st); break;                     \
+    case 6: F<1, 2>(p, s, st); break;                     \
+    case 7: F<1, 3>(p, s, st); break;                     \
+    case 9: F<2, 1>(p, s, st); break;                     \
+    case 10: F<2, 2>(p, s, st); break;                    \
+    case 11: F<2, 3>(p, s, st); break;                    \
+    case 13: F<3, 1>(p, s, st); break;                    \
+    case 14: F<3, 2>(p, s, st); break;                    \
+    default: F<3, 3>(p, s, st); break;                    \
+  }
+
+hipError_t launch_unpermute(const MoveParams &p, hipStream_t st) {
+  const Shape s = shape(p, p.features / 8, false);
+  EXL3_BY_TYPES(unpermute)
+  return hipGetLastError();
+}
+
+hipError_t launch_unpermute_backward(const MoveParams &p, hipStream_t st) {
+  const Shape s = shape(p, p.features / 8, true);
+  EXL3_BY_TYPES(backward)
+  return hipGetLastError();
+}
+#undef EXL3_BY_TYPES
+
+}  // namespace exl3

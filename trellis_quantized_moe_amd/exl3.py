@@ -65,6 +65,12 @@ class LoraC(ctypes.Structure):
         (n, ctypes.c_void_p) for n in ("a", "b", "scale", "ranks")]
 
 
+class W4C(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("in_features", "out_features", "num_experts", "group_size")] + [
+        (n, ctypes.c_void_p) for n in ("q", "scale", "zero")] + [("scale_dtype", ctypes.c_int32)]
+
+
 class LayoutC(ctypes.Structure):
     _fields_ = [(n, ctypes.c_size_t) for n in
                 ("ctrl", "meta", "expert_of_pos", "plan", "xt", "at", "d", "yacc",
@@ -109,6 +115,13 @@ _SIGS = {
     "exl3_lora_workspace_size": (_sz, [_i32] * 4),
     "exl3_lora": (_i32, [ctypes.POINTER(LoraC), _vp, _i32, _i64, _i32, _vp, _i32, _vp, _i32, _i64,
                          _vp, _i32, _i64, _vp, _sz, _vp, _PP]),
+    "exl3_permute": (_i32, [_vp, _i32, _i64, _i32, _i32, _i32, _vp, _vp, _i64, _vp, _PP]),
+    "exl3_unpermute": (_i32, [_vp, _i32, _i64, _i32, _i32, _i32, _vp, _vp, _i32, _vp, _i32, _i64,
+                              _vp, _PP]),
+    "exl3_unpermute_backward": (_i32, [_vp, _i32, _i64, _i32, _i32, _i32, _vp, _vp, _i32, _i64,
+                                       _vp, _i32, _vp, _i64, _vp, _i32, _vp, _PP]),
+    "exl3_w4_linear": (_i32, [ctypes.POINTER(W4C), _vp, _i32, _i64, _i32, _vp, _vp, _i32, _i64,
+                              _vp, _PP]),
     "exl3_decode_tiles": (_i32, [_vp, _i32, _i32, _vp, _vp, _PP]),
     "exl3_events_create": (_i32, [_i32, ctypes.POINTER(ctypes.c_void_p)]),
     "exl3_events_destroy": (_i32, [_i32, ctypes.POINTER(ctypes.c_void_p)]),
@@ -117,7 +130,8 @@ _SIGS = {
 KERNEL_NAMES = {1: "route_pack", 2: "rotate", 3: "gemm_gateup", 4: "gemm_down",
                 5: "combine", 6: "gemm_linear", 7: "decode_tiles", 8: "gemm_experts",
                 9: "route_topk", 10: "balance", 11: "balance_sum", 12: "route_backward",
-                13: "lora_a", 14: "lora_b", 15: "lora"}
+                13: "lora_a", 14: "lora_b", 15: "lora", 16: "permute", 17: "unpermute",
+                18: "unpermute_backward", 19: "w4"}
 
 
 def lib():
@@ -536,6 +550,181 @@ def exl3_lora(x, a, b, ids, scale=None, ranks=None, base=None, out_dtype=None, o
                            ids.data_ptr(), _dt(ids), basep, baset, ldb, out.data_ptr(), _dt(out),
                            _matrix(out, rows, N, "out"), ws.data_ptr(), ws.numel(), _stream(),
                            _prof()))
+    return out
+
+
+# ------------------------------------- rows to experts and their products
+def _pos(meta, rows, topk):
+    """Address of the packed positions of rows * topk choices."""
+    if topk < 1 or rows * topk > _MAX:
+        _refuse("%d choices of %d rows are out of range", topk, rows)
+    return _vector(meta["pos_of_pair"], rows * topk, torch.int32, "pos_of_pair")
+
+
+def _packed(t, topk, name):
+    """Rows and features of a packed tensor [rows * topk, features]."""
+    if t.dim() != 2 or topk < 1 or t.shape[0] % topk:
+        _refuse("%s must be [rows * %d, features], got %s", name, topk, list(t.shape))
+    return t.shape[0] // topk, t.shape[1]
+
+
+def exl3_permute(x, meta, topk, out=None):
+    """Rows x [rows, features] to their experts: out [rows * topk, features]
+    holds x[t] at the packed position of every choice of row t. ``meta`` is
+    exl3_route_pack's (its "pos_of_pair" is read). Packed rows past the last
+    kept pair keep what ``out`` held (without ``out``: anything). The gradient
+    with respect to x is exl3_unpermute of the gradient of out, without w."""
+    if x.dim() != 2:
+        _refuse("x must be [rows, features], got %s", list(x.shape))
+    rows, H = x.shape
+    if rows > _MAX or H > _MAX:
+        _too_large(rows, H)
+    pos = _pos(meta, rows, topk)
+    if out is None:
+        out = torch.empty(rows * topk, H, dtype=x.dtype, device=x.device)
+    elif out.dtype is not x.dtype:
+        _refuse("out must have the dtype of x, %s, got %s", x.dtype, out.dtype)
+    _check(lib().exl3_permute(x.data_ptr(), _dt(x), _matrix(x, rows, H, "x"), rows, topk, H, pos,
+                              out.data_ptr(), _matrix(out, rows * topk, H, "out"), _stream(),
+                              _prof()))
+    return out
+
+
+def exl3_unpermute(y, meta, topk, w=None, out_dtype=None, out=None):
+    """Experts' results y [rows * topk, features] back to their rows: out[t] is
+    the sum of y at the packed positions of row t's choices, each times its
+    route weight w [rows, topk] (without w: 1). Dropped choices take no part.
+    The result is not part of autograd's graph; exl3_unpermute_backward gives
+    the gradient."""
+    rows, H = _packed(y, topk, "y")
+    if y.shape[0] > _MAX or H > _MAX:
+        _too_large(y.shape[0], H)
+    pos = _pos(meta, rows, topk)
+    wp, wt = None, 0
+    if w is not None:
+        wp, wt = _pairs(w, rows, topk, "w"), _dt(w)
+    if out is None:
+        out = torch.empty(rows, H, dtype=out_dtype or y.dtype, device=y.device)
+    _check(lib().exl3_unpermute(y.data_ptr(), _dt(y), _matrix(y, rows * topk, H, "y"), rows, topk,
+                                H, pos, wp, wt, out.data_ptr(), _dt(out),
+                                _matrix(out, rows, H, "out"), _stream(), _prof()))
+    return out
+
+
+def exl3_unpermute_backward(dout, meta, topk, y=None, w=None, dy_dtype=None, dw_dtype=None, dy=None,
+                            dw=None):
+    """Gradient of exl3_unpermute: (dy, dw) from dout [rows, features], the
+    gradient of its result. dy [rows * topk, features] has the dtype of ``y``
+    (without y: ``dy_dtype``, by default that of dout); packed rows past the
+    last kept pair keep what ``dy`` held. dw [rows, topk] is what
+    exl3_route_backward takes; it needs ``y`` and is None without it."""
+    if dout.dim() != 2:
+        _refuse("dout must be [rows, features], got %s", list(dout.shape))
+    rows, H = dout.shape
+    if rows > _MAX or H > _MAX:
+        _too_large(rows, H)
+    pos = _pos(meta, rows, topk)
+    yp, ldy, wp, wt, dwp, dwt = None, 0, None, 0, None, 0
+    if w is not None:
+        wp, wt = _pairs(w, rows, topk, "w"), _dt(w)
+    if dy is None:
+        dy = torch.empty(rows * topk, H, device=dout.device,
+                         dtype=y.dtype if y is not None else dy_dtype or dout.dtype)
+    if y is not None:
+        if y.dtype is not dy.dtype:
+            _refuse("dy must have the dtype of y, %s, got %s", y.dtype, dy.dtype)
+        yp, ldy = y.data_ptr(), _matrix(y, rows * topk, H, "y")
+        if dw is None:
+            dw = torch.empty(rows, topk, device=dout.device,
+                             dtype=dw_dtype or (w.dtype if w is not None else torch.float32))
+        dwp, dwt = _pairs(dw, rows, topk, "dw"), _dt(dw)
+    elif dw is not None:
+        _refuse("dw needs y")
+    _check(lib().exl3_unpermute_backward(dout.data_ptr(), _dt(dout),
+                                         _matrix(dout, rows, H, "dout"), rows, topk, H, pos, yp,
+                                         _dt(dy), ldy, wp, wt, dy.data_ptr(),
+                                         _matrix(dy, rows * topk, H, "dy"), dwp, dwt, _stream(),
+                                         _prof()))
+    return dy, dw
+
+
+class DeviceW4:
+    """4-bit weights of a projection, of one expert or several, laid out for
+    exl3_w4_linear on the device that they are on.
+
+    ``q`` uint8 [experts, out, in / 2] (or [out, in / 2]) holds two weights a
+    byte, the even input in the lower four bits; ``scale`` fp16 or bf16
+    [experts, out, in / group] and ``zero`` (uint8 of 0..15, the same shape; None:
+    8) belong to groups of 32, 64 or 128 inputs: weight = scale * (q - zero).
+    Outputs are a multiple of 8. The tensors given are not kept."""
+
+    def __init__(self, q, scale, zero=None):
+        if q.dim() == 2:
+            q, scale = q[None], scale[None]
+            zero = None if zero is None else zero[None]
+        if q.dim() != 3 or q.dtype != torch.uint8 or 0 in q.shape:
+            _refuse("q must be uint8 [experts, out, in / 2], got %s of %s", list(q.shape), q.dtype)
+        E, N, K = q.shape[0], q.shape[1], 2 * q.shape[2]
+        if scale.dim() != 3 or scale.shape[:2] != (E, N) or scale.dtype not in (torch.float16,
+                                                                               torch.bfloat16):
+            _refuse("scale must be fp16 or bf16 [%d, %d, groups], got %s of %s", E, N,
+                    list(scale.shape), scale.dtype)
+        group = next((g for g in (32, 64, 128) if g * scale.shape[2] == K), 0)
+        if not group:
+            _refuse("%d inputs in %d groups: groups must have 32, 64 or 128", K, scale.shape[2])
+        if zero is not None:
+            if zero.shape != scale.shape or zero.dtype != torch.uint8:
+                _refuse("zero must be uint8 %s, got %s of %s", list(scale.shape),
+                        list(zero.shape), zero.dtype)
+            if int(zero.max()) > 15:
+                _refuse("zero has values above 15")
+        self.in_features, self.out_features = K, N
+        self.num_experts, self.group_size = E, group
+        NT, KT, NG = (N + 15) // 16, (K + 127) // 128, 128 // group
+        self.q = torch.empty(E, NT, KT, 64, 16, dtype=torch.uint8, device=q.device)
+        self.scale = torch.empty(E, NT, KT, NG, 16, dtype=scale.dtype, device=q.device)
+        self.zero = None if zero is None else torch.empty_like(self.scale, dtype=torch.uint8)
+
+        def padded(t, cols):
+            return torch.nn.functional.pad(t, (0, cols - t.shape[1], 0, 16 * NT - N))
+
+        for e in range(E):  # one expert at a time: little extra memory
+            v = padded(torch.stack([q[e] & 15, q[e] >> 4], dim=2).reshape(N, K), 128 * KT)
+            v = v.reshape(NT, 16, KT, 4, 4, 8)  # output, tile, word, lane group, input
+            v = v[..., [0, 4, 1, 5]] | v[..., [2, 6, 3, 7]] << 4
+            self.q[e] = v.permute(0, 2, 4, 1, 3, 5).reshape(NT, KT, 64, 16)
+            for to, t in ((self.scale, scale), (self.zero, zero)):
+                if t is not None:
+                    to[e] = padded(t[e], KT * NG).reshape(NT, 16, KT, NG).permute(0, 2, 3, 1)
+        self._c = W4C(K, N, E, group, self.q.data_ptr(), self.scale.data_ptr(),
+                      0 if zero is None else self.zero.data_ptr(), _dt(scale))
+
+    def cstruct(self):
+        return self._c
+
+
+def exl3_w4_linear(x, weight, expert_offset=None, out_dtype=None, out=None):
+    """x [rows, in] times the transposed 4-bit weights (a DeviceW4): packed rows
+    with their experts' weights, where ``expert_offset`` is exl3_route_pack's
+    "expert_offset", or all rows with a single projection's. x is fp16 or bf16;
+    x and ``out`` [rows, out] may be column slices of wider tensors. Without
+    ``out`` the result has ``out_dtype``, by default that of x; rows past the
+    last expert's keep what ``out`` held (without ``out``: anything). The
+    result is not part of autograd's graph."""
+    if x.dim() != 2:
+        _refuse("x must be [rows, in], got %s", list(x.shape))
+    rows, N = x.shape[0], weight.out_features
+    if rows > _MAX:
+        _too_large(rows)
+    if expert_offset is not None:
+        expert_offset = _vector(expert_offset, weight.num_experts + 1, torch.int32,
+                                "expert_offset")
+    if out is None:
+        out = torch.empty(rows, N, dtype=out_dtype or x.dtype, device=x.device)
+    _check(lib().exl3_w4_linear(ctypes.byref(weight.cstruct()), x.data_ptr(), _dt(x),
+                                _matrix(x, rows, weight.in_features, "x"), rows, expert_offset,
+                                out.data_ptr(), _dt(out), _matrix(out, rows, N, "out"), _stream(),
+                                _prof()))
     return out
 
 
