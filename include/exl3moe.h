@@ -520,8 +520,8 @@ int32_t exl3_unpermute_backward(const void *dout, int32_t dout_dtype, int64_t ld
  *   q     [E][NT][KT][64][4] words: word i of lane 16 kg + n of tile (nt, kt)
  *         holds inputs 128 kt + 32 i + 8 kg + 0..7 of output 16 nt + n, those
  *         numbered 0, 2, 4, 6, 1, 3, 5, 7 in bits 0-3, 4-7, .. 28-31
- *   scale [E][NT][KT][128 / G][16] fp16 or bf16: group 128 / G * kt + g of
- *         output 16 nt + n
+ *   scale [E][NT][KT][16][128 / G] fp16 or bf16: of output 16 nt + n, groups
+ *         128 / G * kt + g
  *   zero  the same order, uint8 (its lower 4 bits), or NULL (all 8)
  */
 typedef struct exl3_w4 {

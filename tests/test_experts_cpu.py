@@ -81,7 +81,7 @@ def test_weight_tiles(E, N, K, G, zeros):
     zero = torch.randint(0, 16, (E, N, K // G), generator=g, dtype=torch.uint8) if zeros else None
     W = exl3.DeviceW4(q, scale, zero)
     NT, KT, NG = (N + 15) // 16, (K + 127) // 128, 128 // G
-    assert W.q.shape == (E, NT, KT, 64, 16) and W.scale.shape == (E, NT, KT, NG, 16)
+    assert W.q.shape == (E, NT, KT, 64, 16) and W.scale.shape == (E, NT, KT, 16, NG)
     words = W.q.numpy().view(np.uint32)
     v = np.empty((E, N, K), np.uint8)
     v[:, :, 0::2], v[:, :, 1::2] = q.numpy() & 15, q.numpy() >> 4
@@ -95,10 +95,10 @@ def test_weight_tiles(E, N, K, G, zeros):
                     for n in range(16):
                         at = (e, 16 * nt + n, kt * NG + gi)
                         inside = at[1] < N and at[2] < K // G
-                        assert float(W.scale[e, nt, kt, gi, n]) == (float(scale[at]) if inside
+                        assert float(W.scale[e, nt, kt, n, gi]) == (float(scale[at]) if inside
                                                                     else 0)
                         if zeros:
-                            assert int(W.zero[e, nt, kt, gi, n]) == (int(zero[at]) if inside else 0)
+                            assert int(W.zero[e, nt, kt, n, gi]) == (int(zero[at]) if inside else 0)
     assert (W.zero is None) == (not zeros)
     c = W.cstruct()
     assert (c.in_features, c.out_features, c.num_experts, c.group_size) == (K, N, E, G)

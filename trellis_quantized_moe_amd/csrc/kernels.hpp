@@ -203,7 +203,7 @@ struct MoveParams {
 struct W4Params {
   int K, N, E, group;
   const uint32_t *q;      // [E][ceil(N / 16)][ceil(K / 128)][64][4]
-  const uint16_t *scale;  // [E][ceil(N / 16)][ceil(K / 128)][128 / group][16]
+  const uint16_t *scale;  // [E][ceil(N / 16)][ceil(K / 128)][16][128 / group]
   const uint8_t *zero;    // the same, or null (all 8)
   int scale_bf16;
   const uint16_t *x;  // [rows][K], rows ldx apart

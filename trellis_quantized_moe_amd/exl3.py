@@ -682,7 +682,7 @@ class DeviceW4:
         self.num_experts, self.group_size = E, group
         NT, KT, NG = (N + 15) // 16, (K + 127) // 128, 128 // group
         self.q = torch.empty(E, NT, KT, 64, 16, dtype=torch.uint8, device=q.device)
-        self.scale = torch.empty(E, NT, KT, NG, 16, dtype=scale.dtype, device=q.device)
+        self.scale = torch.empty(E, NT, KT, 16, NG, dtype=scale.dtype, device=q.device)
         self.zero = None if zero is None else torch.empty_like(self.scale, dtype=torch.uint8)
 
         def padded(t, cols):
@@ -695,7 +695,7 @@ class DeviceW4:
             self.q[e] = v.permute(0, 2, 4, 1, 3, 5).reshape(NT, KT, 64, 16)
             for to, t in ((self.scale, scale), (self.zero, zero)):
                 if t is not None:
-                    to[e] = padded(t[e], KT * NG).reshape(NT, 16, KT, NG).permute(0, 2, 3, 1)
+                    to[e] = padded(t[e], KT * NG).reshape(NT, 16, KT, NG).transpose(1, 2)
         self._c = W4C(K, N, E, group, self.q.data_ptr(), self.scale.data_ptr(),
                       0 if zero is None else self.zero.data_ptr(), _dt(scale))
 
