@@ -211,7 +211,7 @@ struct W4Params {
   int64_t ldx;
   int rows;
   const int32_t *offset;  // [E + 1] or null (one expert)
-  int first_tile;         // of row tiles, set by the launcher
+  int64_t first;          // of the launch's workgroups, set by the launcher
   void *out;              // [rows][N], rows ldout apart; dtype codes as RouterParams
   int out_dtype;
   int64_t ldout;

@@ -17,6 +17,7 @@
 // inputs 32 i + 8 kg .. + 7 of output n. In a word, bits 4 p hold input 2 p
 // (p < 4) or 2 (p - 4) + 1, so that one shift and mask gives two neighbours in
 // the two halves of a dword.
+#include <cstdlib>
 #include "common.hpp"
 #include "kernels.hpp"
 
@@ -39,33 +40,67 @@ __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
 }
 
 // Eight weights q - z of a word as the MFMA's operand.
-// fp16: 0x6400 | q is 1024 + q, and 1024 + z is taken off again, exactly.
-// bf16 has no packed subtraction: through fp32, whose upper half is the value.
+// fp16: 0x6400 | q is 1024 + q, 0x6400 | 16 q is 1024 + 16 q: 1024 + z (64 + z
+// after a sixteenth) is taken off again, exactly; nine instructions.
+// bf16: 0x4300 | q is 128 + q. It has no packed subtraction: a dot product with
+// (1, 0) or (0, 1) takes 128 + z off in fp32, whose upper half is the value;
+// nineteen instructions.
+struct Masks {
+  // in registers that the compiler does not fold back into literals: an
+  // and-or takes none
+  uint32_t low, high;
+  // bf16 (1, 0) and (0, 1); as a literal the first becomes an inline constant,
+  // which the dot product does not take as these bits
+  uint32_t first, second;
+  __device__ __forceinline__ Masks() {
+    asm volatile("s_mov_b32 %0, 0x00003f80" : "=s"(first));
+    asm volatile("s_mov_b32 %0, 0x3f800000" : "=s"(second));
+    asm volatile("v_mov_b32 %0, 0x000f000f" : "=v"(low));
+    asm volatile("v_mov_b32 %0, 0x00f000f0" : "=v"(high));
+  }
+};
+// What weights_of needs of a zero.
 template <bool BF16>
-__device__ __forceinline__ u32x4 weights_of(uint32_t w, int z) {
+struct Zero {
+  float f;
+  f16x2 one, sixteenth;
+  __device__ __forceinline__ explicit Zero(int z) {
+    if constexpr (BF16) {
+      f = (float)(-128 - z);
+    } else {
+      const _Float16 a = (_Float16)(float)(-1024 - z), b = (_Float16)(float)(-64 - z);
+      one = (f16x2){a, a};
+      sixteenth = (f16x2){b, b};
+    }
+  }
+};
+template <bool BF16>
+__device__ __forceinline__ u32x4 weights_of(uint32_t w, const Zero<BF16> &z, const Masks &m) {
   u32x4 r;
   if constexpr (BF16) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    const bf16x2 first = __builtin_bit_cast(bf16x2, m.first),
+                 second = __builtin_bit_cast(bf16x2, m.second);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float lo = (float)((int)(w >> (4 * i) & 15u) - z);
-      const float hi = (float)((int)(w >> (4 * i + 16) & 15u) - z);
+      const bf16x2 v = __builtin_bit_cast(bf16x2, (w >> (4 * i) & m.low) | 0x43004300u);
+      const float lo = __builtin_amdgcn_fdot2_f32_bf16(v, first, z.f, false);
+      const float hi = __builtin_amdgcn_fdot2_f32_bf16(v, second, z.f, false);
       r[i] = __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, hi),
                                    __builtin_bit_cast(uint32_t, lo), 0x07060302u);
     }
   } else {
-    const _Float16 off = (_Float16)(float)(1024 + z);
-    const f16x2 o2 = {off, off};
+    const f16x2 sixteen = {(_Float16)0.0625f, (_Float16)0.0625f};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t m = (w >> (4 * i) & 0x000f000fu) | 0x64006400u;
-      r[i] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, m) - o2);
+    for (int i = 0; i < 4; i += 2) {
+      const uint32_t v = w >> (4 * i);
+      const f16x2 a = __builtin_bit_cast(f16x2, (v & m.low) | 0x64006400u);
+      const f16x2 b = __builtin_bit_cast(f16x2, (v & m.high) | 0x64006400u);
+      r[i] = __builtin_bit_cast(uint32_t, a + z.one);
+      r[i + 1] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(b, sixteen, z.sixteenth));
     }
   }
   return r;
-}
-
-__device__ __forceinline__ float scale_of(const W4Params &p, int64_t i) {
-  return p.scale_bf16 ? bf16_bits_to_f32(p.scale[i]) : f16_bits_to_f32(p.scale[i]);
 }
 
 // A sum of only zeros that ended below the smallest subnormal is +0 in every
@@ -76,124 +111,251 @@ __device__ __forceinline__ void store_out(const W4Params &p, int64_t at, float v
   else ((uint16_t *)p.out)[at] = f32_to_out16(v, p.out_dtype == 2);
 }
 
-// Rows of tile `idx` of `tm` rows: tiles count up through the experts, each
-// with ceil(rows / tm) of them. False past the last tile. Offsets are kept
-// within the call's rows.
-__device__ __forceinline__ bool find_tile(const W4Params &p, int tm, int idx, int &expert,
-                                          int &row, int &nrows) {
-  if (!p.offset) {
-    expert = 0;
-    row = idx * tm;
-    nrows = min(tm, p.rows - row);
-    return row < p.rows;
-  }
+// What a workgroup works on: item `item` of the tiles of `tm` rows (counted up
+// through the experts, each with ceil(rows / tm) of them) times `per` blocks of
+// outputs, block within tile. False past the last item. Workgroups are dealt to
+// the 8 XCDs in turn; each XCD gets a run of neighbouring items, whose rows of x
+// and weights its L2 then holds for several of them. Offsets are kept within
+// the call's rows.
+struct Item {
+  int expert, row0, nrows, block;
+};
+__device__ __forceinline__ bool find_item(const W4Params &p, int tm, int per, Item &it) {
   const int lane = threadIdx.x & 63;
-  int base = 0;
-  for (int e0 = 0; e0 < p.E; e0 += 64) {
-    const int e = e0 + lane;
-    int lo = 0, cnt = 0;
-    if (e < p.E) {
-      lo = min(max(p.offset[e], 0), p.rows);
-      cnt = max(min(max(p.offset[e + 1], 0), p.rows) - lo, 0);
+  const int C = (p.E + 63) / 64;  // experts of a lane
+  auto rows_before = [&](int e) { return (uint32_t)min(max(p.offset[e], 0), p.rows); };
+  auto rows_of = [](uint32_t lo, uint32_t hi) { return hi > lo ? hi - lo : 0u; };
+  uint32_t mine = 0, upto = 0, total;
+  if (p.offset) {
+    uint32_t prev = rows_before(min(lane * C, p.E));
+    for (int e = lane * C; e < min(lane * C + C, p.E); ++e) {
+      const uint32_t next = rows_before(e + 1);
+      mine += (rows_of(prev, next) + tm - 1) / tm;
+      prev = next;
     }
-    const int mine = (cnt + tm - 1) / tm;
-    int upto = mine;  // tiles of this window's experts up to this lane's
+    upto = mine;  // tiles of the experts up to this lane's last
 #pragma unroll
     for (int s = 1; s < 64; s <<= 1) {
-      const int v = __shfl_up(upto, s, 64);
+      const uint32_t v = __shfl_up(upto, s, 64);
       upto += lane >= s ? v : 0;
     }
-    const int rel = idx - base;
-    const uint64_t hit = __ballot(rel < upto);
-    if (hit) {
-      const int l = __ffsll((long long)hit) - 1;
-      const int first = __shfl(upto - mine, l, 64);
-      const int lo_l = __shfl(lo, l, 64), cnt_l = __shfl(cnt, l, 64);
-      expert = __builtin_amdgcn_readfirstlane(e0 + l);
-      row = __builtin_amdgcn_readfirstlane(lo_l + (rel - first) * tm);
-      nrows = __builtin_amdgcn_readfirstlane(min(tm, cnt_l - (rel - first) * tm));
+    total = __builtin_amdgcn_readlane(upto, 63);
+  } else {
+    total = (uint32_t)(p.rows + tm - 1) / tm;
+  }
+  const int64_t items = (int64_t)total * per, id = p.first + blockIdx.x;
+  if (id >= items) return false;
+  const int64_t item = (id & 7) * (items >> 3) + min(id & 7, items & 7) + (id >> 3);
+  const uint32_t idx = (uint32_t)(item / per);
+  it.block = (int)(item % per);
+  if (!p.offset) {
+    it.expert = 0;
+    it.row0 = idx * tm;
+    it.nrows = min(tm, p.rows - it.row0);
+    return true;
+  }
+  const int l = max(__ffsll((long long)__ballot(idx < upto)) - 1, 0);
+  uint32_t rel = idx - __builtin_amdgcn_readlane(upto - mine, l);  // among lane l's tiles
+  uint32_t prev = rows_before(min(l * C, p.E));
+  for (int e = l * C; e < p.E; ++e) {
+    // whatever the offsets are, what is returned lies within the call's rows
+    const uint32_t next = rows_before(e + 1), rows = rows_of(prev, next), at = rel * tm;
+    if (at < rows) {
+      it.expert = e;
+      it.row0 = (int)(prev + at);
+      it.nrows = (int)min((uint32_t)tm, rows - at);
       return true;
     }
-    base += __shfl(upto, 63, 64);
+    rel -= (rows + tm - 1) / tm;
+    prev = next;
   }
   return false;
 }
 
-// Few rows: a workgroup has 16 outputs of 16 MT rows, its waves take tiles of
-// 128 inputs in turn and leave each group's t in LDS, from where the
-// workgroup's threads add them in order, MT values each.
-constexpr int kWaves = 4;
+// ---------------------------------------------------------------- few rows
+// A lane's share of a weight tile (16 outputs x 128 inputs): its 32 weights and
+// the scales and zeros of its output's groups.
+template <int G>
+struct Tile {
+  static constexpr int NG = kTileK / G;
+  u32x4 q;
+  uint32_t scale[(NG + 1) / 2], zero;
 
-template <int MT, int G, bool BF16>
-__global__ void __launch_bounds__(64 * kWaves) w4_rows_kernel(W4Params p) {
-  constexpr int NG = kTileK / G;  // groups of a tile
-  constexpr int CH = G / 32;      // MFMAs of a group
-  __shared__ f32x4 ts[2][kWaves * NG][MT][64];
-  __shared__ float ss[2][kWaves * NG][16];
-  int expert, row0, nrows;
+  // tile: index among all weight tiles
+  __device__ __forceinline__ void load(const W4Params &p, int64_t tile, int lane) {
+    q = *(const u32x4 *)(p.q + (tile * 64 + lane) * 4);
+    const int64_t at = (tile * 16 + (lane & 15)) * NG;
+    if constexpr (NG == 1) {
+      scale[0] = p.scale[at];
+      zero = p.zero ? p.zero[at] : 8u;
+    } else if constexpr (NG == 2) {
+      scale[0] = *(const uint32_t *)(p.scale + at);
+      zero = p.zero ? *(const uint16_t *)(p.zero + at) : 0x0808u;
+    } else {
+      typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+      const u32x2 v = *(const u32x2 *)(p.scale + at);
+      scale[0] = v[0];
+      scale[1] = v[1];
+      zero = p.zero ? *(const uint32_t *)(p.zero + at) : 0x08080808u;
+    }
+  }
+  __device__ __forceinline__ int zero_of(int g) const { return (int)(zero >> (8 * g)) & 15; }
+  __device__ __forceinline__ float scale_of(const W4Params &p, int g) const {
+    const uint16_t v = (uint16_t)(scale[g >> 1] >> (16 * (g & 1)));
+    const float sb = bf16_bits_to_f32(v), sh = f16_bits_to_f32(v);
+    return p.scale_bf16 ? sb : sh;
+  }
+  // t of group g, a: x of the tile's 128 inputs
+  template <bool BF16>
+  __device__ __forceinline__ f32x4 group(const u32x4 (&a)[4], int g, const Masks &ms) const {
+    const Zero<BF16> z(zero_of(g));
+    f32x4 t = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int c = 0; c < G / 32; ++c)
+      t = mfma<BF16>(a[g * (G / 32) + c], weights_of(q[g * (G / 32) + c], z, ms), t);
+    return t;
+  }
+};
+
+// The x operand of 128 inputs from input k on, of the row at xr (which points
+// at this lane's 8 kg): pieces past K read the first one again (their groups do
+// not exist).
+__device__ __forceinline__ void load_x(const uint16_t *xr, int k, int K, u32x4 (&a)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) a[i] = *(const u32x4 *)(xr + k + (k + 32 * i < K ? 32 * i : 0));
+}
+
+// Few rows and few tiles: the workgroup's 8 waves share the inputs of 16 outputs
+// of up to 16 rows. A wave takes every eighth tile of a window, all of whose
+// weights are asked for at once, and leaves each group's t in LDS; the
+// workgroup's threads add them in order, one output value each.
+constexpr int kSplitWaves = 8, kSlots = 32;  // groups of a window
+
+template <int G, bool BF16>
+__global__ void __launch_bounds__(64 * kSplitWaves) w4_split_kernel(W4Params p) {
+  constexpr int NG = kTileK / G;
+  constexpr int U = kSlots / (kSplitWaves * NG);  // tiles of a wave in a window
+  __shared__ f32x4 ts[kSlots][64];
+  __shared__ float ss[kSlots][16];
   const int NT = (p.N + 15) / 16, KT = (p.K + kTileK - 1) / kTileK, groups = p.K / G;
-  const int nt = blockIdx.x % NT;
-  if (!find_tile(p, 16 * MT, p.first_tile + blockIdx.x / NT, expert, row0, nrows)) return;
+  Item it;
+  if (!find_item(p, 16, NT, it)) return;
+  const int nt = it.block, row0 = it.row0, nrows = it.nrows;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int n = lane & 15, kg = lane >> 4;
-  const int64_t tile0 = ((int64_t)expert * NT + nt) * KT;
-  const uint16_t *xr[MT];
+  const int64_t tile0 = ((int64_t)it.expert * NT + nt) * KT;
+  // rows past the last one read it again and are not stored
+  const uint16_t *xr = p.x + (int64_t)(row0 + min(n, nrows - 1)) * p.ldx + 8 * kg;
+  Tile<G> w[U];
+  const Masks ms;
+  auto load = [&](int kb) {
 #pragma unroll
-  for (int m = 0; m < MT; ++m)  // rows past the last one read it again and are not stored
-    xr[m] = p.x + (int64_t)(row0 + min(16 * m + n, nrows - 1)) * p.ldx + 8 * kg;
-  float acc[MT] = {};
-  int buf = 0;
-  for (int kb = 0; kb < KT; kb += kWaves, buf ^= 1) {
-    const int kt = kb + wave;
-    if (kt < KT) {
-      const u32x4 q = *(const u32x4 *)(p.q + ((tile0 + kt) * 64 + lane) * 4);
+    for (int u = 0; u < U; ++u)
+      w[u].load(p, tile0 + min(kb + u * kSplitWaves + wave, KT - 1), lane);
+  };
+  load(0);
+  float acc = 0.f;
+  for (int kb = 0; kb < KT; kb += kSplitWaves * U) {
+    u32x4 a[U][4];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      load_x(xr, min(kb + u * kSplitWaves + wave, KT - 1) * kTileK, p.K, a[u]);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
-        if (kt * NG + g >= groups) break;  // K ends inside the tile
-        const int64_t si = ((tile0 + kt) * 16 + n) * NG + g;
-        const int z = p.zero ? p.zero[si] & 15 : 8;
-        f32x4 t[MT];
-#pragma unroll
-        for (int m = 0; m < MT; ++m) t[m] = (f32x4){0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int c = 0; c < CH; ++c) {
-          const int i = g * CH + c;
-          const u32x4 b = weights_of<BF16>(q[i], z);
-#pragma unroll
-          for (int m = 0; m < MT; ++m)
-            t[m] = mfma<BF16>(*(const u32x4 *)(xr[m] + kt * kTileK + 32 * i), b, t[m]);
-        }
-#pragma unroll
-        for (int m = 0; m < MT; ++m) ts[buf][wave * NG + g][m][lane] = t[m];
-        if (kg == 0) ss[buf][wave * NG + g][n] = scale_of(p, si);
+        const int slot = (u * kSplitWaves + wave) * NG + g;
+        ts[slot][lane] = w[u].template group<BF16>(a[u], g, ms);
+        if (kg == 0) ss[slot][n] = w[u].scale_of(p, g);
       }
     }
+    const int next = kb + kSplitWaves * U;
+    if (next < KT) load(next);
     __syncthreads();
-    const int have = min(kWaves * NG, groups - kb * NG);
-    for (int s = 0; s < have; ++s) {
-      const float sc = ss[buf][s][(threadIdx.x >> 2) & 15];
+    const int have = min(kSlots, groups - kb * NG);
+    if (threadIdx.x < 256) {
+      const float *t = (const float *)ts + threadIdx.x;
+      const float *s = (const float *)ss + ((threadIdx.x >> 2) & 15);
+      if (have == kSlots) {
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
-        acc[m] = fmaf(sc, ((const float *)ts[buf][s][m])[threadIdx.x], acc[m]);
+        for (int i = 0; i < kSlots; ++i) acc = fmaf(s[16 * i], t[256 * i], acc);
+      } else {
+        for (int i = 0; i < have; ++i) acc = fmaf(s[16 * i], t[256 * i], acc);
+      }
     }
+    if (next < KT) __syncthreads();
   }
   // thread 4 l + r holds lane l's value r: output l % 16 of row 4 (l / 16) + r
   const int col = 16 * nt + ((threadIdx.x >> 2) & 15);
-  if (col >= p.N) return;
+  const int r = 4 * (threadIdx.x >> 6) + (threadIdx.x & 3);
+  if (threadIdx.x < 256 && col < p.N && r < nrows)
+    store_out(p, (int64_t)(row0 + r) * p.ldout + col, acc);
+}
+
+// Few rows and many tiles: a wave has all inputs of 16 J outputs of up to 16
+// rows and adds the groups in order as it goes; the next tiles' weights are
+// asked for before these are multiplied. Waves do not wait for each other.
+template <int G, bool BF16, int J>
+__global__ void __launch_bounds__(256, J == 1 ? 5 : J == 2 ? (G == 32 ? 3 : 4) : 2) w4_rows_kernel(W4Params p) {
+  constexpr int NG = kTileK / G, D = 2;  // steps asked for ahead
+  const int NT = (p.N + 15) / 16, KT = (p.K + kTileK - 1) / kTileK, groups = p.K / G;
+  Item it;
+  if (!find_item(p, 16, (NT + 4 * J - 1) / (4 * J), it)) return;
+  const int nt = (it.block * 4 + (int)(threadIdx.x >> 6)) * J, row0 = it.row0, nrows = it.nrows;
+  if (nt >= NT) return;
+  const int lane = threadIdx.x & 63;
+  const int n = lane & 15, kg = lane >> 4;
+  int64_t tile[J];
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    const int r = 16 * m + 4 * (threadIdx.x >> 6) + (threadIdx.x & 3);
-    if (r >= nrows) break;
-    store_out(p, (int64_t)(row0 + r) * p.ldout + col, acc[m]);
+  for (int j = 0; j < J; ++j) tile[j] = ((int64_t)it.expert * NT + min(nt + j, NT - 1)) * KT;
+  const uint16_t *xr = p.x + (int64_t)(row0 + min(n, nrows - 1)) * p.ldx + 8 * kg;
+  Tile<G> w[D][J];
+  const Masks ms;
+  u32x4 a[D][4];
+  f32x4 acc[J];
+  auto load = [&](int d, int kt) {
+    kt = min(kt, KT - 1);
+#pragma unroll
+    for (int j = 0; j < J; ++j) w[d][j].load(p, tile[j] + kt, lane);
+    load_x(xr, kt * kTileK, p.K, a[d]);
+  };
+#pragma unroll
+  for (int j = 0; j < J; ++j) acc[j] = (f32x4){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int d = 0; d < D; ++d) load(d, d);
+  for (int kt = 0; kt < KT; kt += D) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          const f32x4 t = w[d][j].template group<BF16>(a[d], g, ms);
+          // 0 past K: adds nothing
+          const bool in = (kt + d) * NG + g < groups;
+          const float sc = w[d][j].scale_of(p, g);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[j][r] = in ? fmaf(sc, t[r], acc[j][r]) : acc[j][r];
+        }
+      }
+      load(d, kt + d + D);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const int col = 16 * (nt + j) + n;
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (col < p.N && 4 * kg + r < nrows)
+        store_out(p, (int64_t)(row0 + 4 * kg + r) * p.ldout + col, acc[j][r]);
   }
 }
 
 // ------------------------------------------------------------- many rows
 // A workgroup of four waves has 128 rows x 256 outputs, a wave all rows of 64
 // outputs, so that each weight is unpacked once in a workgroup. The tile's x
-// (128 x 128 a step, 32 KB) goes from global memory to LDS in the order of the
-// MFMA's operand (a fragment is 1 KB, lane by lane) and is read by all four
-// waves; the next step's copies run while this one is multiplied. A wave keeps
+// (128 x 128 a step, 32 KB) goes from global memory to LDS, where all four waves
+// read it; the next step's copies run while this one is multiplied. A wave keeps
 // 128 sums a lane; t of a group lives for four MFMAs.
 constexpr int kWideM = 128, kWideN = 256;
 constexpr int kNT = kWideN / 64;  // output tiles of a wave
@@ -232,51 +394,55 @@ struct WideLds {
   static_assert(kBytes <= 80 * 1024, "two workgroups per CU");
 };
 
-// What a wave of the wide kernel is given.
-struct WideArgs {
-  int expert, row0, nrows, nt0;  // nt0: first of its output tiles
-};
-
 // A wave's part of a tile of up to 16 MT rows.
 template <int G, bool BF16, int MT>
-__device__ __forceinline__ void wide_tile(const W4Params &p, const WideArgs &w, char *lds) {
+__device__ __forceinline__ void wide_tile(const W4Params &p, const Item &w, char *lds) {
   using L = WideLds<G>;
   constexpr int NG = L::NG, CH = G / 32;
   constexpr int MW = (MT + 3) / 4;  // row tiles that a wave copies
   const int NT = (p.N + 15) / 16, KT = (p.K + kTileK - 1) / kTileK;
   const int lane = threadIdx.x & 63, wave = (int)uniform(threadIdx.x >> 6);
   const int n = lane & 15, kg = lane >> 4;
-  const bool active = w.nt0 < NT;  // a wave without outputs only copies
-  const int nt0 = min(w.nt0, NT - 1), last = NT - 1 - nt0;
+  const int first = w.block * (kWideN / 16) + wave * kNT;  // of the wave's output tiles
+  const bool active = first < NT;  // a wave without outputs only copies
+  const int nt0 = min(first, NT - 1), last = NT - 1 - nt0;
   const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
 
-  uint32_t avoff[MW];
-#pragma unroll
-  for (int m = 0; m < MW; ++m) {  // rows past the last one read it again and are not stored
-    const int r = min((wave * MW + m) * 16 + n, w.nrows - 1);
-    avoff[m] = (uint32_t)((r * p.ldx + 8 * kg) * 2);
-  }
   const char *abase = uniform(p.x + (int64_t)w.row0 * p.ldx);
   const int64_t wtile = ((int64_t)w.expert * NT + nt0) * KT;
   // a tile's scales are 2 NG pieces of 16 bytes, its zeros NG
-  const uint32_t soff = (uint32_t)(min(lane / (2 * NG), last) * KT * 32 * NG + lane % (2 * NG) * 16);
-  const uint32_t zoff = (uint32_t)(min(lane / NG, last) * KT * 16 * NG + lane % NG * 16);
   const char *sbase = uniform(p.scale + wtile * 16 * NG);
   const char *zbase = uniform(p.zero ? p.zero + wtile * 16 * NG : nullptr);
   // copies of step kt into buffer kt % 2; x past K is zeros, so that groups past
   // K add nothing
-  auto copies = [&](int kt) {
+  auto copies = [&](int kt, int lane) {
+    const uint32_t soff =
+        (uint32_t)(min(lane / (2 * NG), last) * KT * 32 * NG + lane % (2 * NG) * 16);
+    const uint32_t zoff = (uint32_t)(min(lane / NG, last) * KT * 16 * NG + lane % NG * 16);
     const int chunks = min(4, (p.K - kt * kTileK) / 32), buf = kt & 1;
     const int at = buf * L::kX + wave * MW * 4096;
     if (MT % 4 == 0 || wave * MW < MT) {
 #pragma unroll
       for (int m = 0; m < MW; ++m)
-        for (int i = 0; i < 4; ++i) {
-          if (i < chunks)
-            copy_to_lds(avoff[m], uniform(abase + (int64_t)kt * (2 * kTileK) + 64 * i),
-                        uniform(lds0 + at + m * 4096 + i * 1024));
-          else
-            *(u32x4 *)(lds + at + m * 4096 + i * 1024 + lane * 16) = (u32x4){0, 0, 0, 0};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          // 8 rows of 128 bytes; a row's eight pieces stand where fragment reads
+          // of 16 rows meet 16 different places. Rows past the last one read it
+          // again and are not stored.
+          const int row = min((wave * MW + m) * 16 + 8 * h + (lane >> 3), w.nrows - 1);
+          const uint32_t piece = (lane & 7) ^ (4 * h + (lane >> 4));
+          const uint32_t voff = __umul24(row, (uint32_t)(2 * p.ldx)) + 16 * piece;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int to = at + m * 4096 + i * 2048 + h * 1024;
+            const char *from = uniform(abase + (int64_t)kt * (2 * kTileK) + 128 * i);
+            if (2 * i + 2 <= chunks) {
+              copy_to_lds(voff, from, uniform(lds0 + to));
+            } else {  // K ends in these 64 inputs or before
+              *(u32x4 *)(lds + to + lane * 16) =
+                  (int)(2 * i + piece / 4) < chunks ? *(gu32x4p)(from + voff) : (u32x4){0, 0, 0, 0};
+            }
+          }
         }
     }
     if (!active) return;
@@ -288,12 +454,12 @@ __device__ __forceinline__ void wide_tile(const W4Params &p, const WideArgs &w, 
                   uniform(lds0 + L::kZeroOff + (buf * 4 + wave) * L::kZeros));
   };
   const char *qbase = uniform(p.q + wtile * 256);
-  const uint32_t lane16 = 16 * lane;
+  const Masks ms;
   u32x4 raw[kNT];
-  auto load_weights = [&](int kt) {  // tile j's: KT steps of 1 KB
+  auto load_weights = [&](int kt, int lane) {  // tile j's: KT steps of 1 KB
 #pragma unroll
     for (int j = 0; j < kNT; ++j)
-      raw[j] = *(const u32x4 *)(qbase + ((int64_t)min(j, last) * KT + kt) * 1024 + lane16);
+      raw[j] = *(gu32x4p)(qbase + ((int64_t)min(j, last) * KT + kt) * 1024 + 16 * lane);
   };
 
   f32x4 acc[MT][kNT];
@@ -301,27 +467,50 @@ __device__ __forceinline__ void wide_tile(const W4Params &p, const WideArgs &w, 
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int j = 0; j < kNT; ++j) acc[m][j] = (f32x4){0.f, 0.f, 0.f, 0.f};
-  copies(0);
-  load_weights(0);
+  copies(0, lane);
+  load_weights(0, lane);
 
   for (int kt = 0; kt < KT; ++kt) {
     // this step's copies have landed, everybody is done with the last step's
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     const int buf = kt & 1;
-    if (kt + 1 < KT) copies(kt + 1);
+    int lane = threadIdx.x & 63;  // addresses are formed from it anew, not kept
+    asm volatile("" : "+v"(lane));
+    const int n = lane & 15;
+    if (kt + 1 < KT) copies(kt + 1, lane);
     if (!active) continue;
     const char *ss = lds + L::kScaleOff + (buf * 4 + wave) * L::kScales;
     const char *zs = lds + L::kZeroOff + (buf * 4 + wave) * L::kZeros;
-    const char *xs = lds + buf * L::kX + lane * 16;
+    const uint32_t xs =
+        buf * L::kX + (n >> 3) * 1024 + (n & 7) * 128 + (((lane >> 4) ^ (n >> 1)) & 7) * 16;
     u32x4 now[kNT];
 #pragma unroll
     for (int j = 0; j < kNT; ++j) now[j] = raw[j];
-    if (kt + 1 < KT) load_weights(kt + 1);
+    if (kt + 1 < KT) load_weights(kt + 1, lane);
+    // fragment f is x of piece f % CH of row tile f / CH % MT of group f / CH / MT;
+    // four are in registers, a fragment's place is filled again once its last
+    // MFMAs are issued. Output tiles go in pairs: while the MFMAs of one run, the
+    // t of the pair before are added. The barriers hold the compiler to this
+    // order: it would load earlier and keep more than there are registers for.
+    constexpr int kFrags = 4 * MT;
+    auto fragment = [&](int f) {
+      const int c = f % CH, m = f / CH % MT, g = f / (CH * MT);
+      const int i = g * CH + c;
+      return *(const u32x4 *)(lds + (i & 1 ? xs ^ 64 : xs) + m * 4096 + (i >> 1) * 2048);
+    };
+    u32x4 a[4];
+#pragma unroll
+    for (int f = 0; f < 4; ++f) a[f] = fragment(f);
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
       float sc[kNT];
       u32x4 b[kNT][CH];
+      f32x4 t[2][2];  // of two pairs of output tiles: one is formed, one added
+      auto add = [&](int m, int h, int v) {  // value v of 8 of pair h of row tile m
+        const int j = 2 * h + v / 4, r = v % 4;
+        acc[m][j][r] = fmaf(sc[j], t[h & 1][v / 4][r], acc[m][j][r]);
+      };
 #pragma unroll
       for (int j = 0; j < kNT; ++j) {
         const int at = (16 * j + n) * NG + g;
@@ -329,30 +518,41 @@ __device__ __forceinline__ void wide_tile(const W4Params &p, const WideArgs &w, 
         const float sb = bf16_bits_to_f32(v), sh = f16_bits_to_f32(v);
         sc[j] = p.scale_bf16 ? sb : sh;
         const int zv = ((const uint8_t *)zs)[at] & 15;
-        const int z = p.zero ? zv : 8;
+        const Zero<BF16> z(p.zero ? zv : 8);
 #pragma unroll
-        for (int c = 0; c < CH; ++c) b[j][c] = weights_of<BF16>(now[j][g * CH + c], z);
+        for (int c = 0; c < CH; ++c) b[j][c] = weights_of(now[j][g * CH + c], z, ms);
       }
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        // keeps later rows' fragments from being loaded (and held) early
-        __builtin_amdgcn_sched_barrier(0);
-        asm volatile("" ::: "memory");
-        u32x4 a[CH];
+      for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int c = 0; c < CH; ++c) a[c] = *(const u32x4 *)(xs + (m * 4 + g * CH + c) * 1024);
-        f32x4 t[kNT];
+        for (int h = 0; h < kNT / 2; ++h) {
 #pragma unroll
-        for (int j = 0; j < kNT; ++j) t[j] = (f32x4){0.f, 0.f, 0.f, 0.f};
+          for (int c = 0; c < CH; ++c) {
+            const int f = (g * MT + m) * CH + c;
 #pragma unroll
-        for (int c = 0; c < CH; ++c)
+            for (int i = 0; i < 2; ++i) {
+              f32x4 &to = t[h & 1][i];
+              const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+              __builtin_amdgcn_sched_barrier(0);
+              to = mfma<BF16>(a[f % 4], b[2 * h + i][c], c == 0 ? zero : to);
+              __builtin_amdgcn_sched_barrier(0);
+              // a part of the sums of the pair before
+              if (m > 0 || h > 0) {
+                const int pm = h > 0 ? m : m - 1, ph = h > 0 ? h - 1 : kNT / 2 - 1;
 #pragma unroll
-          for (int j = 0; j < kNT; ++j) t[j] = mfma<BF16>(a[c], b[j][c], t[j]);
+                for (int v = (2 * c + i) * (4 / CH); v < (2 * c + i + 1) * (4 / CH); ++v)
+                  add(pm, ph, v);
+              }
+            }
+            if (h == kNT / 2 - 1 && f + 4 < kFrags) {
+              __builtin_amdgcn_sched_barrier(0);
+              a[f % 4] = fragment(f + 4);
+            }
+          }
+        }
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int j = 0; j < kNT; ++j)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) acc[m][j][r] = fmaf(sc[j], t[j][r], acc[m][j][r]);
-      }
+      for (int v = 0; v < 8; ++v) add(MT - 1, kNT / 2 - 1, v);
     }
   }
   if (!active) return;
@@ -364,7 +564,7 @@ __device__ __forceinline__ void wide_tile(const W4Params &p, const WideArgs &w, 
       if (row >= w.nrows) continue;
 #pragma unroll
       for (int j = 0; j < kNT; ++j) {
-        const int col = 16 * (w.nt0 + j) + n;
+        const int col = 16 * (first + j) + n;
         if (col < p.N) store_out(p, (int64_t)(w.row0 + row) * p.ldout + col, acc[m][j][r]);
       }
     }
@@ -374,37 +574,27 @@ __device__ __forceinline__ void wide_tile(const W4Params &p, const WideArgs &w, 
 template <int G, bool BF16>
 __global__ void __launch_bounds__(256, 2) w4_wide_kernel(W4Params p) {
   extern __shared__ __attribute__((aligned(1024))) char lds[];
-  const int NB = (p.N + kWideN - 1) / kWideN;
-  WideArgs w;
-  if (!find_tile(p, kWideM, p.first_tile + blockIdx.x / NB, w.expert, w.row0, w.nrows)) return;
-  w.nt0 = (blockIdx.x % NB) * (kWideN / 16) + (int)uniform(threadIdx.x >> 6) * kNT;
+  Item w;
+  if (!find_item(p, kWideM, (p.N + kWideN - 1) / kWideN, w)) return;
   if (w.nrows <= 32) wide_tile<G, BF16, 2>(p, w, lds);
   else if (w.nrows <= 64) wide_tile<G, BF16, 4>(p, w, lds);
   else wide_tile<G, BF16, 8>(p, w, lds);
 }
 
-template <int G>
-void wide_of(const W4Params &p, unsigned blocks, hipStream_t st) {
-  if (p.bf16) w4_wide_kernel<G, true><<<blocks, 256, WideLds<G>::kBytes, st>>>(p);
-  else w4_wide_kernel<G, false><<<blocks, 256, WideLds<G>::kBytes, st>>>(p);
-}
-void wide_kernel(const W4Params &p, unsigned blocks, hipStream_t st) {
-  if (p.group == 32) wide_of<32>(p, blocks, st);
-  else if (p.group == 64) wide_of<64>(p, blocks, st);
-  else wide_of<128>(p, blocks, st);
-}
-
-template <int MT, int G>
-void rows_of(const W4Params &p, unsigned blocks, hipStream_t st) {
-  if (p.bf16) w4_rows_kernel<MT, G, true><<<blocks, 64 * kWaves, 0, st>>>(p);
-  else w4_rows_kernel<MT, G, false><<<blocks, 64 * kWaves, 0, st>>>(p);
-}
-template <int MT>
-void rows_kernel(const W4Params &p, unsigned blocks, hipStream_t st) {
-  if (p.group == 32) rows_of<MT, 32>(p, blocks, st);
-  else if (p.group == 64) rows_of<MT, 64>(p, blocks, st);
-  else rows_of<MT, 128>(p, blocks, st);
-}
+// Calls K<group, bf16, V...>.
+#define EXL3_W4_KERNEL(K, threads, lds, ...)                                                     \
+  do {                                                                                           \
+    if (q.group == 32) {                                                                         \
+      if (q.bf16) K<32, true, ##__VA_ARGS__><<<blocks, threads, lds, st>>>(q);                   \
+      else K<32, false, ##__VA_ARGS__><<<blocks, threads, lds, st>>>(q);                         \
+    } else if (q.group == 64) {                                                                  \
+      if (q.bf16) K<64, true, ##__VA_ARGS__><<<blocks, threads, lds, st>>>(q);                   \
+      else K<64, false, ##__VA_ARGS__><<<blocks, threads, lds, st>>>(q);                         \
+    } else {                                                                                     \
+      if (q.bf16) K<128, true, ##__VA_ARGS__><<<blocks, threads, lds, st>>>(q);                  \
+      else K<128, false, ##__VA_ARGS__><<<blocks, threads, lds, st>>>(q);                        \
+    }                                                                                            \
+  } while (0)
 
 // Most tiles of tm rows that the call's rows can make.
 int64_t most_tiles(const W4Params &p, int tm) {
@@ -417,10 +607,9 @@ int64_t most_tiles(const W4Params &p, int tm) {
 // unless a launch cannot hold them (its threads are counted in 32 bits).
 template <typename F>
 hipError_t over_tiles(W4Params p, int tm, int per, F f) {
-  const int64_t tiles = most_tiles(p, tm), step = (1 << 22) / per;
-  for (int64_t first = 0; first < tiles; first += step) {
-    p.first_tile = (int)first;
-    f(p, (unsigned)((tiles - first < step ? tiles - first : step) * per));
+  const int64_t items = most_tiles(p, tm) * per, step = 1 << 22;
+  for (p.first = 0; p.first < items; p.first += step) {
+    f(p, (unsigned)(items - p.first < step ? items - p.first : step));
     if (hipError_t e = hipGetLastError()) return e;
   }
   return hipSuccess;
@@ -429,12 +618,31 @@ hipError_t over_tiles(W4Params p, int tm, int per, F f) {
 }  // namespace
 
 hipError_t launch_w4(const W4Params &p, hipStream_t st) {
+  const int NT = (p.N + 15) / 16;
   const int64_t each = p.rows / (p.offset ? p.E : 1);  // rows of an expert
-  if (each > 64 && p.ldx < (1 << 23))
-    return over_tiles(p, kWideM, (p.N + kWideN - 1) / kWideN,
-                      [&](const W4Params &q, unsigned blocks) { wide_kernel(q, blocks, st); });
-  return over_tiles(p, 16, (p.N + 15) / 16,
-                    [&](const W4Params &q, unsigned blocks) { rows_kernel<1>(q, blocks, st); });
+  static const int form = getenv("W4_FORM") ? atoi(getenv("W4_FORM")) : 0;
+  if (form == 1 || (!form && each > 64 && p.ldx < (1 << 23)))
+    return over_tiles(p, kWideM, (p.N + kWideN - 1) / kWideN, [&](const W4Params &q, unsigned blocks) {
+      const int lds = q.group == 32 ? WideLds<32>::kBytes
+                      : q.group == 64 ? WideLds<64>::kBytes : WideLds<128>::kBytes;
+      EXL3_W4_KERNEL(w4_wide_kernel, 256, lds);
+    });
+  if (form == 3 || (!form && most_tiles(p, 16) * NT >= 8192))
+    return over_tiles(p, 16, (NT + 7) / 8, [&](const W4Params &q, unsigned blocks) {
+      EXL3_W4_KERNEL(w4_rows_kernel, 256, 0, 2);
+    });
+  if (form == 4)
+    return over_tiles(p, 16, (NT + 3) / 4, [&](const W4Params &q, unsigned blocks) {
+      EXL3_W4_KERNEL(w4_rows_kernel, 256, 0, 1);
+    });
+  if (form == 5)
+    return over_tiles(p, 16, (NT + 15) / 16, [&](const W4Params &q, unsigned blocks) {
+      EXL3_W4_KERNEL(w4_rows_kernel, 256, 0, 4);
+    });
+  return over_tiles(p, 16, NT, [&](const W4Params &q, unsigned blocks) {
+    EXL3_W4_KERNEL(w4_split_kernel, 64 * kSplitWaves, 0);
+  });
 }
+#undef EXL3_W4_KERNEL
 
 }  // namespace exl3
