@@ -42,31 +42,31 @@ __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
 // Eight weights q - z of a word as the MFMA's operand.
 // fp16: 0x6400 | q is 1024 + q, 0x6400 | 16 q is 1024 + 16 q: 1024 + z (64 + z
 // after a sixteenth) is taken off again, exactly; nine instructions.
-// bf16: 0x4300 | q is 128 + q. It has no packed subtraction: a dot product with
-// (1, 0) or (0, 1) takes 128 + z off in fp32, whose upper half is the value;
-// nineteen instructions.
+// bf16 has no packed subtraction: four q - z at a time as signed bytes (128 + q
+// - z borrows from no neighbour), each through fp32, whose upper half is the
+// value; nineteen instructions.
 struct Masks {
   // in registers that the compiler does not fold back into literals: an
   // and-or takes none
   uint32_t low, high;
-  // bf16 (1, 0) and (0, 1); as a literal the first becomes an inline constant,
-  // which the dot product does not take as these bits
-  uint32_t first, second;
-  __device__ __forceinline__ Masks() {
-    asm volatile("s_mov_b32 %0, 0x00003f80" : "=s"(first));
-    asm volatile("s_mov_b32 %0, 0x3f800000" : "=s"(second));
-    asm volatile("v_mov_b32 %0, 0x000f000f" : "=v"(low));
-    asm volatile("v_mov_b32 %0, 0x00f000f0" : "=v"(high));
+  __device__ __forceinline__ explicit Masks(bool bf16) {
+    if (bf16) {
+      asm volatile("v_mov_b32 %0, 0x0f0f0f0f" : "=v"(low));
+      high = 0;
+    } else {
+      asm volatile("v_mov_b32 %0, 0x000f000f" : "=v"(low));
+      asm volatile("v_mov_b32 %0, 0x00f000f0" : "=v"(high));
+    }
   }
 };
 // What weights_of needs of a zero.
 template <bool BF16>
 struct Zero {
-  float f;
+  uint32_t bytes;
   f16x2 one, sixteenth;
   __device__ __forceinline__ explicit Zero(int z) {
     if constexpr (BF16) {
-      f = (float)(-128 - z);
+      bytes = (uint32_t)z * 0x01010101u;
     } else {
       const _Float16 a = (_Float16)(float)(-1024 - z), b = (_Float16)(float)(-64 - z);
       one = (f16x2){a, a};
@@ -78,16 +78,16 @@ template <bool BF16>
 __device__ __forceinline__ u32x4 weights_of(uint32_t w, const Zero<BF16> &z, const Masks &m) {
   u32x4 r;
   if constexpr (BF16) {
-    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-    const bf16x2 first = __builtin_bit_cast(bf16x2, m.first),
-                 second = __builtin_bit_cast(bf16x2, m.second);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const bf16x2 v = __builtin_bit_cast(bf16x2, (w >> (4 * i) & m.low) | 0x43004300u);
-      const float lo = __builtin_amdgcn_fdot2_f32_bf16(v, first, z.f, false);
-      const float hi = __builtin_amdgcn_fdot2_f32_bf16(v, second, z.f, false);
-      r[i] = __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, hi),
-                                   __builtin_bit_cast(uint32_t, lo), 0x07060302u);
+    for (int h = 0; h < 2; ++h) {  // bytes 0, 1, 2, 3 hold weights 2 h + 0, 4, 1, 5
+      const uint32_t v =
+          (((w >> (4 * h) & m.low) | 0x80808080u) - z.bytes) ^ 0x80808080u;
+      uint32_t f[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        f[i] = __builtin_bit_cast(uint32_t, (float)(int8_t)(v >> (8 * i)));
+      r[h] = __builtin_amdgcn_perm(f[2], f[0], 0x07060302u);
+      r[h + 2] = __builtin_amdgcn_perm(f[3], f[1], 0x07060302u);
     }
   } else {
     const f16x2 sixteen = {(_Float16)0.0625f, (_Float16)0.0625f};
@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(64 * kSplitWaves) w4_split_kernel(W4Params p) 
   // rows past the last one read it again and are not stored
   const uint16_t *xr = p.x + (int64_t)(row0 + min(n, nrows - 1)) * p.ldx + 8 * kg;
   Tile<G> w[U];
-  const Masks ms;
+  const Masks ms(BF16);
   auto load = [&](int kb) {
 #pragma unroll
     for (int u = 0; u < U; ++u)
@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(256, J == 1 ? 5 : J == 2 ? (G == 32 ? 3 : 4) :
   for (int j = 0; j < J; ++j) tile[j] = ((int64_t)it.expert * NT + min(nt + j, NT - 1)) * KT;
   const uint16_t *xr = p.x + (int64_t)(row0 + min(n, nrows - 1)) * p.ldx + 8 * kg;
   Tile<G> w[D][J];
-  const Masks ms;
+  const Masks ms(BF16);
   u32x4 a[D][4];
   f32x4 acc[J];
   auto load = [&](int d, int kt) {
@@ -454,7 +454,7 @@ __device__ __forceinline__ void wide_tile(const W4Params &p, const Item &w, char
                   uniform(lds0 + L::kZeroOff + (buf * 4 + wave) * L::kZeros));
   };
   const char *qbase = uniform(p.q + wtile * 256);
-  const Masks ms;
+  const Masks ms(BF16);
   u32x4 raw[kNT];
   auto load_weights = [&](int kt, int lane) {  // tile j's: KT steps of 1 KB
 #pragma unroll
