@@ -17,7 +17,6 @@
 // inputs 32 i + 8 kg .. + 7 of output n. In a word, bits 4 p hold input 2 p
 // (p < 4) or 2 (p - 4) + 1, so that one shift and mask gives two neighbours in
 // the two halves of a dword.
-#include <cstdlib>
 #include "common.hpp"
 #include "kernels.hpp"
 
@@ -292,65 +291,6 @@ __global__ void __launch_bounds__(64 * kSplitWaves) w4_split_kernel(W4Params p) 
     store_out(p, (int64_t)(row0 + r) * p.ldout + col, acc);
 }
 
-// Few rows and many tiles: a wave has all inputs of 16 J outputs of up to 16
-// rows and adds the groups in order as it goes; the next tiles' weights are
-// asked for before these are multiplied. Waves do not wait for each other.
-template <int G, bool BF16, int J>
-__global__ void __launch_bounds__(256, J == 1 ? 5 : J == 2 ? (G == 32 ? 3 : 4) : 2) w4_rows_kernel(W4Params p) {
-  constexpr int NG = kTileK / G, D = 2;  // steps asked for ahead
-  const int NT = (p.N + 15) / 16, KT = (p.K + kTileK - 1) / kTileK, groups = p.K / G;
-  Item it;
-  if (!find_item(p, 16, (NT + 4 * J - 1) / (4 * J), it)) return;
-  const int nt = (it.block * 4 + (int)(threadIdx.x >> 6)) * J, row0 = it.row0, nrows = it.nrows;
-  if (nt >= NT) return;
-  const int lane = threadIdx.x & 63;
-  const int n = lane & 15, kg = lane >> 4;
-  int64_t tile[J];
-#pragma unroll
-  for (int j = 0; j < J; ++j) tile[j] = ((int64_t)it.expert * NT + min(nt + j, NT - 1)) * KT;
-  const uint16_t *xr = p.x + (int64_t)(row0 + min(n, nrows - 1)) * p.ldx + 8 * kg;
-  Tile<G> w[D][J];
-  const Masks ms(BF16);
-  u32x4 a[D][4];
-  f32x4 acc[J];
-  auto load = [&](int d, int kt) {
-    kt = min(kt, KT - 1);
-#pragma unroll
-    for (int j = 0; j < J; ++j) w[d][j].load(p, tile[j] + kt, lane);
-    load_x(xr, kt * kTileK, p.K, a[d]);
-  };
-#pragma unroll
-  for (int j = 0; j < J; ++j) acc[j] = (f32x4){0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int d = 0; d < D; ++d) load(d, d);
-  for (int kt = 0; kt < KT; kt += D) {
-#pragma unroll
-    for (int d = 0; d < D; ++d) {
-#pragma unroll
-      for (int j = 0; j < J; ++j) {
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          const f32x4 t = w[d][j].template group<BF16>(a[d], g, ms);
-          // 0 past K: adds nothing
-          const bool in = (kt + d) * NG + g < groups;
-          const float sc = w[d][j].scale_of(p, g);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) acc[j][r] = in ? fmaf(sc, t[r], acc[j][r]) : acc[j][r];
-        }
-      }
-      load(d, kt + d + D);
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < J; ++j) {
-    const int col = 16 * (nt + j) + n;
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-      if (col < p.N && 4 * kg + r < nrows)
-        store_out(p, (int64_t)(row0 + 4 * kg + r) * p.ldout + col, acc[j][r]);
-  }
-}
-
 // ------------------------------------------------------------- many rows
 // A workgroup of four waves has 128 rows x 256 outputs, a wave all rows of 64
 // outputs, so that each weight is unpacked once in a workgroup. The tile's x
@@ -581,6 +521,152 @@ __global__ void __launch_bounds__(256, 2) w4_wide_kernel(W4Params p) {
   else wide_tile<G, BF16, 8>(p, w, lds);
 }
 
+// ----------------------------------------------------------- in between
+// Tiles of 16 MT rows x 64 J outputs, four waves of 16 J outputs: enough tiles
+// for the whole card where those of the wide kernel are too few, and less left
+// empty by experts of a few rows. With one or two workgroups to a CU nothing
+// hides a load but distance, so everything (x, weights, scales, zeros) goes
+// through LDS in a ring of S steps, S - 1 of them under way. All copies of a
+// step are counted: the wait leaves the later steps' in flight.
+template <int G, int MT, int J, int S, int W>
+struct MidLds {
+  static constexpr int NG = kTileK / G;
+  static constexpr int kX = MT * 4096, kQ = J * 1024, kScales = 16 * J * NG * 2,
+                       kZeros = 16 * J * NG;  // x of the workgroup, the others of a wave
+  static constexpr int kQOff = kX, kScaleOff = kQOff + W * kQ, kZeroOff = kScaleOff + W * kScales,
+                       kStep = kZeroOff + W * kZeros;
+  static constexpr int kBytes = S * kStep;
+};
+
+template <int G, bool BF16, int MT, int J, int S, int W>
+__global__ void __launch_bounds__(64 * W, 2) w4_mid_kernel(W4Params p) {
+  using L = MidLds<G, MT, J, S, W>;
+  constexpr int NG = L::NG, CH = G / 32;
+  constexpr int XB = (4 * MT + W - 1) / W;   // blocks of x (1 KB) that a wave copies
+  constexpr int kCopies = XB + J + 2;  // of a wave and step
+  static_assert((S - 2) * kCopies < 64, "vmcnt range");
+  extern __shared__ __attribute__((aligned(1024))) char lds[];
+  const int NT = (p.N + 15) / 16, KT = (p.K + kTileK - 1) / kTileK, groups = p.K / G;
+  Item it;
+  if (!find_item(p, 16 * MT, (NT + W * J - 1) / (W * J), it)) return;
+  const int lane = threadIdx.x & 63, wave = (int)uniform(threadIdx.x >> 6);
+  const int n = lane & 15, kg = lane >> 4;
+  // waves past the last output work on the last ones and do not store
+  const int first = (it.block * W + wave) * J, nt0 = min(first, NT - 1), last = NT - 1 - nt0;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
+  const int64_t wtile = ((int64_t)uniform(it.expert) * NT + nt0) * KT;
+  const char *abase = uniform(p.x + (int64_t)it.row0 * p.ldx);
+  const char *qbase = uniform(p.q + wtile * 256);
+  const char *sbase = uniform(p.scale + wtile * 16 * NG);
+  const char *zbase = p.zero ? uniform(p.zero + wtile * 16 * NG) : sbase;  // not used then
+  const uint32_t soff =
+      (uint32_t)(min(lane / (2 * NG), last) * KT * 32 * NG + lane % (2 * NG) * 16);
+  const uint32_t zoff = (uint32_t)(min(lane / NG, last) * KT * 16 * NG + lane % NG * 16);
+  uint32_t avoff[XB], piece[XB];
+#pragma unroll
+  for (int b = 0; b < XB; ++b) {  // see the wide kernel: block b of this wave, 8 rows x 128 bytes
+    const int id = (wave * XB + b) % (4 * MT), m = id >> 2, h = id & 1;
+    const int row = min(m * 16 + 8 * h + (lane >> 3), it.nrows - 1);
+    piece[b] = (lane & 7) ^ (4 * h + (lane >> 4));
+    avoff[b] = __umul24(row, (uint32_t)(2 * p.ldx));
+  }
+  auto copies = [&](int kt, int slot) {
+    kt = min(kt, KT - 1);  // past the end: copied and not used, to keep the count
+    const int chunks = (p.K - kt * kTileK) / 32;
+    const uint32_t to = lds0 + slot * L::kStep;
+#pragma unroll
+    for (int b = 0; b < XB; ++b) {
+      const int id = (wave * XB + b) % (4 * MT), i = id >> 1 & 1;
+      // pieces past K read the row's first one again; their groups are not used
+      const uint32_t at = (int)(8 * i + piece[b]) < 4 * chunks ? 128 * i + 16 * piece[b] : 0;
+      copy_to_lds(avoff[b] + at, uniform(abase + (int64_t)kt * (2 * kTileK)),
+                  uniform(to + (id >> 2) * 4096 + i * 2048 + (id & 1) * 1024));
+    }
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+      copy_to_lds(16 * lane, uniform(qbase + ((int64_t)min(j, last) * KT + kt) * 1024),
+                  uniform(to + L::kQOff + wave * L::kQ + j * 1024));
+    if (lane < 2 * NG * J)
+      copy_to_lds(soff, uniform(sbase + (int64_t)kt * 32 * NG),
+                  uniform(to + L::kScaleOff + wave * L::kScales));
+    if (lane < NG * J)
+      copy_to_lds(zoff, uniform(zbase + (int64_t)kt * 16 * NG),
+                  uniform(to + L::kZeroOff + wave * L::kZeros));
+  };
+  const Masks ms(BF16);
+  f32x4 acc[MT][J];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int j = 0; j < J; ++j) acc[m][j] = (f32x4){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int s = 0; s < S - 1; ++s) copies(s, s);
+  const uint32_t xat = (n >> 3) * 1024 + (n & 7) * 128 + ((kg ^ (n >> 1)) & 7) * 16;
+  int slot = 0;
+  for (int kt = 0; kt < KT; ++kt) {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"((S - 2) * kCopies) : "memory");
+    __syncthreads();  // this step is there, everybody is done with the one before
+    copies(kt + S - 1, slot == 0 ? S - 1 : slot - 1);
+    const char *step = lds + slot * L::kStep;
+    slot = slot == S - 1 ? 0 : slot + 1;
+    const char *ss = step + L::kScaleOff + wave * L::kScales;
+    const char *zs = step + L::kZeroOff + wave * L::kZeros;
+    u32x4 q[J];
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+      q[j] = *(const u32x4 *)(step + L::kQOff + wave * L::kQ + j * 1024 + 16 * lane);
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      if (NG > 1 && kt * NG + g >= groups) break;
+      float sc[J];
+      u32x4 b[J][CH];
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        const int at = (16 * j + n) * NG + g;
+        const uint16_t v = ((const uint16_t *)ss)[at];
+        const float sb = bf16_bits_to_f32(v), sh = f16_bits_to_f32(v);
+        sc[j] = p.scale_bf16 ? sb : sh;
+        const int zv = ((const uint8_t *)zs)[at] & 15;
+        const Zero<BF16> z(p.zero ? zv : 8);
+#pragma unroll
+        for (int c = 0; c < CH; ++c) b[j][c] = weights_of(q[j][g * CH + c], z, ms);
+      }
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        f32x4 t[J];
+#pragma unroll
+        for (int j = 0; j < J; ++j) t[j] = (f32x4){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+          const int i = g * CH + c;
+          const u32x4 a = *(const u32x4 *)(step + (i & 1 ? xat ^ 64 : xat) + m * 4096 +
+                                           (i >> 1) * 2048);
+#pragma unroll
+          for (int j = 0; j < J; ++j) t[j] = mfma<BF16>(a, b[j][c], t[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[m][j][r] = fmaf(sc[j], t[j][r], acc[m][j][r]);
+      }
+    }
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no copy may land after the end
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = 16 * m + 4 * kg + r;
+      if (row >= it.nrows) continue;
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        const int col = 16 * (first + j) + n;
+        if (col < p.N) store_out(p, (int64_t)(it.row0 + row) * p.ldout + col, acc[m][j][r]);
+      }
+    }
+  }
+}
+
 // Calls K<group, bf16, V...>.
 #define EXL3_W4_KERNEL(K, threads, lds, ...)                                                     \
   do {                                                                                           \
@@ -615,31 +701,51 @@ hipError_t over_tiles(W4Params p, int tm, int per, F f) {
   return hipSuccess;
 }
 
+template <int MT, int J, int S, int W>
+hipError_t mid(const W4Params &p, hipStream_t st) {
+  return over_tiles(p, 16 * MT, (p.N + 16 * W * J - 1) / (16 * W * J),
+                    [&](const W4Params &q, unsigned blocks) {
+                      const int lds = q.group == 32   ? MidLds<32, MT, J, S, W>::kBytes
+                                      : q.group == 64 ? MidLds<64, MT, J, S, W>::kBytes
+                                                      : MidLds<128, MT, J, S, W>::kBytes;
+                      EXL3_W4_KERNEL(w4_mid_kernel, 64 * W, lds, MT, J, S, W);
+                    });
+}
+
 }  // namespace
 
+// The form is chosen by how many rows an expert has (its tile should not stay
+// half empty) and how many tiles there are for 256 CUs. us of the forms on either
+// side of a border, fp16, groups of 128:
+//   4096 -> 4096, one projection:      rows 2048: wide 98, <4, 2, 2, 8> 81; 4096: 140, 162
+//     rows 1024: <4, 2, 2, 8> 51, <2, 2, 3, 4> 62; rows 512: 48, 36; <2, 1, 3, 4> 36
+//     rows 256: <2, 2, 3, 4> 28, <2, 1, 3, 4> 23; rows 64: <2, 1, 3, 4> 19, <1, 1, 3, 4> 16
+//     rows 64: <1, 1, 3, 4> 16, split 22; rows 16: 15, 8
+//   128 experts, top-8, 4096 -> 1536:  2048 rows: wide 314, <4, 2, 2, 8> 324; 1024: 224, 217
+//     rows 512: <4, 2, 2, 8> 138, <2, 2, 3, 4> 153; rows 128: 95, <1, 2, 3, 4> 79
 hipError_t launch_w4(const W4Params &p, hipStream_t st) {
-  const int NT = (p.N + 15) / 16;
-  const int64_t each = p.rows / (p.offset ? p.E : 1);  // rows of an expert
-  static const int form = getenv("W4_FORM") ? atoi(getenv("W4_FORM")) : 0;
-  if (form == 1 || (!form && each > 64 && p.ldx < (1 << 23)))
-    return over_tiles(p, kWideM, (p.N + kWideN - 1) / kWideN, [&](const W4Params &q, unsigned blocks) {
-      const int lds = q.group == 32 ? WideLds<32>::kBytes
-                      : q.group == 64 ? WideLds<64>::kBytes : WideLds<128>::kBytes;
-      EXL3_W4_KERNEL(w4_wide_kernel, 256, lds);
-    });
-  if (form == 3 || (!form && most_tiles(p, 16) * NT >= 8192))
-    return over_tiles(p, 16, (NT + 7) / 8, [&](const W4Params &q, unsigned blocks) {
-      EXL3_W4_KERNEL(w4_rows_kernel, 256, 0, 2);
-    });
-  if (form == 4)
-    return over_tiles(p, 16, (NT + 3) / 4, [&](const W4Params &q, unsigned blocks) {
-      EXL3_W4_KERNEL(w4_rows_kernel, 256, 0, 1);
-    });
-  if (form == 5)
-    return over_tiles(p, 16, (NT + 15) / 16, [&](const W4Params &q, unsigned blocks) {
-      EXL3_W4_KERNEL(w4_rows_kernel, 256, 0, 4);
-    });
-  return over_tiles(p, 16, NT, [&](const W4Params &q, unsigned blocks) {
+  // what the rows make when they spread evenly over the experts
+  const int64_t experts = p.offset ? (p.E < p.rows ? p.E : p.rows) : 1;
+  const int64_t each = (p.rows + experts - 1) / experts;
+  auto tiles = [&](int tm, int tn) {
+    return experts * ((each + tm - 1) / tm) * ((p.N + tn - 1) / tn);
+  };
+  if (p.ldx < (1 << 23)) {  // a tile's rows of x within 32 bits
+    if (each >= 96 && tiles(128, 256) >= 384)
+      return over_tiles(p, kWideM, (p.N + kWideN - 1) / kWideN,
+                        [&](const W4Params &q, unsigned blocks) {
+                          const int lds = q.group == 32   ? WideLds<32>::kBytes
+                                          : q.group == 64 ? WideLds<64>::kBytes
+                                                          : WideLds<128>::kBytes;
+                          EXL3_W4_KERNEL(w4_wide_kernel, 256, lds);
+                        });
+    if (each >= 24 && tiles(64, 256) >= 256) return mid<4, 2, 2, 8>(p, st);
+    if (each >= 12 && tiles(32, 128) >= 512) return mid<2, 2, 3, 4>(p, st);
+    if (each >= 12 && tiles(32, 64) >= 256) return mid<2, 1, 3, 4>(p, st);
+    if (tiles(16, 128) >= 512) return mid<1, 2, 3, 4>(p, st);
+    if (tiles(16, 64) >= 256) return mid<1, 1, 3, 4>(p, st);
+  }
+  return over_tiles(p, 16, (p.N + 15) / 16, [&](const W4Params &q, unsigned blocks) {
     EXL3_W4_KERNEL(w4_split_kernel, 64 * kSplitWaves, 0);
   });
 }
