@@ -312,6 +312,21 @@ __device__ __forceinline__ void copy_to_lds(uint32_t voff, const void *base, uin
       : "v"(voff), "s"(base), "s"(lds)
       : "memory");
 }
+// The same for the first `lanes` lanes, without a branch.
+__device__ __forceinline__ void copy_to_lds(uint32_t voff, const void *base, uint32_t lds,
+                                            int lanes) {
+  uint64_t saved;
+  asm volatile(
+      "s_mov_b64 %0, exec\n\t"
+      "s_and_b64 exec, exec, %4\n\t"
+      "s_mov_b32 m0, %3\n\t"
+      "s_nop 1\n\t"
+      "global_load_lds_dwordx4 %1, %2\n\t"
+      "s_mov_b64 exec, %0"
+      : "=&s"(saved)
+      : "v"(voff), "s"(base), "s"(lds), "s"(lanes == 64 ? ~0ull : (1ull << lanes) - 1)
+      : "memory", "scc");
+}
 __device__ __forceinline__ uint32_t uniform(uint32_t v) {
   return (uint32_t)__builtin_amdgcn_readfirstlane((int)v);
 }
@@ -352,15 +367,14 @@ __device__ __forceinline__ void wide_tile(const W4Params &p, const Item &w, char
   const int64_t wtile = ((int64_t)w.expert * NT + nt0) * KT;
   // a tile's scales are 2 NG pieces of 16 bytes, its zeros NG
   const char *sbase = uniform(p.scale + wtile * 16 * NG);
-  const char *zbase = uniform(p.zero ? p.zero + wtile * 16 * NG : nullptr);
-  // copies of step kt into buffer kt % 2; x past K is zeros, so that groups past
-  // K add nothing
+  const char *zbase = p.zero ? uniform(p.zero + wtile * 16 * NG) : sbase;  // not used then
+  // copies of step kt into buffer kt % 2
   auto copies = [&](int kt, int lane) {
     const uint32_t soff =
         (uint32_t)(min(lane / (2 * NG), last) * KT * 32 * NG + lane % (2 * NG) * 16);
     const uint32_t zoff = (uint32_t)(min(lane / NG, last) * KT * 16 * NG + lane % NG * 16);
-    const int chunks = min(4, (p.K - kt * kTileK) / 32), buf = kt & 1;
-    const int at = buf * L::kX + wave * MW * 4096;
+    const int chunks = (p.K - kt * kTileK) / 32, buf = kt & 1;
+    const uint32_t at = lds0 + buf * L::kX + wave * MW * 4096;
     if (MT % 4 == 0 || wave * MW < MT) {
 #pragma unroll
       for (int m = 0; m < MW; ++m)
@@ -368,30 +382,36 @@ __device__ __forceinline__ void wide_tile(const W4Params &p, const Item &w, char
         for (int h = 0; h < 2; ++h) {
           // 8 rows of 128 bytes; a row's eight pieces stand where fragment reads
           // of 16 rows meet 16 different places. Rows past the last one read it
-          // again and are not stored.
+          // again and are not stored, pieces past K the row's first of the step.
           const int row = min((wave * MW + m) * 16 + 8 * h + (lane >> 3), w.nrows - 1);
           const uint32_t piece = (lane & 7) ^ (4 * h + (lane >> 4));
           const uint32_t voff = __umul24(row, (uint32_t)(2 * p.ldx)) + 16 * piece;
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const int to = at + m * 4096 + i * 2048 + h * 1024;
-            const char *from = uniform(abase + (int64_t)kt * (2 * kTileK) + 128 * i);
-            if (2 * i + 2 <= chunks) {
-              copy_to_lds(voff, from, uniform(lds0 + to));
-            } else {  // K ends in these 64 inputs or before
-              *(u32x4 *)(lds + to + lane * 16) =
-                  (int)(2 * i + piece / 4) < chunks ? *(gu32x4p)(from + voff) : (u32x4){0, 0, 0, 0};
-            }
+            uint32_t from = voff + 128 * i;
+            if (NG > 1) from = (int)(8 * i + piece) < 4 * chunks ? from : voff - 16 * piece;
+            copy_to_lds(from, uniform(abase + (int64_t)kt * (2 * kTileK)),
+                        uniform(at + m * 4096 + i * 2048 + h * 1024));
           }
         }
     }
     if (!active) return;
-    if (lane < 8 * NG)
-      copy_to_lds(soff, uniform(sbase + (int64_t)kt * 32 * NG),
-                  uniform(lds0 + L::kScaleOff + (buf * 4 + wave) * L::kScales));
-    if (zbase && lane < 4 * NG)
-      copy_to_lds(zoff, uniform(zbase + (int64_t)kt * 16 * NG),
-                  uniform(lds0 + L::kZeroOff + (buf * 4 + wave) * L::kZeros));
+    copy_to_lds(soff, uniform(sbase + (int64_t)kt * 32 * NG),
+                uniform(lds0 + L::kScaleOff + (buf * 4 + wave) * L::kScales), 8 * NG);
+    copy_to_lds(zoff, uniform(zbase + (int64_t)kt * 16 * NG),
+                uniform(lds0 + L::kZeroOff + (buf * 4 + wave) * L::kZeros), 4 * NG);
+  };
+  // Zeros over the pieces of the last step past K: groups past K add nothing.
+  auto clear_past_k = [&](int kt) {
+    const int chunks = (p.K - kt * kTileK) / 32;
+    if (NG == 1 || chunks >= 4) return;
+    for (int u = threadIdx.x; u < MT * 256; u += 256) {  // 16 bytes: row tile, i, row, piece
+      const int r = u >> 3 & 15, i = u >> 7 & 1, piece = (u & 7) ^ (r >> 1);
+      if (8 * i + piece >= 4 * chunks)
+        *(u32x4 *)(lds + (kt & 1) * L::kX + (u >> 8) * 4096 + i * 2048 + r * 128 + (u & 7) * 16) =
+            (u32x4){0, 0, 0, 0};
+    }
+    __syncthreads();
   };
   const char *qbase = uniform(p.q + wtile * 256);
   const Masks ms(BF16);
@@ -414,6 +434,7 @@ __device__ __forceinline__ void wide_tile(const W4Params &p, const Item &w, char
     // this step's copies have landed, everybody is done with the last step's
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
+    if (kt == KT - 1) clear_past_k(kt);
     const int buf = kt & 1;
     int lane = threadIdx.x & 63;  // addresses are formed from it anew, not kept
     asm volatile("" : "+v"(lane));
@@ -586,12 +607,10 @@ __global__ void __launch_bounds__(64 * W, 2) w4_mid_kernel(W4Params p) {
     for (int j = 0; j < J; ++j)
       copy_to_lds(16 * lane, uniform(qbase + ((int64_t)min(j, last) * KT + kt) * 1024),
                   uniform(to + L::kQOff + wave * L::kQ + j * 1024));
-    if (lane < 2 * NG * J)
-      copy_to_lds(soff, uniform(sbase + (int64_t)kt * 32 * NG),
-                  uniform(to + L::kScaleOff + wave * L::kScales));
-    if (lane < NG * J)
-      copy_to_lds(zoff, uniform(zbase + (int64_t)kt * 16 * NG),
-                  uniform(to + L::kZeroOff + wave * L::kZeros));
+    copy_to_lds(soff, uniform(sbase + (int64_t)kt * 32 * NG),
+                uniform(to + L::kScaleOff + wave * L::kScales), 2 * NG * J);
+    copy_to_lds(zoff, uniform(zbase + (int64_t)kt * 16 * NG),
+                uniform(to + L::kZeroOff + wave * L::kZeros), NG * J);
   };
   const Masks ms(BF16);
   f32x4 acc[MT][J];
