@@ -102,8 +102,7 @@ __device__ __forceinline__ u32x4 weights_of(uint32_t w, const Zero<BF16> &z, con
   return r;
 }
 
-// A sum of only zeros that ended below the smallest subnormal is +0 in every
-// form (some add groups of zeros past K).
+// + 0: see store_tile.
 __device__ __forceinline__ void store_out(const W4Params &p, int64_t at, float v) {
   v += 0.f;
   if (p.out_dtype == 3) ((float *)p.out)[at] = v;
@@ -336,6 +335,61 @@ __device__ __forceinline__ const char *uniform(const void *p) {
                                    uniform((uint32_t)b));
 }
 
+// Stores a wave's sums of 16 MT rows x 16 J outputs: through its own piece of LDS, two row tiles at a time, so that a lane stores 16 bytes of a
+// row. Stored as the MFMA leaves them, two or four bytes a lane, the wide tiles
+// of a 4096 -> 4096 prompt took 16 us longer.
+template <int MT, int J>
+struct Epilogue {
+  static constexpr int kRound = MT < 2 ? MT : 2;      // row tiles at a time
+  static constexpr int kRow = 64 * J + 16;  // rows 4 apart start 16 banks apart
+  static constexpr int kBytes = 16 * kRound * kRow;
+};
+template <int MT, int J>
+__device__ __forceinline__ void store_tile(const W4Params &p, const Item &it, int first_tile,
+                                           const f32x4 (&acc)[MT][J], char *lds) {
+  using E = Epilogue<MT, J>;
+  const int lane = threadIdx.x & 63, n = lane & 15, kg = lane >> 4;
+  const int col0 = 16 * first_tile, rows = 16 * E::kRound;
+#pragma unroll
+  for (int m0 = 0; m0 < MT; m0 += E::kRound) {
+    lds_exchange();
+#pragma unroll
+    for (int m = 0; m < E::kRound; ++m)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+          // + 0: a sum of only zeros that ended below the smallest subnormal is
+          // +0 in every form (some add groups of zeros past K)
+          *(float *)(lds + (16 * m + 4 * kg + r) * E::kRow + (16 * j + n) * 4) =
+              acc[m0 + m][j][r] + 0.f;
+    lds_exchange();
+    if (p.out_dtype == 3) {
+#pragma unroll
+      for (int u = lane; u < rows * 4 * J; u += 64) {
+        const int r = u / (4 * J), c = u % (4 * J) * 4, row = 16 * m0 + r;
+        const f32x4 v = *(const f32x4 *)(lds + r * E::kRow + c * 4);
+        if (row < it.nrows && col0 + c < p.N)
+          *(f32x4 *)((float *)p.out + (int64_t)(it.row0 + row) * p.ldout + col0 + c) = v;
+      }
+    } else {
+#pragma unroll
+      for (int u = lane; u < rows * 2 * J; u += 64) {
+        const int r = u / (2 * J), c = u % (2 * J) * 8, row = 16 * m0 + r;
+        const f32x4 v = *(const f32x4 *)(lds + r * E::kRow + c * 4),
+                    w = *(const f32x4 *)(lds + r * E::kRow + c * 4 + 16);
+        u32x4 o;
+        o[0] = f32x2_to_out16(v[0], v[1], p.out_dtype == 2);
+        o[1] = f32x2_to_out16(v[2], v[3], p.out_dtype == 2);
+        o[2] = f32x2_to_out16(w[0], w[1], p.out_dtype == 2);
+        o[3] = f32x2_to_out16(w[2], w[3], p.out_dtype == 2);
+        if (row < it.nrows && col0 + c < p.N)
+          *(u32x4 *)((uint16_t *)p.out + (int64_t)(it.row0 + row) * p.ldout + col0 + c) = o;
+      }
+    }
+  }
+}
+
 // Buffers of a workgroup in LDS: two steps of x, of each wave's scales (its 64
 // outputs' groups) and zeros.
 template <int G>
@@ -516,20 +570,9 @@ __device__ __forceinline__ void wide_tile(const W4Params &p, const Item &w, char
       for (int v = 0; v < 8; ++v) add(MT - 1, kNT / 2 - 1, v);
     }
   }
-  if (!active) return;
-#pragma unroll
-  for (int m = 0; m < MT; ++m) {
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int row = 16 * m + 4 * kg + r;
-      if (row >= w.nrows) continue;
-#pragma unroll
-      for (int j = 0; j < kNT; ++j) {
-        const int col = 16 * (first + j) + n;
-        if (col < p.N) store_out(p, (int64_t)(w.row0 + row) * p.ldout + col, acc[m][j][r]);
-      }
-    }
-  }
+  __syncthreads();  // everybody is done with x
+  static_assert(4 * Epilogue<MT, kNT>::kBytes <= 2 * L::kX, "fits where x was");
+  if (active) store_tile<MT, kNT>(p, w, first, acc, lds + wave * Epilogue<MT, kNT>::kBytes);
 }
 
 template <int G, bool BF16>
@@ -670,20 +713,11 @@ __global__ void __launch_bounds__(64 * W, 2) w4_mid_kernel(W4Params p) {
       }
     }
   }
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no copy may land after the end
-#pragma unroll
-  for (int m = 0; m < MT; ++m) {
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int row = 16 * m + 4 * kg + r;
-      if (row >= it.nrows) continue;
-#pragma unroll
-      for (int j = 0; j < J; ++j) {
-        const int col = 16 * (first + j) + n;
-        if (col < p.N) store_out(p, (int64_t)(it.row0 + row) * p.ldout + col, acc[m][j][r]);
-      }
-    }
-  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no copy may land from here on
+  __syncthreads();
+  using E = Epilogue<MT, J>;
+  static_assert(W * E::kBytes <= L::kBytes, "fits where the ring was");
+  store_tile<MT, J>(p, it, first, acc, lds + wave * E::kBytes);
 }
 
 // Calls K<group, bf16, V...>.
