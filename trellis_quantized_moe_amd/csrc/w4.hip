@@ -65,7 +65,7 @@ struct Zero {
   f16x2 one, sixteenth;
   __device__ __forceinline__ explicit Zero(int z) {
     if constexpr (BF16) {
-      bytes = (uint32_t)z * 0x01010101u;
+      bytes = __builtin_amdgcn_perm(0u, (uint32_t)z, 0u);  // in all four
     } else {
       const _Float16 a = (_Float16)(float)(-1024 - z), b = (_Float16)(float)(-64 - z);
       one = (f16x2){a, a};
@@ -502,7 +502,7 @@ __device__ __forceinline__ void wide_tile(const W4Params &p, const Item &w, char
     u32x4 now[kNT];
 #pragma unroll
     for (int j = 0; j < kNT; ++j) now[j] = raw[j];
-    if (kt + 1 < KT) load_weights(kt + 1, lane);
+    if (NG > 1 && kt + 1 < KT) load_weights(kt + 1, lane);
     // fragment f is x of piece f % CH of row tile f / CH % MT of group f / CH / MT;
     // four are in registers, a fragment's place is filled again once its last
     // MFMAs are issued. Output tiles go in pairs: while the MFMAs of one run, the
@@ -537,6 +537,9 @@ __device__ __forceinline__ void wide_tile(const W4Params &p, const Item &w, char
 #pragma unroll
         for (int c = 0; c < CH; ++c) b[j][c] = weights_of(now[j][g * CH + c], z, ms);
       }
+      if (NG == 1 && kt + 1 < KT) load_weights(kt + 1, lane);  // now that `raw` is free
+      // MFMAs first: the other wave's unpacking fits between them
+      __builtin_amdgcn_s_setprio(1);
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -568,6 +571,7 @@ __device__ __forceinline__ void wide_tile(const W4Params &p, const Item &w, char
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int v = 0; v < 8; ++v) add(MT - 1, kNT / 2 - 1, v);
+      __builtin_amdgcn_s_setprio(0);
     }
   }
   __syncthreads();  // everybody is done with x
