@@ -121,14 +121,20 @@ struct Item {
 __device__ __forceinline__ bool find_item(const W4Params &p, int tm, int per, Item &it) {
   const int lane = threadIdx.x & 63;
   const int C = (p.E + 63) / 64;  // experts of a lane
+  constexpr int kKept = 4;        // whose ends stay in registers
   auto rows_before = [&](int e) { return (uint32_t)min(max(p.offset[e], 0), p.rows); };
-  auto rows_of = [](uint32_t lo, uint32_t hi) { return hi > lo ? hi - lo : 0u; };
+  auto tiles_of = [tm](uint32_t lo, uint32_t hi) { return hi > lo ? (hi - lo + tm - 1) / tm : 0u; };
+  uint32_t ends[kKept + 1];
   uint32_t mine = 0, upto = 0, total;
   if (p.offset) {
-    uint32_t prev = rows_before(min(lane * C, p.E));
-    for (int e = lane * C; e < min(lane * C + C, p.E); ++e) {
-      const uint32_t next = rows_before(e + 1);
-      mine += (rows_of(prev, next) + tm - 1) / tm;
+#pragma unroll
+    for (int i = 0; i <= kKept; ++i) ends[i] = rows_before(min(lane * C + min(i, C), p.E));
+#pragma unroll
+    for (int i = 0; i < kKept; ++i) mine += tiles_of(ends[i], ends[i + 1]);
+    uint32_t prev = ends[kKept];
+    for (int i = kKept; i < C; ++i) {
+      const uint32_t next = rows_before(min(lane * C + i + 1, p.E));
+      mine += tiles_of(prev, next);
       prev = next;
     }
     upto = mine;  // tiles of the experts up to this lane's last
@@ -143,9 +149,17 @@ __device__ __forceinline__ bool find_item(const W4Params &p, int tm, int per, It
   }
   const int64_t items = (int64_t)total * per, id = p.first + blockIdx.x;
   if (id >= items) return false;
-  const int64_t item = (id & 7) * (items >> 3) + min(id & 7, items & 7) + (id >> 3);
-  const uint32_t idx = (uint32_t)(item / per);
-  it.block = (int)(item % per);
+  uint32_t idx;
+  if (items < (1ll << 31)) {  // a division in 32 bits
+    const uint32_t n = (uint32_t)items, i = (uint32_t)id;
+    const uint32_t item = (i & 7) * (n >> 3) + min(i & 7, n & 7) + (i >> 3);
+    idx = item / (uint32_t)per;
+    it.block = (int)(item - idx * per);
+  } else {
+    const int64_t item = (id & 7) * (items >> 3) + min(id & 7, items & 7) + (id >> 3);
+    idx = (uint32_t)(item / per);
+    it.block = (int)(item % per);
+  }
   if (!p.offset) {
     it.expert = 0;
     it.row0 = idx * tm;
@@ -154,17 +168,28 @@ __device__ __forceinline__ bool find_item(const W4Params &p, int tm, int per, It
   }
   const int l = max(__ffsll((long long)__ballot(idx < upto)) - 1, 0);
   uint32_t rel = idx - __builtin_amdgcn_readlane(upto - mine, l);  // among lane l's tiles
-  uint32_t prev = rows_before(min(l * C, p.E));
-  for (int e = l * C; e < p.E; ++e) {
-    // whatever the offsets are, what is returned lies within the call's rows
-    const uint32_t next = rows_before(e + 1), rows = rows_of(prev, next), at = rel * tm;
+  // whatever the offsets are, what is returned lies within the call's rows
+  auto here = [&](int e, uint32_t lo, uint32_t hi) {
+    const uint32_t rows = hi > lo ? hi - lo : 0u, at = rel * tm;
     if (at < rows) {
       it.expert = e;
-      it.row0 = (int)(prev + at);
+      it.row0 = (int)(lo + at);
       it.nrows = (int)min((uint32_t)tm, rows - at);
       return true;
     }
-    rel -= (rows + tm - 1) / tm;
+    rel -= tiles_of(lo, hi);
+    return false;
+  };
+  uint32_t prev = __builtin_amdgcn_readlane(ends[0], l);
+#pragma unroll
+  for (int i = 0; i < kKept; ++i) {
+    const uint32_t next = __builtin_amdgcn_readlane(ends[i + 1], l);
+    if (here(min(l * C + i, p.E - 1), prev, next)) return true;
+    prev = next;
+  }
+  for (int e = l * C + kKept; e < min(l * C + C, p.E); ++e) {
+    const uint32_t next = rows_before(e + 1);
+    if (here(e, prev, next)) return true;
     prev = next;
   }
   return false;
@@ -411,7 +436,6 @@ __device__ __forceinline__ void wide_tile(const W4Params &p, const Item &w, char
   constexpr int MW = (MT + 3) / 4;  // row tiles that a wave copies
   const int NT = (p.N + 15) / 16, KT = (p.K + kTileK - 1) / kTileK;
   const int lane = threadIdx.x & 63, wave = (int)uniform(threadIdx.x >> 6);
-  const int n = lane & 15, kg = lane >> 4;
   const int first = w.block * (kWideN / 16) + wave * kNT;  // of the wave's output tiles
   const bool active = first < NT;  // a wave without outputs only copies
   const int nt0 = min(first, NT - 1), last = NT - 1 - nt0;
