@@ -1174,6 +1174,10 @@ int32_t check_rows(const void *p, int32_t dtype, int64_t ld, int64_t cols) {
   if (!aligned16(p) || ld * (int64_t)float_size(dtype) % 16) return EXL3_E_ALIGN;
   return EXL3_OK;
 }
+// Whether a result of that many values is larger than the L2s (8 x 4 MB).
+int past_l2(int64_t rows, int64_t features, int32_t dtype) {
+  return rows * features * (int64_t)float_size(dtype) > (int64_t)32 << 20;
+}
 
 }  // namespace
 
@@ -1204,6 +1208,7 @@ int32_t exl3_permute(const void *x, int32_t dtype, int64_t ld_x, int32_t rows, i
   p.ldx = ld_x;
   p.out = out;
   p.ldout = ld_out;
+  p.stream = past_l2(p.pairs, features, dtype);
   ProfScope ps(prof, (hipStream_t)stream, EXL3_K_PERMUTE);
   return launch_permute(p, (hipStream_t)stream) == hipSuccess ? EXL3_OK : EXL3_E_LAUNCH;
 }
@@ -1238,6 +1243,7 @@ int32_t exl3_unpermute(const void *y, int32_t y_dtype, int64_t ld_y, int32_t row
   p.out = out;
   p.o_dtype = out_dtype;
   p.ldout = ld_out;
+  p.stream = past_l2(rows, features, out_dtype);
   ProfScope ps(prof, (hipStream_t)stream, EXL3_K_UNPERMUTE);
   return launch_unpermute(p, (hipStream_t)stream) == hipSuccess ? EXL3_OK : EXL3_E_LAUNCH;
 }
@@ -1283,6 +1289,7 @@ int32_t exl3_unpermute_backward(const void *dout, int32_t dout_dtype, int64_t ld
   p.lddout = ld_dout;
   p.dw = dw;
   p.dw_dtype = dw_dtype;
+  p.stream = past_l2(p.pairs, features, y_dtype);
   ProfScope ps(prof, (hipStream_t)stream, EXL3_K_UNPERMUTE_BACKWARD);
   return launch_unpermute_backward(p, (hipStream_t)stream) == hipSuccess ? EXL3_OK
                                                                          : EXL3_E_LAUNCH;

@@ -197,6 +197,7 @@ struct MoveParams {
   int64_t lddout;
   void *dw;  // backward: [rows][topk] or null
   int dw_dtype;
+  int stream;  // out is larger than the L2s
 };
 
 // Products with 4-bit weights (w4.hip).

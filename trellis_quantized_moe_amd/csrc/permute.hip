@@ -43,16 +43,24 @@ __device__ __forceinline__ void unpack(const Eight<DT> &e, float (&f)[8]) {
     }
   }
 }
-template <int DT>
+// Results that the L2s cannot hold go past them (stream): 8 x 4 MB. us of one and
+// the other: 5284 rows x 13 x 2048 carried in bf16 (281 MB) 51 and 57, 4001 rows
+// of 6144 summed from 8 in fp32 146 and 152; at 5 MB no difference.
+template <bool STREAM>
+__device__ __forceinline__ void store16(void *p, u32x4 v) {
+  if constexpr (STREAM) __builtin_nontemporal_store(v, (u32x4 *)p);
+  else *(u32x4 *)p = v;
+}
+template <int DT, bool STREAM>
 __device__ __forceinline__ void store_eight(char *p, const float (&f)[8]) {
   if constexpr (DT == 3) {
-    *(f32x4 *)p = (f32x4){f[0], f[1], f[2], f[3]};
-    *(f32x4 *)(p + 16) = (f32x4){f[4], f[5], f[6], f[7]};
+    store16<STREAM>(p, __builtin_bit_cast(u32x4, (f32x4){f[0], f[1], f[2], f[3]}));
+    store16<STREAM>(p + 16, __builtin_bit_cast(u32x4, (f32x4){f[4], f[5], f[6], f[7]}));
   } else {
     u32x4 v;
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = f32x2_to_out16(f[2 * i], f[2 * i + 1], DT == 2);
-    *(u32x4 *)p = v;
+    store16<STREAM>(p, v);
   }
 }
 __device__ __forceinline__ float load_weight(const void *w, int dtype, int64_t i) {
@@ -67,6 +75,27 @@ __device__ __forceinline__ int64_t row_groups(const MoveParams &p) {
   return ((int64_t)p.rows + blockDim.y - 1) / blockDim.y;
 }
 
+// Choices j0 .. j0 + B - 1 of row t: packed positions (-1: dropped, or past topk)
+// and weights. All loads are asked for before the first is needed.
+template <int B>
+__device__ __forceinline__ void load_choices(const MoveParams &p, int64_t t, int j0, int (&q)[B],
+                                             float (&w)[B]) {
+#pragma unroll
+  for (int i = 0; i < B; ++i) q[i] = p.pos[t * p.topk + min(j0 + i, p.topk - 1)];
+  if (p.w) {
+#pragma unroll
+    for (int i = 0; i < B; ++i)
+      w[i] = load_weight(p.w, p.w_dtype, t * p.topk + min(j0 + i, p.topk - 1));
+  } else {
+#pragma unroll
+    for (int i = 0; i < B; ++i) w[i] = 1.f;
+  }
+#pragma unroll
+  for (int i = 0; i < B; ++i)
+    q[i] = j0 + i < p.topk && (uint32_t)q[i] < (uint32_t)p.pairs ? q[i] : -1;
+}
+
+template <bool STREAM>
 __global__ void __launch_bounds__(kThreads) permute_kernel(MoveParams p) {
   const int units = (int)((int64_t)p.features * p.esize / 16);
   const int u = blockIdx.y * blockDim.x + threadIdx.x;
@@ -74,16 +103,20 @@ __global__ void __launch_bounds__(kThreads) permute_kernel(MoveParams p) {
     const int64_t t = g * blockDim.y + threadIdx.y;
     if (t >= p.rows || u >= units) continue;
     const u32x4 v = *(const u32x4 *)((const char *)p.x + t * p.ldx * p.esize + 16 * (int64_t)u);
-    for (int j = 0; j < p.topk; ++j) {
-      const int q = p.pos[t * p.topk + j];
-      if ((uint32_t)q < (uint32_t)p.pairs)
-        *(u32x4 *)((char *)p.out + q * p.ldout * p.esize + 16 * (int64_t)u) = v;
+    for (int j0 = 0; j0 < p.topk; j0 += kBatch) {
+      int q[kBatch];
+      float w[kBatch];  // none here
+      load_choices(p, t, j0, q, w);
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+        if (q[i] >= 0)
+          store16<STREAM>((char *)p.out + q[i] * p.ldout * p.esize + 16 * (int64_t)u, v);
     }
   }
 }
 
 // DY: type of y, DO: of out. B choices at once.
-template <int DY, int DO, int B>
+template <int DY, int DO, int B, bool STREAM>
 __global__ void __launch_bounds__(kThreads) unpermute_kernel(MoveParams p) {
   constexpr int SY = DY == 3 ? 4 : 2, SO = DO == 3 ? 4 : 2;
   const int u = blockIdx.y * blockDim.x + threadIdx.x;
@@ -93,32 +126,27 @@ __global__ void __launch_bounds__(kThreads) unpermute_kernel(MoveParams p) {
     float acc[8] = {};
     for (int j0 = 0; j0 < p.topk; j0 += B) {
       Eight<DY> raw[B];
-      bool held[B];
+      int q[B];
       float w[B];
+      load_choices(p, t, j0, q, w);
 #pragma unroll
-      for (int i = 0; i < B; ++i) {
-        const int64_t pair = t * p.topk + min(j0 + i, p.topk - 1);
-        const int q = p.pos[pair];
-        held[i] = j0 + i < p.topk && (uint32_t)q < (uint32_t)p.pairs;
-        w[i] = p.w ? load_weight(p.w, p.w_dtype, pair) : 1.f;
-        // a dropped choice reads row 0 and is not added
-        raw[i] = load_eight<DY>((const char *)p.x + ((held[i] ? q : 0) * p.ldx + 8 * u) * SY);
-      }
+      for (int i = 0; i < B; ++i)  // a dropped choice reads row 0 and is not added
+        raw[i] = load_eight<DY>((const char *)p.x + (max(q[i], 0) * p.ldx + 8 * u) * SY);
 #pragma unroll
       for (int i = 0; i < B; ++i) {
         float y[8];
         unpack<DY>(raw[i], y);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) acc[k] = held[i] ? fmaf(w[i], y[k], acc[k]) : acc[k];
+        for (int k = 0; k < 8; ++k) acc[k] = q[i] >= 0 ? fmaf(w[i], y[k], acc[k]) : acc[k];
       }
     }
-    store_eight<DO>((char *)p.out + (t * p.ldout + 8 * u) * SO, acc);
+    store_eight<DO, STREAM>((char *)p.out + (t * p.ldout + 8 * u) * SO, acc);
   }
 }
 
 // DY: type of y and dy, DO: of dout. WITH_DW: y is read and dw written. A
 // block's lanes cover a whole row, so that <dout, y> needs no second launch.
-template <int DY, int DO, bool WITH_DW>
+template <int DY, int DO, bool WITH_DW, bool STREAM>
 __global__ void __launch_bounds__(kThreads) unpermute_backward_kernel(MoveParams p) {
   constexpr int SY = DY == 3 ? 4 : 2, SO = DO == 3 ? 4 : 2;
   __shared__ float part[kThreads / 64][kBatch];
@@ -129,19 +157,9 @@ __global__ void __launch_bounds__(kThreads) unpermute_backward_kernel(MoveParams
     const bool in = t < p.rows;
     for (int j0 = 0; j0 < p.topk; j0 += kBatch) {
       float dot[kBatch] = {};
-      int64_t at[kBatch];  // packed row, -1: none
+      int at[kBatch];
       float w[kBatch];
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        at[i] = -1;
-        w[i] = 0.f;
-        if (in && j0 + i < p.topk) {
-          const int64_t pair = t * p.topk + j0 + i;
-          const int q = p.pos[pair];
-          if ((uint32_t)q < (uint32_t)p.pairs) at[i] = q;
-          w[i] = p.w ? load_weight(p.w, p.w_dtype, pair) : 1.f;
-        }
-      }
+      load_choices(p, in ? t : 0, j0, at, w);
       if (in) {
         for (int u = threadIdx.x; u < units; u += lanes) {
           float d[8];
@@ -159,7 +177,7 @@ __global__ void __launch_bounds__(kThreads) unpermute_backward_kernel(MoveParams
             float o[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) o[k] = w[i] * d[k];
-            store_eight<DY>((char *)p.out + (at[i] * p.ldout + 8 * u) * SY, o);
+            store_eight<DY, STREAM>((char *)p.out + (at[i] * p.ldout + 8 * u) * SY, o);
             if constexpr (WITH_DW) {
               float y[8];
               unpack<DY>(raw[i], y);
@@ -170,10 +188,12 @@ __global__ void __launch_bounds__(kThreads) unpermute_backward_kernel(MoveParams
         }
       }
       if constexpr (WITH_DW) {
-        const int within = min(lanes, 64);
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i)
-          for (int s = within / 2; s; s >>= 1) dot[i] += __shfl_xor(dot[i], s, 64);
+        for (int s = 32; s; s >>= 1)
+          if (s < lanes) {
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) dot[i] += __shfl_xor(dot[i], s, 64);
+          }
         if (lanes > 64) {
           // a row takes all of the block: one value per wave and choice
           __syncthreads();
@@ -203,15 +223,15 @@ __global__ void __launch_bounds__(kThreads) unpermute_backward_kernel(MoveParams
   }
 }
 
-// Lanes of a row of `units` pieces: the power of two that holds them, at most
-// a block, in powers that a block holds a whole number of.
+// Lanes of a row of `units` pieces: the power of two that holds them, at most a
+// block; a row of more than a wave takes the block.
 struct Shape {
   dim3 grid, block;
 };
 Shape shape(const MoveParams &p, int units, bool whole_row) {
   int lanes = 1;
   while (lanes < units && lanes < kThreads) lanes *= 2;
-  if (lanes == kThreads / 2) lanes = kThreads;  // a block's barrier is one row's
+  if (lanes > 64) lanes = kThreads;  // the backward pass's barriers are one row's
   const int per = kThreads / lanes;
   const int64_t groups = ((int64_t)p.rows + per - 1) / per;
   Shape s;
@@ -221,24 +241,35 @@ Shape shape(const MoveParams &p, int units, bool whole_row) {
   return s;
 }
 
+template <int DY, int DO, int B>
+void unpermute_batch(const MoveParams &p, const Shape &s, hipStream_t st) {
+  if (p.stream) unpermute_kernel<DY, DO, B, true><<<s.grid, s.block, 0, st>>>(p);
+  else unpermute_kernel<DY, DO, B, false><<<s.grid, s.block, 0, st>>>(p);
+}
 template <int DY, int DO>
 void unpermute(const MoveParams &p, const Shape &s, hipStream_t st) {
-  if (p.topk == 1) unpermute_kernel<DY, DO, 1><<<s.grid, s.block, 0, st>>>(p);
-  else if (p.topk == 2) unpermute_kernel<DY, DO, 2><<<s.grid, s.block, 0, st>>>(p);
-  else if (p.topk <= 4) unpermute_kernel<DY, DO, 4><<<s.grid, s.block, 0, st>>>(p);
-  else unpermute_kernel<DY, DO, kBatch><<<s.grid, s.block, 0, st>>>(p);
+  if (p.topk == 1) unpermute_batch<DY, DO, 1>(p, s, st);
+  else if (p.topk == 2) unpermute_batch<DY, DO, 2>(p, s, st);
+  else if (p.topk <= 4) unpermute_batch<DY, DO, 4>(p, s, st);
+  else unpermute_batch<DY, DO, kBatch>(p, s, st);
+}
+template <int DY, int DO, bool WITH_DW>
+void backward_of(const MoveParams &p, const Shape &s, hipStream_t st) {
+  if (p.stream) unpermute_backward_kernel<DY, DO, WITH_DW, true><<<s.grid, s.block, 0, st>>>(p);
+  else unpermute_backward_kernel<DY, DO, WITH_DW, false><<<s.grid, s.block, 0, st>>>(p);
 }
 template <int DY, int DO>
 void backward(const MoveParams &p, const Shape &s, hipStream_t st) {
-  if (p.dw) unpermute_backward_kernel<DY, DO, true><<<s.grid, s.block, 0, st>>>(p);
-  else unpermute_backward_kernel<DY, DO, false><<<s.grid, s.block, 0, st>>>(p);
+  if (p.dw) backward_of<DY, DO, true>(p, s, st);
+  else backward_of<DY, DO, false>(p, s, st);
 }
 
 }  // namespace
 
 hipError_t launch_permute(const MoveParams &p, hipStream_t st) {
   const Shape s = shape(p, (int)((int64_t)p.features * p.esize / 16), false);
-  permute_kernel<<<s.grid, s.block, 0, st>>>(p);
+  if (p.stream) permute_kernel<true><<<s.grid, s.block, 0, st>>>(p);
+  else permute_kernel<false><<<s.grid, s.block, 0, st>>>(p);
   return hipGetLastError();
 }
 

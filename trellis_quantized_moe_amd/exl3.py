@@ -685,17 +685,23 @@ class DeviceW4:
         self.scale = torch.empty(E, NT, KT, 16, NG, dtype=scale.dtype, device=q.device)
         self.zero = None if zero is None else torch.empty_like(self.scale, dtype=torch.uint8)
 
-        def padded(t, cols):
-            return torch.nn.functional.pad(t, (0, cols - t.shape[1], 0, 16 * NT - N))
+        def padded(t, cols):  # outputs and columns that the tiles have and t lacks: 0
+            return torch.nn.functional.pad(t, (0, cols - t.shape[2], 0, 16 * NT - N))
 
-        for e in range(E):  # one expert at a time: little extra memory
-            v = padded(torch.stack([q[e] & 15, q[e] >> 4], dim=2).reshape(N, K), 128 * KT)
-            v = v.reshape(NT, 16, KT, 4, 4, 8)  # output, tile, word, lane group, input
-            v = v[..., [0, 4, 1, 5]] | v[..., [2, 6, 3, 7]] << 4
-            self.q[e] = v.permute(0, 2, 4, 1, 3, 5).reshape(NT, KT, 64, 16)
+        step = max(1, (1 << 27) // (N * K))  # experts at a time: little extra memory
+        for e in range(0, E, step):
+            w = q[e:e + step].contiguous().view(torch.int32)  # inputs 0 .. 7 from bit 0 on
+            even, odd = w & 0x0f0f0f0f, (w >> 4) & 0x0f0f0f0f
+            for sh, mask in ((4, 0x00ff00ff), (8, 0x0000ffff)):
+                even, odd = (even | even >> sh) & mask, (odd | odd >> sh) & mask
+            w = padded(even | odd << 16, 16 * KT).reshape(-1, NT, 16, KT, 4, 4)
+            # output, tile, word, lane group -> tile, lane group, output, word
+            w = w.permute(0, 1, 3, 5, 2, 4).contiguous()
+            self.q[e:e + step] = w.view(torch.uint8).reshape(-1, NT, KT, 64, 16)
             for to, t in ((self.scale, scale), (self.zero, zero)):
                 if t is not None:
-                    to[e] = padded(t[e], KT * NG).reshape(NT, 16, KT, NG).transpose(1, 2)
+                    t = padded(t[e:e + step], KT * NG).reshape(-1, NT, 16, KT, NG)
+                    to[e:e + step] = t.transpose(2, 3)
         self._c = W4C(K, N, E, group, self.q.data_ptr(), self.scale.data_ptr(),
                       0 if zero is None else self.zero.data_ptr(), _dt(scale))
 
