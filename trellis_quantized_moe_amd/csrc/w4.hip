@@ -631,7 +631,8 @@ struct MidLds {
 };
 
 template <int G, bool BF16, int MT, int J, int S, int W>
-__global__ void __launch_bounds__(64 * W, 2) w4_mid_kernel(W4Params p) {
+__global__ void __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2, 4)))
+w4_mid_kernel(W4Params p) {
   using L = MidLds<G, MT, J, S, W>;
   constexpr int NG = L::NG, CH = G / 32;
   constexpr int XB = (4 * MT + W - 1) / W;   // blocks of x (1 KB) that a wave copies
