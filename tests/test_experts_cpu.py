@@ -104,6 +104,22 @@ def test_weight_tiles(E, N, K, G, zeros):
     assert (c.in_features, c.out_features, c.num_experts, c.group_size) == (K, N, E, G)
 
 
+def test_weights_that_lie_apart():
+    """Slices at odd addresses, transposed and expanded tensors: the same tiles."""
+    g = torch.Generator().manual_seed(1)
+    q = torch.randint(0, 256, (3, 16, 32), generator=g, dtype=torch.uint8)
+    s = torch.rand(3, 16, 2, generator=g).half().requires_grad_()
+    want = exl3.DeviceW4(q, s)
+    assert not want.scale.requires_grad
+    odd = torch.empty(q.numel() + 3, dtype=torch.uint8)
+    odd[3:] = q.reshape(-1)
+    for other in (odd[3:].view(3, 16, 32), q.transpose(0, 2).contiguous().transpose(0, 2)):
+        assert torch.equal(exl3.DeviceW4(other, s).q, want.q)
+    one = exl3.DeviceW4(q[:1].expand(3, 16, 32), s[:1].expand(3, 16, 2))
+    for e in range(3):
+        assert torch.equal(one.q[e], want.q[0]) and torch.equal(one.scale[e], want.scale[0])
+
+
 # ----------------------------------------------------------------- refusals
 P = 1 << 20  # an address that is no device memory
 FAR = 1 << 32

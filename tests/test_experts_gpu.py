@@ -160,6 +160,39 @@ def test_unpermute_backward(T, k, H, y_dt, w_dt, o_dt, pad):
     assert none is None and _same(only[:kept], got[:kept])
 
 
+@pytest.mark.parametrize("dt,w_dt", [("f16", "f32"), ("bf16", "bf16"), ("f32", None)])
+def test_moves_of_more_than_the_l2s_hold(dt, w_dt):
+    """Large results take other stores: the rows of small calls, byte for byte."""
+    T, k, H = 9000, 3, 2056
+    meta = _meta(T, k, 11, 4)
+    pos = meta["pos_of_pair"].view(T, k)
+    kept = int(meta["expert_offset"][-1])
+    g = torch.Generator(device=DEV).manual_seed(3)
+    x = torch.randn(T, H, generator=g, device=DEV).to(DT[dt])
+    w = None if w_dt is None else torch.rand(T, k, generator=g, device=DEV).to(DT[w_dt])
+    zeros = torch.zeros(T * k, H, dtype=DT[dt], device=DEV)
+    xs = exl3.exl3_permute(x, meta, k, out=zeros.clone())
+    out = exl3.exl3_unpermute(xs, meta, k, w)
+    dy, dw = exl3.exl3_unpermute_backward(x, meta, k, xs, w, dy=zeros.clone())
+    want = zeros.clone()
+    flat = pos.reshape(-1).long()
+    held = flat >= 0
+    want[flat[held]] = x.repeat_interleave(k, 0)[held]
+    assert _same(xs, want) and (xs[kept:] == 0).all() and (dy[kept:] == 0).all()
+    for lo in (0, 4321, T - 20):  # 20 rows, their packed rows moved to the front
+        p = pos[lo:lo + 20].reshape(-1).long()
+        part = torch.full((20 * k,), -1, dtype=torch.int32, device=DEV)
+        part[p >= 0] = torch.arange(int((p >= 0).sum()), dtype=torch.int32, device=DEV)
+        few = {"pos_of_pair": part}
+        rows = p[p >= 0]
+        y = zeros[:20 * k].clone()
+        y[:rows.numel()] = xs[rows]
+        pw = None if w is None else w[lo:lo + 20].contiguous()
+        assert _same(exl3.exl3_unpermute(y, few, k, pw), out[lo:lo + 20])
+        sy, sw = exl3.exl3_unpermute_backward(x[lo:lo + 20], few, k, y, pw)
+        assert _same(sy[:rows.numel()], dy[rows]) and _same(sw, dw[lo:lo + 20])
+
+
 def test_gradients_against_differences():
     """Whole numbers: every value and difference is exact, so the directional
     derivative along each single input equals the gradient's entry."""
@@ -346,6 +379,63 @@ def test_w4_whole_numbers(case):
     assert np.array_equal(_np(out), ref)
 
 
+# Sizes that the kernels' forms are chosen for: tiles of 128 x 256, 64 x 256,
+# 32 x 128, 32 x 64, 16 x 128, 16 x 64 and 16 x 16.
+FORMS = [(5000, 24, 2056), (2700, 64, 1032), (1100, 64, 1032), (700, 32, 520), (330, 64, 1032),
+         (70, 33, 520), (60, 9, 328)]
+
+
+def _spread(rows, E, g):
+    """Offsets of experts of about rows / E rows each, some of them empty."""
+    e = torch.randint(0, E, (rows,), generator=g)
+    e[e == E // 2] = 0
+    return torch.cat([torch.zeros(1, dtype=torch.int64),
+                      torch.bincount(e, minlength=E).cumsum(0)]).to(torch.int32)
+
+
+@pytest.mark.parametrize("rows,E,N", FORMS)
+@pytest.mark.parametrize("K,G,zeros,x_dt,o_dt", [
+    (384, 128, False, "f16", "f16"), (256, 128, True, "bf16", "f32"),
+    (320, 64, True, "bf16", "bf16"), (576, 64, False, "f16", "f32"),
+    (160, 32, True, "f16", "f32"), (352, 32, False, "bf16", "f16"), (32, 32, True, "bf16", "f32")])
+def test_w4_forms(rows, E, N, K, G, zeros, x_dt, o_dt):
+    _say("form", rows, E, N, K, G, zeros, x_dt, o_dt)
+    g = torch.Generator().manual_seed(rows + K)
+    W, host = _weight(E, N, K, G, zeros, "bf16" if zeros else "f16", g)
+    off = _spread(rows, E, g)
+    x = _wide(torch.randn(rows + 5, K, generator=g), 8, DT[x_dt])
+    out = torch.full((rows + 5, N + 8), MARK, dtype=DT[o_dt], device=DEV)
+    exl3.exl3_w4_linear(x, W, off.to(DEV), out=out[:, :N])
+    w, xn, o = ow4.weights(*host), _np(x), off.numpy()
+    ref = ow4.linear(xn, w, o, np.full((rows + 5, N), MARK))
+    mag = ow4.linear(np.abs(xn), np.abs(w), o)
+    _within(_np(out[:, :N]), ref, DT[o_dt], (2 * K + K // G) * U, mag)
+    assert (out[:, N:] == MARK).all() and (out[rows:] == MARK).all()
+
+
+@pytest.mark.parametrize("rows,E,N", FORMS[:6])
+@pytest.mark.parametrize("K,G,x_dt", [(384, 128, "f16"), (320, 64, "bf16"), (352, 32, "f16")])
+def test_w4_forms_give_the_same_bytes(rows, E, N, K, G, x_dt):
+    """Rows of a few experts of a large call, alone: another form, the same bytes.
+    Rows that hold infinities and NaN leave the others as they are."""
+    g = torch.Generator().manual_seed(rows + G)
+    W, _ = _weight(E, N, K, G, True, "f16", g)
+    off = _spread(rows, E, g)
+    x = torch.randn(rows, K, generator=g).to(DT[x_dt]).to(DEV)
+    f32 = torch.float32
+    full = exl3.exl3_w4_linear(x, W, off.to(DEV), f32)
+    for lo, hi in ((0, 1), (int(off[1]) - 3, int(off[1]) + 20), (rows // 2, rows // 2 + 200),
+                   (rows - 40, rows)):
+        lo, hi = max(lo, 0), min(hi, rows)
+        part = exl3.exl3_w4_linear(x[lo:hi], W, (off - lo).clamp(0, hi - lo).to(DEV), f32)
+        assert _same(part, full[lo:hi]), (lo, hi)
+    x[1, K - 1], x[rows // 2, 0] = float("nan"), float("inf")
+    got = exl3.exl3_w4_linear(x, W, off.to(DEV), f32)
+    rest = [r for r in range(rows) if r not in (1, rows // 2)]
+    assert _same(got[rest], full[rest])
+    assert got[1].isnan().all() and not got[rows // 2].isfinite().any()
+
+
 @pytest.mark.parametrize("x_dt,G,zeros,K", [("f16", 128, False, 1664), ("bf16", 32, True, 1184),
                                             ("f16", 64, True, 1088), ("bf16", 128, True, 2176)])
 def test_w4_rows_are_independent_of_their_company(x_dt, G, zeros, K):
@@ -444,6 +534,20 @@ def test_w4_rows_at_a_large_distance():
     fx[:, :K] = x
     fo = torch.empty(rows, ld, dtype=torch.float16, device=DEV)
     assert _same(exl3.exl3_w4_linear(fx[:, :K], W, out=fo[:, :N]), want)
+
+
+def test_w4_rows_farther_apart_than_tiles_take():
+    """Row distances from 2^23 on leave the 32-bit offsets within a tile."""
+    g = torch.Generator().manual_seed(9)
+    rows, K, N = 40, 192, 4104
+    W, _ = _weight(1, N, K, 64, True, "f16", g)
+    x = torch.randn(rows, K, generator=g).half().to(DEV)
+    want = exl3.exl3_w4_linear(x, W)
+    for ld in ((1 << 23) - 8, 1 << 23):
+        far = torch.empty(rows, ld, dtype=torch.float16, device=DEV)
+        far[:, :K] = x
+        assert _same(exl3.exl3_w4_linear(far[:, :K], W), want), ld
+        del far
 
 
 # ------------------------------------------------- streams, graphs, devices

@@ -658,6 +658,7 @@ class DeviceW4:
     8) belong to groups of 32, 64 or 128 inputs: weight = scale * (q - zero).
     Outputs are a multiple of 8. The tensors given are not kept."""
 
+    @torch.no_grad()
     def __init__(self, q, scale, zero=None):
         if q.dim() == 2:
             q, scale = q[None], scale[None]
@@ -688,6 +689,8 @@ class DeviceW4:
         def padded(t, cols):  # outputs and columns that the tiles have and t lacks: 0
             return torch.nn.functional.pad(t, (0, cols - t.shape[2], 0, 16 * NT - N))
 
+        if q.storage_offset() % 4:
+            q = q.clone()  # read as words
         step = max(1, (1 << 27) // (N * K))  # experts at a time: little extra memory
         for e in range(0, E, step):
             w = q[e:e + step].contiguous().view(torch.int32)  # inputs 0 .. 7 from bit 0 on
