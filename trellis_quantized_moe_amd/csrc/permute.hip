@@ -7,7 +7,10 @@
 // move. Work is cut by row t, so that the side that has one row per token (x,
 // out, dout) is moved once, and its topk packed rows are whole rows wherever
 // they stand. A lane moves 16 bytes (8 values) at a time; a row takes the lanes
-// it fills (up to 256), so short rows share a wave.
+// it fills (up to 256), so short rows share a wave. Measured (a large copy: 5.15
+// TB/s): 8192 rows of 6144 to 8 places each in bf16, 816 MB, 157 us; 4001 rows
+// summed from 8 in fp32, 757 MB, 146; gradients of 8192 rows of 6144 with 4
+// choices in fp16, 1007 MB, 206. One row: 3 us, an empty launch 2.5.
 #include "common.hpp"
 #include "kernels.hpp"
 
@@ -115,7 +118,8 @@ __global__ void __launch_bounds__(kThreads) permute_kernel(MoveParams p) {
   }
 }
 
-// DY: type of y, DO: of out. B choices at once.
+// DY: type of y, DO: of out. B choices at once: their loads are all in flight
+// before the first is added (one after the other, 8 choices wait 8 times).
 template <int DY, int DO, int B, bool STREAM>
 __global__ void __launch_bounds__(kThreads) unpermute_kernel(MoveParams p) {
   constexpr int SY = DY == 3 ? 4 : 2, SO = DO == 3 ? 4 : 2;
@@ -145,7 +149,9 @@ __global__ void __launch_bounds__(kThreads) unpermute_kernel(MoveParams p) {
 }
 
 // DY: type of y and dy, DO: of dout. WITH_DW: y is read and dw written. A
-// block's lanes cover a whole row, so that <dout, y> needs no second launch.
+// block's lanes cover a whole row, so that <dout, y> needs no second launch; the
+// 8 sums of a batch cross the wave together (one after the other, 2 rows of 13
+// choices took 13 us instead of 9).
 template <int DY, int DO, bool WITH_DW, bool STREAM>
 __global__ void __launch_bounds__(kThreads) unpermute_backward_kernel(MoveParams p) {
   constexpr int SY = DY == 3 ? 4 : 2, SO = DO == 3 ? 4 : 2;
