@@ -809,12 +809,17 @@ hipError_t mid(const W4Params &p, hipStream_t st) {
 // The form is chosen by how many rows an expert has (its tile should not stay
 // half empty) and how many tiles there are for 256 CUs. us of the forms on either
 // side of a border, fp16, groups of 128:
-//   4096 -> 4096, one projection:      rows 2048: wide 98, <4, 2, 2, 8> 81; 4096: 140, 162
-//     rows 1024: <4, 2, 2, 8> 51, <2, 2, 3, 4> 62; rows 512: 48, 36; <2, 1, 3, 4> 36
-//     rows 256: <2, 2, 3, 4> 28, <2, 1, 3, 4> 23; rows 64: <2, 1, 3, 4> 19, <1, 1, 3, 4> 16
-//     rows 64: <1, 1, 3, 4> 16, split 22; rows 16: 15, 8
-//   128 experts, top-8, 4096 -> 1536:  2048 rows: wide 314, <4, 2, 2, 8> 324; 1024: 224, 217
-//     rows 512: <4, 2, 2, 8> 138, <2, 2, 3, 4> 153; rows 128: 95, <1, 2, 3, 4> 79
+//   4096 -> 4096, one projection:
+//     rows 4096: wide 122, <4, 2, 2, 8> 154; rows 2048: 83, 78
+//     rows 1024: <4, 2, 2, 8> 52, <2, 2, 3, 4> 57; rows 512: 48, 33
+//     rows 512: <2, 2, 3, 4> 33, <2, 1, 3, 4> 36; rows 256: 25, 23
+//     rows 128: <2, 1, 3, 4> 18, <1, 1, 3, 4> 19; rows 64: 18, 15
+//     rows 64: <1, 1, 3, 4> 15, split 22; rows 32: 15, 14
+//   128 experts, top-8, 4096 -> 1536:
+//     tokens 2048: wide 286, <4, 2, 2, 8> 318; tokens 1024: 197, 205; tokens 512: 139, 128
+//     tokens 512: <4, 2, 2, 8> 128, <2, 2, 3, 4> 123; tokens 1024: 205, 224
+//     tokens 256: <2, 2, 3, 4> 89, <1, 2, 3, 4> 102; tokens 128: 88, 80
+//     tokens 16: <1, 2, 3, 4> 52, <1, 1, 3, 4> 58; tokens 2: 20, 20, split 20
 hipError_t launch_w4(const W4Params &p, hipStream_t st) {
   // what the rows make when they spread evenly over the experts
   const int64_t experts = p.offset ? (p.E < p.rows ? p.E : p.rows) : 1;
