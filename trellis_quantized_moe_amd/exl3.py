@@ -558,7 +558,9 @@ def _pos(meta, rows, topk):
     """Address of the packed positions of rows * topk choices."""
     if topk < 1 or rows * topk > _MAX:
         _refuse("%d choices of %d rows are out of range", topk, rows)
-    return _vector(meta["pos_of_pair"], rows * topk, torch.int32, "pos_of_pair")
+    pos = meta["pos_of_pair"]
+    # alloc_meta's buffers have one element where a batch has none
+    return _vector(pos, rows * topk or min(pos.numel(), 1), torch.int32, "pos_of_pair")
 
 
 def _packed(t, topk, name):
