@@ -133,15 +133,25 @@ __global__ void __launch_bounds__(kThreads) unpermute_kernel(MoveParams p) {
       int q[B];
       float w[B];
       load_choices(p, t, j0, q, w);
+      int some = -1;  // a row that may be read
+      uint32_t taken = 0;  // bit i: choice i takes part (keeping q: 7 registers more)
 #pragma unroll
-      for (int i = 0; i < B; ++i)  // a dropped choice reads row 0 and is not added
-        raw[i] = load_eight<DY>((const char *)p.x + (max(q[i], 0) * p.ldx + 8 * u) * SY);
+      for (int i = 0; i < B; ++i) {
+        taken |= (uint32_t)(q[i] >= 0) << i;
+        some = max(some, q[i]);
+      }
+      if (some < 0) continue;
+#pragma unroll
+      for (int i = 0; i < B; ++i) {  // a dropped choice reads another's row and is not added
+        const int row = q[i] >= 0 ? q[i] : some;
+        raw[i] = load_eight<DY>((const char *)p.x + (row * p.ldx + 8 * u) * SY);
+      }
 #pragma unroll
       for (int i = 0; i < B; ++i) {
         float y[8];
         unpack<DY>(raw[i], y);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) acc[k] = q[i] >= 0 ? fmaf(w[i], y[k], acc[k]) : acc[k];
+        for (int k = 0; k < 8; ++k) acc[k] = taken >> i & 1 ? fmaf(w[i], y[k], acc[k]) : acc[k];
       }
     }
     store_eight<DO, STREAM>((char *)p.out + (t * p.ldout + 8 * u) * SO, acc);
