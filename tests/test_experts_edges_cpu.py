@@ -143,3 +143,20 @@ def test_unpermute_reads_the_rows_of_choices_alone(tmp_path):
     assert r.returncode == 0, r.stderr[-2000:]
     r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=60)
     assert r.returncode == 0 and r.stdout == "all read\n", (r.returncode, r.stdout)
+
+
+# ------------------------------------------------------- weights laid out
+def test_experts_an_odd_number_of_bytes_apart():
+    """Every expert's weights are read as words, wherever they start; also where
+    a step of the layout holds one expert."""
+    g = torch.Generator().manual_seed(1)
+    E, N, K = 2, 2056, 32768  # a step holds at most 2^27 weights: one expert
+    q = torch.randint(0, 256, (E, N * K // 2), generator=g, dtype=torch.uint8)
+    s = torch.rand(E, N, K // 128, generator=g).half()
+    want = exl3.DeviceW4(q.view(E, N, K // 2), s).q
+    for first, more in ((0, 1), (0, 2), (1, 3), (2, 5)):
+        far = torch.zeros(first + E * (N * K // 2 + more), dtype=torch.uint8)
+        apart = far[first:].view(E, -1)[:, :N * K // 2]
+        apart.copy_(q)
+        got = exl3.DeviceW4(apart.view(E, N, K // 2), s).q
+        assert torch.equal(got, want), (first, more)

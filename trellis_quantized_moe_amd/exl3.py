@@ -691,11 +691,12 @@ class DeviceW4:
         def padded(t, cols):  # outputs and columns that the tiles have and t lacks: 0
             return torch.nn.functional.pad(t, (0, cols - t.shape[2], 0, 16 * NT - N))
 
-        if q.storage_offset() % 4:
-            q = q.clone()  # read as words
         step = max(1, (1 << 27) // (N * K))  # experts at a time: little extra memory
         for e in range(0, E, step):
-            w = q[e:e + step].contiguous().view(torch.int32)  # inputs 0 .. 7 from bit 0 on
+            w = q[e:e + step].reshape(-1)
+            if w.storage_offset() % 4:
+                w = w.clone()
+            w = w.view(torch.int32).view(-1, N, K // 8)  # inputs 0 .. 7 from bit 0 on
             even, odd = w & 0x0f0f0f0f, (w >> 4) & 0x0f0f0f0f
             for sh, mask in ((4, 0x00ff00ff), (8, 0x0000ffff)):
                 even, odd = (even | even >> sh) & mask, (odd | odd >> sh) & mask
