@@ -160,3 +160,14 @@ def test_experts_an_odd_number_of_bytes_apart():
         apart.copy_(q)
         got = exl3.DeviceW4(apart.view(E, N, K // 2), s).q
         assert torch.equal(got, want), (first, more)
+
+
+@pytest.mark.parametrize("E,N,K", [(1, 4, 64), (2, 12, 64), (1, 65544, 32), (1, 8, 65568),
+                                   (1025, 8, 32), ((1 << 32) + 1, 8, 32)])
+def test_weights_that_no_product_takes_are_refused_at_once(E, N, K):
+    """Outputs that are no multiple of 8 and sizes past the limits: at the
+    layout, not at the first product."""
+    q = torch.zeros(1, 1, K // 2, dtype=torch.uint8).expand(E, N, K // 2)
+    s = torch.ones(1, 1, 1).half().expand(E, N, K // 32)
+    with pytest.raises(exl3.Exl3Error, match="status -[37]|out of range"):
+        exl3.DeviceW4(q, s)

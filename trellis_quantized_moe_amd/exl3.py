@@ -658,7 +658,8 @@ class DeviceW4:
     byte, the even input in the lower four bits; ``scale`` fp16 or bf16
     [experts, out, in / group] and ``zero`` (uint8 of 0..15, the same shape; None:
     8) belong to groups of 32, 64 or 128 inputs: weight = scale * (q - zero).
-    Outputs are a multiple of 8. The tensors given are not kept."""
+    Outputs are a multiple of 8, inputs and outputs at most 65536, experts at
+    most 1024. The tensors given are not kept."""
 
     @torch.no_grad()
     def __init__(self, q, scale, zero=None):
@@ -681,6 +682,12 @@ class DeviceW4:
                         list(zero.shape), zero.dtype)
             if int(zero.max()) > 15:
                 _refuse("zero has values above 15")
+        if max(E, N, K) > _MAX:
+            _too_large(E, N, K)
+        # the limits of the products: a call without rows checks no more
+        none = W4C(K, N, E, group, None, None, None, _dt(scale))
+        _check(lib().exl3_w4_linear(ctypes.byref(none), None, F16, K, 0, None, None, F16, N, None,
+                                    None))
         self.in_features, self.out_features = K, N
         self.num_experts, self.group_size = E, group
         NT, KT, NG = (N + 15) // 16, (K + 127) // 128, 128 // group
