@@ -508,9 +508,13 @@ int32_t exl3_unpermute_backward(const void *dout, int32_t dout_dtype, int64_t ld
  * packed rows with their experts' weights (expert_offset [num_experts + 1] as
  * exl3_route_pack writes it), or of all rows with one projection's
  * (num_experts 1, expert_offset NULL):
- *   out[p][n] = sum over k of x[p][k] scale[e][n][k / G] (q[e][n][k] - zero[e][n][k / G])
+ *   out[p][n] = sum over groups g of G inputs of scale[e][n][g] t_g
+ *   t_g       = sum over k in g of x[p][k] (q[e][n][k] - zero[e][n][g])
  * for expert_offset[e] <= p < expert_offset[e + 1]. The weights enter the sums
  * as the whole numbers q - zero and the scales in fp32: no weight is rounded.
+ * t_g is formed first, in fp32: it is finite where |x| < 2^117 (every fp16
+ * value), whatever the scale, and may overflow past that. A scale that is
+ * infinite or NaN multiplies t_g, not its terms.
  * Rows outside every expert's range are not written; offsets are clamped to
  * [0, rows], and ranges that overlap or descend leave rows unwritten or
  * written by either expert. A row's bytes do not depend on the other rows,

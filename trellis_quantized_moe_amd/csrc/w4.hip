@@ -5,7 +5,7 @@
 // q - z is a whole number of at most 15 in size, exact in fp16 and bf16, so the
 // weights enter the MFMA as they are and t_g is a sum of exact products in fp32;
 // the scale is applied to t_g in fp32: out = fma(s_g, t_g, out), g ascending.
-// No weight is rounded.
+// No weight is rounded. |t_g| <= 15 * 128 |x|: finite for |x| below 2^117.
 //
 // A row's bytes depend on that row and its expert's weights alone: every form
 // sums a group by the same chain of v_mfma_f32_16x16x32 (32 inputs each,

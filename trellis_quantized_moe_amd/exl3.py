@@ -728,8 +728,9 @@ def exl3_w4_linear(x, weight, expert_offset=None, out_dtype=None, out=None):
     "expert_offset", or all rows with a single projection's. x is fp16 or bf16;
     x and ``out`` [rows, out] may be column slices of wider tensors. Without
     ``out`` the result has ``out_dtype``, by default that of x; rows past the
-    last expert's keep what ``out`` held (without ``out``: anything). The
-    result is not part of autograd's graph."""
+    last expert's keep what ``out`` held (without ``out``: anything). A group's
+    sum is formed before its scale, in fp32: bf16 x from 2^117 on may overflow
+    it. The result is not part of autograd's graph."""
     if x.dim() != 2:
         _refuse("x must be [rows, in], got %s", list(x.shape))
     rows, N = x.shape[0], weight.out_features
