@@ -9,7 +9,7 @@
 // they stand. A lane moves 16 bytes (8 values) at a time; a row takes the lanes
 // it fills (up to 256), so short rows share a wave. Measured (a large copy: 5.15
 // TB/s): 8192 rows of 6144 to 8 places each in bf16, 816 MB, 157 us; 4001 rows
-// summed from 8 in fp32, 757 MB, 146; gradients of 8192 rows of 6144 with 4
+// summed from 8 in fp32, 757 MB, 148; gradients of 8192 rows of 6144 with 4
 // choices in fp16, 1007 MB, 206. One row: 3 us, an empty launch 2.5.
 #include "common.hpp"
 #include "kernels.hpp"
@@ -48,7 +48,7 @@ __device__ __forceinline__ void unpack(const Eight<DT> &e, float (&f)[8]) {
 }
 // Results that the L2s cannot hold go past them (stream): 8 x 4 MB. us of one and
 // the other: 5284 rows x 13 x 2048 carried in bf16 (281 MB) 51 and 57, 4001 rows
-// of 6144 summed from 8 in fp32 146 and 152; at 5 MB no difference.
+// of 6144 summed from 8 in fp32 149 and 153; at 5 MB no difference.
 template <bool STREAM>
 __device__ __forceinline__ void store16(void *p, u32x4 v) {
   if constexpr (STREAM) __builtin_nontemporal_store(v, (u32x4 *)p);

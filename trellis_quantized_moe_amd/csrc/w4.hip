@@ -39,7 +39,7 @@ __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
 }
 
 // Eight weights q - z of a word as the MFMA's operand.
-// fp16: 0x6400 | q is 1024 + q, 0x6400 | 16 q is 1024 + 16 q: 1024 + z (64 + z
+// fp16, a well-known way: 0x6400 | q is 1024 + q, 0x6400 | 16 q is 1024 + 16 q: 1024 + z (64 + z
 // after a sixteenth) is taken off again, exactly; nine instructions.
 // bf16 has no packed subtraction: four q - z at a time as signed bytes (128 + q
 // - z borrows from no neighbour), each through fp32, whose upper half is the
@@ -629,7 +629,10 @@ __global__ void __launch_bounds__(256, 2) w4_wide_kernel(W4Params p) {
 // counted and the wait leaves the later steps' in flight, so nothing else in the
 // loop may load from or store to global memory. Three steps: a fourth costs
 // a workgroup to a CU (bf16, groups of 32, 61 rows x top-8 of 192 experts: 349 us
-// instead of 313). Few rows are bound by memory: the same in fp16 266 us, 5.0 TB/s.
+// instead of 313). Few rows are bound by memory: the same in fp16 263 to 299 us (4.5
+// to 5.1 TB/s). One projection of few rows is bound by the latency of a step
+// (0.55 us) times their number, whatever the rows of a tile: 64 rows of 4096 -> 4096,
+// where a CU has one workgroup, 15 us at a floor of 1.9.
 template <int G, int MT, int J, int S, int W>
 struct MidLds {
   static constexpr int NG = kTileK / G;
@@ -820,6 +823,9 @@ hipError_t mid(const W4Params &p, hipStream_t st) {
 //     tokens 512: <4, 2, 2, 8> 128, <2, 2, 3, 4> 123; tokens 1024: 205, 224
 //     tokens 256: <2, 2, 3, 4> 89, <1, 2, 3, 4> 102; tokens 128: 88, 80
 //     tokens 16: <1, 2, 3, 4> 52, <1, 1, 3, 4> 58; tokens 2: 20, 20, split 20
+//   16 experts, top-4, 2048 -> 1536, tokens 256: <2, 1, 3, 4> 21.1, <2, 2, 3, 4> 19.5
+// At three of these points the rule takes the slower form: 512 and 1024 tokens of
+// 128 experts (<4, 2, 2, 8>, by 4% each) and the last (by 8%).
 hipError_t launch_w4(const W4Params &p, hipStream_t st) {
   // what the rows make when they spread evenly over the experts
   const int64_t experts = p.offset ? (p.E < p.rows ? p.E : p.rows) : 1;
